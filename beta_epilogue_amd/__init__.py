@@ -3,7 +3,9 @@
 Argument marshalling only: every step of the computation runs in the HIP
 kernels of the shared library.  The C entry points keep their names
 (``gemm_epi_create``, ``gemm_epi_run``, ...); ``FusedGemm`` adds the
-torch-tensor convenience layer (pointers and the current HIP stream).
+torch-tensor convenience layer (pointers and the current HIP stream).  The
+linear layer and the norm (``FusedLinear``, ``FusedLinearGrad``, ``RmsNorm``,
+``RmsNormGrad``, ``FusedNormLinear``) are in ``layers``.
 
 The library must have been built (``python -m beta_epilogue_amd.build`` or
 ``__graft_entry__.build()``); importing the binding without it raises.
@@ -232,3 +234,16 @@ class FusedGemm:
             self.close()
         except Exception:
             pass
+
+
+# The linear layer and the norm (module layers, which imports torch) are
+# loaded when first asked for.
+_LAYERS = ("ACTIVATIONS", "FusedLinear", "FusedLinearGrad", "FusedNormLinear", "RmsNorm", "RmsNormGrad",
+           "linear_variant_names")
+
+
+def __getattr__(name):
+    if name in _LAYERS:
+        from . import layers
+        return getattr(layers, name)
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))

@@ -3,7 +3,9 @@
 libgemm_epi.so is linked from gemm_epi.hip (C ABI, variant table) and
 GEMM_EPI_PARTS objects of gemm_epi_part.hip, each compiling the kernel
 variants of gemm_epi_variants.inc assigned to it; the parts compile in
-parallel.  libmfma_ceiling.so is a measurement tool for bench.py.
+parallel.  The linear layer (gemm_linear*.hip, its tile kernels in
+GEMM_LINEAR_PARTS parts) and the norm (gemm_norm*.hip) are linked in.
+libmfma_ceiling.so is a measurement tool for bench.py.
 """
 from __future__ import annotations
 
@@ -22,11 +24,20 @@ SPLITK_SOURCE = os.path.join(CSRC, "gemm_epi_splitk.hip")
 PREP_SOURCE = os.path.join(CSRC, "gemm_epi_prep.hip")
 PART_SOURCE = os.path.join(CSRC, "gemm_epi_part.hip")
 GEMM_EPI_PARTS = 16
-SOURCES = [MAIN_SOURCE, PART_SOURCE, SPLITK_SOURCE, PREP_SOURCE]
+LINEAR_PART_SOURCE = os.path.join(CSRC, "gemm_linear_part.hip")
+GEMM_LINEAR_PARTS = 8
+LINEAR_SOURCES = [os.path.join(CSRC, f) for f in ("gemm_linear.hip", "gemm_linear_rows.hip", "gemm_linear_grad.hip",
+                                                  "gemm_norm.hip", "gemm_norm_kernels.hip")]
+SOURCES = [MAIN_SOURCE, PART_SOURCE, SPLITK_SOURCE, PREP_SOURCE, LINEAR_PART_SOURCE] + LINEAR_SOURCES
 HEADERS = [os.path.join(CSRC, "gemm_epi_kernel.hpp"), os.path.join(CSRC, "gemm_epi_launch.hpp"),
            os.path.join(CSRC, "gemm_epi_splitk.hpp"), os.path.join(CSRC, "gemm_epi_prep.hpp"),
            os.path.join(CSRC, "gemm_epi_raster.hpp"), os.path.join(CSRC, "gemm_epi_variants.inc"),
-           os.path.join(ROOT, "include", "gemm_epi.h")]
+           os.path.join(CSRC, "gemm_epi_host.hpp"), os.path.join(CSRC, "gemm_epi_plan.hpp"),
+           os.path.join(CSRC, "linear_act.hpp"), os.path.join(CSRC, "gemm_linear_epilogue.hpp"),
+           os.path.join(CSRC, "gemm_linear.hpp"), os.path.join(CSRC, "gemm_linear_variants.inc"),
+           os.path.join(CSRC, "gemm_norm.hpp"),
+           os.path.join(ROOT, "include", "gemm_epi.h"), os.path.join(ROOT, "include", "gemm_epi_linear.h"),
+           os.path.join(ROOT, "include", "gemm_epi_norm.h")]
 # measurement tool used by bench.py --mfma-ceiling (not part of the GEMM path)
 CEILING_LIB = os.path.join(HERE, "libmfma_ceiling.so")
 CEILING_SOURCE = os.path.join(CSRC, "mfma_ceiling.hip")
@@ -114,6 +125,11 @@ def build(verbose: bool = False, extra=(), only=None, cache_dir=None) -> str:
                   obj("splitk.o", SPLITK_SOURCE, [os.path.join(CSRC, "gemm_epi_splitk.hpp"),
                                                   os.path.join(CSRC, "gemm_epi_raster.hpp")]),
                   obj("prep.o", PREP_SOURCE, [os.path.join(CSRC, "gemm_epi_prep.hpp")])]
+        linear_deps = kernel_deps + [os.path.join(CSRC, f) for f in ("gemm_linear.hpp", "gemm_linear_variants.inc",
+                                                                      "linear_act.hpp", "gemm_linear_epilogue.hpp")]
+        units += [obj("linear%d.o" % k, LINEAR_PART_SOURCE, linear_deps, ["-DGEMM_LINEAR_PART=%d" % k])
+                  for k in range(GEMM_LINEAR_PARTS)]
+        units += [obj(os.path.basename(f) + ".o", f, HEADERS) for f in LINEAR_SOURCES]
         jobs = [cmd for _, cmd in units if cmd]
         ceil_tmp = CEILING_LIB + ".tmp%d" % os.getpid()
         jobs.append(["hipcc"] + HIPCC_FLAGS + INCLUDES + ["-shared", "-o", ceil_tmp, CEILING_SOURCE])

@@ -20,16 +20,17 @@
 #include <new>
 
 #include "gemm_epi.h"
+#include "gemm_epi_host.hpp"
 #include "gemm_epi_kernel.hpp"
+#include "gemm_epi_plan.hpp"
 #include "gemm_epi_launch.hpp"
 #include "gemm_epi_splitk.hpp"
 #include "gemm_epi_prep.hpp"
 
-namespace {
+namespace gemm_epi {
 
-thread_local char g_last_error[256] = "";
+static thread_local char g_last_error[256] = "";
 
-int fail(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 int fail(int code, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -37,6 +38,12 @@ int fail(int code, const char* fmt, ...) {
   va_end(ap);
   return code;
 }
+
+void clear_error() { g_last_error[0] = 0; }
+
+}  // namespace gemm_epi
+
+namespace {
 
 using gemm_epi::Params;
 typedef void (*launch_fn)(const Params&, int grid, hipStream_t s);
@@ -83,6 +90,10 @@ const Variant kVariants[] = {
 #undef VD
 constexpr int kNumVariants = (int)(sizeof kVariants / sizeof kVariants[0]);
 
+}  // namespace
+
+namespace gemm_epi {
+
 int elem_bytes(int t) {
   switch (t) {
     case GEMM_EPI_F16:
@@ -106,7 +117,42 @@ bool mul_ok(int64_t a, int64_t b, int64_t* out) {
   return true;
 }
 
-}  // namespace
+int device_query(int* device, int* cus) {
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return fail(GEMM_EPI_ERR_DEVICE, "hipGetDevice failed");
+  hipDeviceProp_t prop;
+  if (hipGetDeviceProperties(&prop, dev) != hipSuccess)
+    return fail(GEMM_EPI_ERR_DEVICE, "hipGetDeviceProperties failed");
+  if (std::strncmp(prop.gcnArchName, "gfx950", 6) != 0)
+    return fail(GEMM_EPI_ERR_DEVICE, "device %d is %s, this library is built for gfx950", dev,
+                prop.gcnArchName);
+  *device = dev;
+  *cus = prop.multiProcessorCount;
+  return GEMM_EPI_OK;
+}
+
+int check_device(int device) {
+  int dev = -1;
+  if (hipGetDevice(&dev) != hipSuccess || dev != device)
+    return fail(GEMM_EPI_ERR_DEVICE, "current device %d is not the handle's device %d", dev, device);
+  return GEMM_EPI_OK;
+}
+
+int check_workspace(const void* ws, int64_t have, int64_t need) {
+  if (need == 0) return GEMM_EPI_OK;
+  if (!ws || have < need)
+    return fail(GEMM_EPI_ERR_INVALID_ARG, "workspace of %lld bytes needed (%lld given)", (long long)need,
+                ws ? (long long)have : 0LL);
+  if ((uintptr_t)ws & 255u) return fail(GEMM_EPI_ERR_ALIGNMENT, "workspace is not 256-byte aligned");
+  return GEMM_EPI_OK;
+}
+
+int launched() {
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? GEMM_EPI_OK : fail(GEMM_EPI_ERR_LAUNCH, "launch failed: %s", hipGetErrorString(e));
+}
+
+}  // namespace gemm_epi
 
 // The uint8 workspace: sums of A rows (L*M int32) and of B columns (L*N),
 // then the flipped copies of A (L*M*K bytes) and B (L*N*K), each part at a
@@ -272,62 +318,21 @@ static bool variant_fits(const Variant& v, const gemm_epi_desc* d) {
   return v.ab == (widened(d) ? gemm_epi::T_F16 : exact_ab(d));
 }
 
-// Plan cost model (measured on MI355X, fp16 with C, X, D, Y; times in us).
-// A K tile of one output tile takes 1.1 us with 256x256 tiles; with the
-// smaller tiles their share of the work at a lower per-CU rate (192x256:
-// 0.75 at 0.9, 128x256: 0.5 at 0.67, 128x128: 0.25 at ~0.46).  The split-K
-// reduction costs 4 us plus its bytes (S partial-sum slots and C, X, D, Y
-// per split tile) at 5 TB/s.
-static double ktile_us(const Variant& v) {
-  if (v.bm == 256 && v.bn == 256) return 1.1;
-  if (v.bm == 192 && v.bn == 256) return 1.1 * 0.75 / 0.9;
-  if (v.bm == 128 && v.bn == 256) return 1.1 * 0.75;
-  return 0.6;
+// The cost model's view of a problem (gemm_epi_plan.hpp).
+static PlanProblem plan_problem(const gemm_epi_desc* d) {
+  double bytes = 0.0;
+  for (int t : {d->c_dtype, d->x_dtype, d->d_dtype, d->y_dtype})
+    if (t != GEMM_EPI_NONE) bytes += elem_bytes(t);
+  return PlanProblem{d->M, d->N, d->K, d->L, bytes, d->ab_dtype != GEMM_EPI_U8};
 }
 
-struct SplitChoice {
-  int64_t splits, tail;  // K slices of the split tiles (1: none), split tiles
-  double us;             // modelled time of the launch
-};
-
-// The library's split choice for variant v and the modelled time: when the
-// last round of tiles (tiles % cus, all of them with fewer tiles than CUs)
-// would leave at least half of the CUs idle, those tiles may run in S K
-// slices after whole-K rounds of the others; S (2 .. min(cus / last,
-// K tiles / 4, 16)) maximises the time saved in the last round,
-// (K tiles - ceil(K tiles / S)) K-tile times, less the reduction's cost; no S
-// with a positive balance, no split.
 static SplitChoice split_choice(const Variant& v, const gemm_epi_desc* d, int64_t cus) {
-  const int64_t tiles = ((d->M + v.bm - 1) / v.bm) * ((d->N + v.bn - 1) / v.bn) * d->L;
-  const int64_t ktiles = (d->K + v.bk - 1) / v.bk;
-  const double tk = ktile_us(v);
-  const int64_t last = tiles % cus;
-  SplitChoice c{1, 0, (double)((tiles + cus - 1) / cus) * ktiles * tk};
-  if (last == 0 || last * 2 > cus || d->ab_dtype == GEMM_EPI_U8) return c;
-  const double slot_bytes = 4.0 * v.bm * v.bn;
-  double epi_bytes = 0.0;
-  for (int t : {d->c_dtype, d->x_dtype, d->d_dtype, d->y_dtype})
-    if (t != GEMM_EPI_NONE) epi_bytes += (double)elem_bytes(t) * v.bm * v.bn;
-  const int64_t smax = std::min<int64_t>(std::min<int64_t>(cus / last, ktiles / 4), 16);
-  double best = 0.0;
-  for (int64_t s = 2; s <= smax; ++s) {
-    const double saved_us = (double)(ktiles - (ktiles + s - 1) / s) * tk;
-    const double cost_us = 4.0 + (double)last * (s * slot_bytes + epi_bytes) / 5.0e6;
-    if (saved_us - cost_us > best) {
-      best = saved_us - cost_us;
-      c.splits = s;
-    }
-  }
-  if (c.splits > 1) {
-    c.tail = last;
-    c.us -= best;
-  }
-  return c;
+  return split_choice(v.bm, v.bn, v.bk, plan_problem(d), cus);
 }
 
 extern "C" int gemm_epi_create_variant(const gemm_epi_desc* desc, int variant,
                                        gemm_epi_handle** out) {
-  g_last_error[0] = 0;
+  clear_error();
   if (!out) return fail(GEMM_EPI_ERR_INVALID_ARG, "out is NULL");
   *out = nullptr;
   int rc = validate_desc(desc);
@@ -372,14 +377,9 @@ extern "C" int gemm_epi_create_variant(const gemm_epi_desc* desc, int variant,
     return fail(GEMM_EPI_ERR_UNSUPPORTED, "uint8 needs M and N below 2^29");
 
   // Device query (the only part that needs a GPU).
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return fail(GEMM_EPI_ERR_DEVICE, "hipGetDevice failed");
-  hipDeviceProp_t prop;
-  if (hipGetDeviceProperties(&prop, dev) != hipSuccess)
-    return fail(GEMM_EPI_ERR_DEVICE, "hipGetDeviceProperties failed");
-  if (std::strncmp(prop.gcnArchName, "gfx950", 6) != 0)
-    return fail(GEMM_EPI_ERR_DEVICE, "device %d is %s, this library is built for gfx950", dev,
-                prop.gcnArchName);
+  int dev = 0, cus = 0;
+  rc = device_query(&dev, &cus);
+  if (rc) return rc;
 
   // Tile shape (the library's choice, where the layout has the smaller
   // kernels: K-major A and B, N-major C/D).  128x128 tiles when the
@@ -397,7 +397,6 @@ extern "C" int gemm_epi_create_variant(const gemm_epi_desc* desc, int variant,
     return -1;
   };
   if (auto_variant && desc->splits == 0) {
-    const int64_t cus = prop.multiProcessorCount;
     const int64_t tiles_default =
         ((desc->M + vp->bm - 1) / vp->bm) * ((desc->N + vp->bn - 1) / vp->bn) * desc->L;
     const int small = find_tile(128, 128);
@@ -423,7 +422,7 @@ extern "C" int gemm_epi_create_variant(const gemm_epi_desc* desc, int variant,
   h->desc = *desc;
   h->variant = variant;
   h->device = dev;
-  h->cus = prop.multiProcessorCount;
+  h->cus = cus;
   h->tiles_m = (desc->M + v.bm - 1) / v.bm;
   h->tiles_n = (desc->N + v.bn - 1) / v.bn;
   h->tiles = h->tiles_m * h->tiles_n * desc->L;
@@ -491,11 +490,12 @@ static bool integral_24(float v) {
   return std::isfinite(v) && std::nearbyint(v) == v && std::fabs(v) <= 16777216.0f;
 }
 
-// One fused GEMM; split-K plans use the handle's workspace (allocated here on
-// first use) or, with use_static, the static scratch array.
+// One fused GEMM; plans with a workspace use ext_ws if given, else the handle's
+// own (allocated here on first use) or, with use_static, the static scratch array.
 static int run_impl(const gemm_epi_handle* hc, const void* A, const void* B, const void* C, const void* X,
-                    void* D, void* Y, float alpha, float beta, float x_factor, void* stream, bool use_static) {
-  g_last_error[0] = 0;
+                    void* D, void* Y, float alpha, float beta, float x_factor, void* stream, bool use_static,
+                    void* ext_ws = nullptr) {
+  clear_error();
   if (!hc) return fail(GEMM_EPI_ERR_INVALID_ARG, "handle is NULL");
   gemm_epi_handle* h = const_cast<gemm_epi_handle*>(hc);  // only the lazily allocated workspace changes
   const gemm_epi_desc& d = h->desc;
@@ -519,10 +519,8 @@ static int run_impl(const gemm_epi_handle* hc, const void* A, const void* B, con
   if (int_path && !(integral_24(alpha) && integral_24(beta) && integral_24(x_factor)))
     return fail(GEMM_EPI_ERR_UNSUPPORTED,
                 "int32 outputs need integral alpha, beta, x_factor with |value| <= 2^24");
-  int dev = -1;
-  if (hipGetDevice(&dev) != hipSuccess || dev != h->device)
-    return fail(GEMM_EPI_ERR_DEVICE, "current device %d is not the handle's device %d", dev,
-                h->device);
+  const int rc = check_device(h->device);
+  if (rc) return rc;
 
   Params p;
   p.A = A;
@@ -566,7 +564,9 @@ static int run_impl(const gemm_epi_handle* hc, const void* A, const void* B, con
   p.u8_bias = 0;
   p.int_unit = int_path && p.ialpha == 1 && (p.ibeta == 1 || !use_c) && (p.ix == 1 || !use_x) ? 1 : 0;
   if (h->ws_bytes > 0) {
-    if (use_static) {
+    if (ext_ws) {
+      p.ws = ext_ws;
+    } else if (use_static) {
       if (h->ws_bytes > kScratchBytes)
         return fail(GEMM_EPI_ERR_UNSUPPORTED,
                     "workspace of %lld bytes exceeds the static scratch of %lld bytes",
@@ -673,6 +673,13 @@ extern "C" int gemm_epi_run_static(const gemm_epi_handle* h, const void* A, cons
   return run_impl(h, A, B, C, X, D, Y, alpha, beta, x_factor, stream, true);
 }
 
+int64_t gemm_epi::handle_workspace(const gemm_epi_handle* h) { return h->ws_bytes; }
+
+int gemm_epi::run_with_workspace(const gemm_epi_handle* h, const void* A, const void* B, const void* C, void* D,
+                                 float beta, void* ws, void* stream) {
+  return run_impl(h, A, B, C, nullptr, D, nullptr, 1.0f, beta, 0.0f, stream, false, ws);
+}
+
 extern "C" int gemm_epi_destroy(gemm_epi_handle* h) {
   if (h && h->ws.load()) (void)hipFree(h->ws.load());
   delete h;
@@ -719,4 +726,4 @@ extern "C" const char* gemm_epi_status_string(int code) {
   }
 }
 
-extern "C" const char* gemm_epi_last_error(void) { return g_last_error; }
+extern "C" const char* gemm_epi_last_error(void) { return gemm_epi::g_last_error; }

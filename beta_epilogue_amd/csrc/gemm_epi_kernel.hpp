@@ -116,6 +116,9 @@ struct Params {
   int32_t int_unit;
 };
 
+// Arguments of the linear layer's kernels (gemm_linear.hpp).
+struct LinParams;
+
 // ---------------------------------------------------------------------------
 // MFMA traits per A/B element type and block size BLK (32: 32x32 output
 // blocks, 16: 16x16).  KSB = bytes of K one MFMA consumes per row.  Lane l
@@ -243,10 +246,15 @@ template <> struct Mma<T_U8, 32> : Mma<T_I8, 32> {};
 //   DQ          two-stage ring: quarters of a K tile's DMA issued early in
 //               step 0 of the K tile before its use (see the mainloop)
 //   BLK         MFMA output block: 32 (32x32) or 16 (16x16)
+//   LIN         the linear layer's arguments, row strides and epilogue
+//               (K-major A and B, N-major D)
 template <int AB_, bool A_KMAJOR_, bool B_KMAJOR_, bool CD_NMAJOR_, int BM_ = 256, int BN_ = 256,
           int ROWB_ = 128, int WAVES_M_ = 2, int WAVES_N_ = 2, int STAGES_ = 2, int DQ_ = 0,
-          int BLK_ = 32>
+          int BLK_ = 32, bool LIN_ = false>
 struct Cfg {
+  static constexpr bool LIN = LIN_;
+  static_assert(!LIN || (A_KMAJOR_ && B_KMAJOR_ && CD_NMAJOR_ && AB_ != T_U8), "layouts of the linear kernels");
+  using params_t = typename std::conditional<LIN_, LinParams, Params>::type;
   static constexpr int BLK = BLK_;
   using MM = Mma<AB_, BLK_>;
   static constexpr int DQ = DQ_;
@@ -957,11 +965,16 @@ struct U8Init {
   }
 };
 
+// The linear layer's epilogue (gemm_linear_epilogue.hpp; LIN kernels only).
+template <class CF, int T, class ACC>
+__device__ void epilogue_linear(const LinParams& p, const ACC (&acc)[CF::FM][CF::FN], char* lds, int wave, int lane,
+                                int mw, int nw);
+
 // ---------------------------------------------------------------------------
 // The kernel
 // ---------------------------------------------------------------------------
 template <class CF>
-__global__ __launch_bounds__(CF::THREADS, 1) void gemm_epi_kernel(Params p) {
+__global__ __launch_bounds__(CF::THREADS, 1) void gemm_epi_kernel(typename CF::params_t p) {
   using MM = typename CF::MM;
   using acc_t = typename MM::acc_t;
   using frag_t = typename MM::frag_t;
@@ -1011,8 +1024,15 @@ __global__ __launch_bounds__(CF::THREADS, 1) void gemm_epi_kernel(Params p) {
     const int m0 = tc.tm * BM, n0 = tc.tn * BN;
 
     // ---- staging set-up --------------------------------------------------
-    opa.setup((const char*)p.A + (int64_t)l * p.M * p.K * ES, p.M, p.K, kbeg, m0, wave, lane);
-    opb.setup((const char*)p.B + (int64_t)l * p.N * p.K * ES, p.N, p.K, kbeg, n0, wave, lane);
+    if constexpr (CF::LIN) {
+      // the row stride stands for the row length: chunks past K are masked
+      // by the K tile's guard, not by the extent
+      opa.setup((const char*)p.A, p.M, p.lda, kbeg, m0, wave, lane);
+      opb.setup((const char*)p.B, p.N, p.ldb, kbeg, n0, wave, lane);
+    } else {
+      opa.setup((const char*)p.A + (int64_t)l * p.M * p.K * ES, p.M, p.K, kbeg, m0, wave, lane);
+      opb.setup((const char*)p.B + (int64_t)l * p.N * p.K * ES, p.N, p.K, kbeg, n0, wave, lane);
+    }
 
     acc_t acc[CF::FM][CF::FN];
 #pragma unroll
@@ -1238,6 +1258,10 @@ __global__ __launch_bounds__(CF::THREADS, 1) void gemm_epi_kernel(Params p) {
       q.relu = 0;
       if constexpr (CF::INT) epilogue_typed<CF, NM, T_I32, true>(q, acc, lds, wave, lane, 0, emw - m0, enw - n0);
       else epilogue_typed<CF, NM, T_F32>(q, acc, lds, wave, lane, 0, emw - m0, enw - n0);
+    } else if constexpr (CF::LIN) {
+      if (p.d_dtype == T_F16) epilogue_linear<CF, T_F16>(p, acc, lds, wave, lane, emw, enw);
+      else if (p.d_dtype == T_BF16) epilogue_linear<CF, T_BF16>(p, acc, lds, wave, lane, emw, enw);
+      else if constexpr (CF::AB != T_E4M3) epilogue_linear<CF, T_F32>(p, acc, lds, wave, lane, emw, enw);
     } else if constexpr (CF::INT) {
       if (p.int_unit) epilogue_typed<CF, NM, T_I32, true>(p, acc, lds, wave, lane, l, emw, enw);
       else epilogue_typed<CF, NM, T_I32, false>(p, acc, lds, wave, lane, l, emw, enw);

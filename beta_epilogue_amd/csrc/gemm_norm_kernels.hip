@@ -1,0 +1,344 @@
+// gemm_norm_kernels.hip -- the root-mean-square norm with the residual's
+// addition, into 16 bits, fp32, or 8 bits with a scale per row, and its
+// backward.
+//
+//   h = x + r (fp32),  s = 1 / sqrt(mean(h^2) + eps),  y = h s w
+//   8 bits: scale = max(max|y| / qmax, 2^-126), q = round(y / scale)
+//   backward, with s of the stored h and g = dy w:
+//     dh = dh_in + s g - h s^3 mean(g h),   dw = sum over rows of dy h s
+//
+// Both are bound by memory: a row is read once into registers (TPR threads
+// with NV groups of 8 elements each), its sums are joined by shuffles and one
+// LDS exchange, and the results are written from the registers, so no byte
+// moves twice.  All sums and the norm itself are fp32; the only roundings are
+// those of the outputs (y and h are both rounded from the fp32 values).
+// Groups of 8 are loaded and stored as 16-byte (8-bit: 8-byte) accesses at
+// element alignment (gfx950 takes unaligned global accesses), so odd row
+// lengths and strides run the same path; a group that the row's end cuts is
+// moved element by element.
+#include "gemm_norm.hpp"
+
+#include "gemm_epi_kernel.hpp"
+
+namespace gemm_epi {
+
+namespace {
+
+template <int T> struct Elem;
+template <> struct Elem<T_F16> { typedef _Float16 type; };
+template <> struct Elem<T_BF16> { typedef __bf16 type; };
+template <> struct Elem<T_F32> { typedef float type; };
+
+typedef v4u v4u_any __attribute__((aligned(2)));  // 16 bytes at element alignment
+typedef v4f v4f_any __attribute__((aligned(4)));
+typedef v2u v2u_any __attribute__((aligned(1)));
+
+typedef float v8f __attribute__((ext_vector_type(8)));
+
+// Elements [c, c + 8) of a row that ends at cols; 0 past its end.
+template <int T>
+__device__ __forceinline__ v8f load8(const void* row, int64_t c, int64_t cols) {
+  const typename Elem<T>::type* p = (const typename Elem<T>::type*)row + c;
+  v8f v = {};
+  if (c + 8 <= cols) {
+    v4f lo, hi;
+    if constexpr (T == T_F32) {
+      lo = *(const v4f_any*)p;
+      hi = *(const v4f_any*)(p + 4);
+    } else {
+      const v4u r = *(const v4u_any*)p;
+      lo = epi_dec<T>(r, 0);
+      hi = epi_dec<T>(r, 1);
+    }
+    v = v8f{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (c + k < cols) v[k] = (float)p[k];
+  }
+  return v;
+}
+
+template <int T>
+__device__ __forceinline__ void store8(void* row, int64_t c, int64_t cols, v8f v) {
+  typename Elem<T>::type* p = (typename Elem<T>::type*)row + c;
+  if (c + 8 <= cols) {
+    if constexpr (T == T_F32) {
+      *(v4f_any*)p = v4f{v[0], v[1], v[2], v[3]};
+      *(v4f_any*)(p + 4) = v4f{v[4], v[5], v[6], v[7]};
+    } else {
+      typedef typename Elem<T>::type vec8 __attribute__((ext_vector_type(8)));
+      vec8 o;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] = (typename Elem<T>::type)v[k];
+      *(v4u_any*)p = __builtin_bit_cast(v4u, o);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (c + k < cols) p[k] = (typename Elem<T>::type)v[k];
+  }
+}
+
+template <int T>
+__device__ __forceinline__ v8f load_weight8(const void* w, bool f32, int64_t c, int64_t cols) {
+  return f32 ? load8<T_F32>(w, c, cols) : load8<T>(w, c, cols);
+}
+
+// Rounds to nearest-even into 8 bits and stores.  A NaN stays NaN in e4m3
+// and becomes 0 in int8 (the row's scale is NaN then).
+template <int T>
+__device__ __forceinline__ void store8_q(void* row, int64_t c, int64_t cols, v8f v) {
+  constexpr float QMAX = T == T_E4M3 ? 448.0f : 127.0f;
+  uint32_t w[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    float q[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float x = v[4 * j + k];
+      q[k] = x > QMAX ? QMAX : (x < -QMAX ? -QMAX : x);
+    }
+    if constexpr (T == T_E4M3) {
+      int b = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+      w[j] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], b, true);
+    } else {
+      w[j] = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[j] |= ((uint32_t)(int)__builtin_rintf(q[k] == q[k] ? q[k] : 0.0f) & 0xffu) << (8 * k);
+    }
+  }
+  uint8_t* p = (uint8_t*)row + c;
+  if (c + 8 <= cols) {
+    *(v2u_any*)p = v2u{w[0], w[1]};
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (c + k < cols) p[k] = (uint8_t)(w[k / 4] >> (8 * (k % 4)));
+  }
+}
+
+// A sum (or maximum) over the TPR threads of a row, in a fixed order; every
+// thread gets it.  red: one word per wave and exchange, not reused before the
+// next barrier of the row.
+struct Sum {
+  static __device__ __forceinline__ float join(float a, float b) { return a + b; }
+};
+struct Max {  // a NaN wins
+  static __device__ __forceinline__ float join(float a, float b) { return b > a || b != b ? b : a; }
+};
+template <class OP, int TPR>
+__device__ __forceinline__ float row_join(float v, float* red) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) v = OP::join(v, __shfl_xor(v, d, 64));
+  if constexpr (TPR > 64) {
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) red[wave] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int w = 1; w < TPR / 64; ++w) v = OP::join(v, red[w]);
+  }
+  return v;
+}
+
+template <int TPR> constexpr int block_threads() { return TPR > 256 ? TPR : 256; }
+
+template <int TX, int TY, int TPR, int NV>
+__global__ __launch_bounds__(block_threads<TPR>()) void rmsnorm_kernel(NormParams p) {
+  constexpr int RPB = block_threads<TPR>() / TPR;
+  constexpr bool Q = TY == T_E4M3 || TY == T_I8;
+  __shared__ float red[2][TPR / 64];
+  const int t = threadIdx.x % TPR;
+  const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+  if (row >= p.rows) return;  // whole waves, and whole workgroups where rows share barriers
+  constexpr int XS = sizeof(typename Elem<TX>::type);
+  const char* x = (const char*)p.x + row * p.ldx * XS;
+  const char* r = p.r ? (const char*)p.r + row * p.ldr * XS : nullptr;
+  v8f h[NV], w[NV];
+  float ss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int64_t c = (int64_t)(i * TPR + t) * 8;
+    h[i] = load8<TX>(x, c, p.cols);
+    if (r) h[i] += load8<TX>(r, c, p.cols);
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) w[i] = load_weight8<TX>(p.w, p.w_f32, (int64_t)(i * TPR + t) * 8, p.cols);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) ss = __builtin_fmaf(h[i][k], h[i][k], ss);
+  }
+  if (p.h) {
+    char* ho = (char*)p.h + row * p.ldh * XS;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) store8<TX>(ho, (int64_t)(i * TPR + t) * 8, p.cols, h[i]);
+  }
+  ss = row_join<Sum, TPR>(ss, red[0]);
+  const float s = 1.0f / __builtin_sqrtf(ss / (float)p.cols + p.eps);
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) h[i][k] = h[i][k] * s * w[i][k];
+  if constexpr (Q) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m = Max::join(m, __builtin_fabsf(h[i][k]));
+    m = row_join<Max, TPR>(m, red[1]);
+    constexpr float QMAX = TY == T_E4M3 ? 448.0f : 127.0f;
+    float scale = m / QMAX;
+    scale = scale < 0x1p-126f ? 0x1p-126f : scale;  // (a NaN stays)
+    const float inv = 1.0f / scale;
+    uint8_t* y = (uint8_t*)p.y + row * p.ldy;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) h[i][k] *= inv;
+      store8_q<TY>(y, (int64_t)(i * TPR + t) * 8, p.cols, h[i]);
+    }
+    if (t == 0) p.scale[row] = scale;
+  } else {
+    char* y = (char*)p.y + row * p.ldy * XS;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) store8<TX>(y, (int64_t)(i * TPR + t) * 8, p.cols, h[i]);
+  }
+}
+
+// The backward: a workgroup walks rows blockIdx, blockIdx + grid, ... (RPB at
+// a time), keeps its weights and its part of dweight in registers, and leaves
+// one partial sum per column; colsum adds the workgroups in a fixed order.
+template <int T, int TPR, int NV>
+__global__ __launch_bounds__(block_threads<TPR>()) void rmsnorm_grad_kernel(NormGradParams p) {
+  constexpr int RPB = block_threads<TPR>() / TPR;
+  constexpr int XS = sizeof(typename Elem<T>::type);
+  __shared__ float red[2][2][TPR / 64];
+  __shared__ float joined[RPB > 1 ? RPB * TPR * NV * 8 : 1];
+  const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  v8f w[NV], dw[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    w[i] = load_weight8<T>(p.w, p.w_f32, (int64_t)(i * TPR + t) * 8, p.cols);
+    dw[i] = v8f{};
+  }
+  const float inv_cols = 1.0f / (float)p.cols;
+  int flip = 0;
+  for (int64_t row = (int64_t)blockIdx.x * RPB + sub; row < p.rows; row += (int64_t)gridDim.x * RPB) {
+    const char* hp = (const char*)p.h + row * p.ldh * XS;
+    const char* gp = (const char*)p.dy + row * p.ldy * XS;
+    v8f h[NV], g[NV];
+    float ss = 0.0f, gh = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      h[i] = load8<T>(hp, (int64_t)(i * TPR + t) * 8, p.cols);
+      g[i] = load8<T>(gp, (int64_t)(i * TPR + t) * 8, p.cols);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        ss = __builtin_fmaf(h[i][k], h[i][k], ss);
+        gh = __builtin_fmaf(g[i][k] * w[i][k], h[i][k], gh);
+      }
+    ss = row_join<Sum, TPR>(ss, red[flip][0]);
+    gh = row_join<Sum, TPR>(gh, red[flip][1]);
+    flip ^= 1;  // the next row's words are others: one barrier separates reuse
+    const float s = 1.0f / __builtin_sqrtf(ss * inv_cols + p.eps);
+    const float f = s * s * s * (gh * inv_cols);
+    char* op = (char*)p.dh + row * p.ldo * XS;
+    const char* ip = p.dh_in ? (const char*)p.dh_in + row * p.ldi * XS : nullptr;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t c = (int64_t)(i * TPR + t) * 8;
+      v8f d = {};
+      if (ip) d = load8<T>(ip, c, p.cols);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        dw[i][k] = __builtin_fmaf(g[i][k] * s, h[i][k], dw[i][k]);
+        d[k] += __builtin_fmaf(g[i][k] * w[i][k], s, -(h[i][k] * f));
+      }
+      store8<T>(op, c, p.cols, d);
+    }
+  }
+  if (!p.partial) return;
+  float* out = p.partial + (int64_t)blockIdx.x * p.cols;
+  if constexpr (RPB > 1) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) joined[(sub * NV * TPR + i * TPR + t) * 8 + k] = dw[i][k];
+    __syncthreads();
+    for (int c = threadIdx.x; c < p.cols; c += block_threads<TPR>()) {
+      float v = joined[c];
+#pragma unroll
+      for (int u = 1; u < RPB; ++u) v += joined[u * NV * TPR * 8 + c];
+      out[c] = v;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) store8<T_F32>(out, (int64_t)(i * TPR + t) * 8, p.cols, dw[i]);
+  }
+}
+
+template <int TX, int TY, int TPR, int NV>
+void norm(const NormParams& p, hipStream_t s) {
+  constexpr int RPB = block_threads<TPR>() / TPR;
+  hipLaunchKernelGGL((rmsnorm_kernel<TX, TY, TPR, NV>), dim3((unsigned)((p.rows + RPB - 1) / RPB)),
+                     dim3(block_threads<TPR>()), 0, s, p);
+}
+
+template <int TX, int TY>
+void norm_cols(const NormParams& p, hipStream_t s) {
+  if (p.cols <= 512) norm<TX, TY, 64, 1>(p, s);
+  else if (p.cols <= 1024) norm<TX, TY, 64, 2>(p, s);
+  else if (p.cols <= 2048) norm<TX, TY, 256, 1>(p, s);
+  else if (p.cols <= 4096) norm<TX, TY, 256, 2>(p, s);
+  else if (p.cols <= 8192) norm<TX, TY, 256, 4>(p, s);
+  else norm<TX, TY, 1024, 2>(p, s);
+}
+
+template <int TX>
+void norm_y(int y_dtype, const NormParams& p, hipStream_t s) {
+  if (y_dtype == T_E4M3) norm_cols<TX, T_E4M3>(p, s);
+  else if (y_dtype == T_I8) norm_cols<TX, T_I8>(p, s);
+  else norm_cols<TX, TX>(p, s);
+}
+
+template <int T, int TPR, int NV>
+void grad(const NormGradParams& p, int grid, hipStream_t s) {
+  hipLaunchKernelGGL((rmsnorm_grad_kernel<T, TPR, NV>), dim3(grid), dim3(block_threads<TPR>()), 0, s, p);
+}
+
+template <int T>
+void grad_cols(const NormGradParams& p, int grid, hipStream_t s) {
+  if (p.cols <= 512) grad<T, 64, 1>(p, grid, s);
+  else if (p.cols <= 1024) grad<T, 64, 2>(p, grid, s);
+  else if (p.cols <= 2048) grad<T, 256, 1>(p, grid, s);
+  else if (p.cols <= 4096) grad<T, 256, 2>(p, grid, s);
+  else if (p.cols <= 8192) grad<T, 256, 4>(p, grid, s);
+  else grad<T, 1024, 2>(p, grid, s);
+}
+
+}  // namespace
+
+void launch_rmsnorm(int x_dtype, int y_dtype, const NormParams& p, hipStream_t s) {
+  if (x_dtype == T_F16) norm_y<T_F16>(y_dtype, p, s);
+  else if (x_dtype == T_BF16) norm_y<T_BF16>(y_dtype, p, s);
+  else norm_y<T_F32>(y_dtype, p, s);
+}
+
+int rmsnorm_grad_grid(int64_t rows, int64_t cols, int cus) {
+  const int64_t groups = cols <= 1024 ? (rows + 3) / 4 : rows;
+  const int64_t most = (int64_t)cus * (cols > 8192 ? 1 : 2);
+  return (int)(groups < most ? groups : most);
+}
+
+void launch_rmsnorm_grad(int x_dtype, const NormGradParams& p, int grid, hipStream_t s) {
+  if (x_dtype == T_F16) grad_cols<T_F16>(p, grid, s);
+  else if (x_dtype == T_BF16) grad_cols<T_BF16>(p, grid, s);
+  else grad_cols<T_F32>(p, grid, s);
+}
+
+}  // namespace gemm_epi
