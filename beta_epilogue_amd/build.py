@@ -26,13 +26,15 @@ PART_SOURCE = os.path.join(CSRC, "gemm_epi_part.hip")
 GEMM_EPI_PARTS = 16
 LINEAR_PART_SOURCE = os.path.join(CSRC, "gemm_linear_part.hip")
 GEMM_LINEAR_PARTS = 8
+LINEAR_GRAD_MM_SOURCE = os.path.join(CSRC, "gemm_linear_grad_mm.hip")
+GEMM_LINEAR_GRAD_PARTS = 4
 LINEAR_SOURCES = [os.path.join(CSRC, f) for f in ("gemm_linear.hip", "gemm_linear_rows.hip", "gemm_linear_grad.hip",
                                                   "gemm_norm.hip", "gemm_norm_kernels.hip")]
-SOURCES = [MAIN_SOURCE, PART_SOURCE, SPLITK_SOURCE, PREP_SOURCE, LINEAR_PART_SOURCE] + LINEAR_SOURCES
+SOURCES = [MAIN_SOURCE, PART_SOURCE, SPLITK_SOURCE, PREP_SOURCE, LINEAR_PART_SOURCE, LINEAR_GRAD_MM_SOURCE] + LINEAR_SOURCES
 HEADERS = [os.path.join(CSRC, "gemm_epi_kernel.hpp"), os.path.join(CSRC, "gemm_epi_launch.hpp"),
            os.path.join(CSRC, "gemm_epi_splitk.hpp"), os.path.join(CSRC, "gemm_epi_prep.hpp"),
            os.path.join(CSRC, "gemm_epi_raster.hpp"), os.path.join(CSRC, "gemm_epi_variants.inc"),
-           os.path.join(CSRC, "gemm_epi_host.hpp"), os.path.join(CSRC, "gemm_epi_plan.hpp"),
+           os.path.join(CSRC, "gemm_epi_host.hpp"),
            os.path.join(CSRC, "linear_act.hpp"), os.path.join(CSRC, "gemm_linear_epilogue.hpp"),
            os.path.join(CSRC, "gemm_linear.hpp"), os.path.join(CSRC, "gemm_linear_variants.inc"),
            os.path.join(CSRC, "gemm_norm.hpp"),
@@ -129,6 +131,8 @@ def build(verbose: bool = False, extra=(), only=None, cache_dir=None) -> str:
                                                                       "linear_act.hpp", "gemm_linear_epilogue.hpp")]
         units += [obj("linear%d.o" % k, LINEAR_PART_SOURCE, linear_deps, ["-DGEMM_LINEAR_PART=%d" % k])
                   for k in range(GEMM_LINEAR_PARTS)]
+        units += [obj("linear_grad%d.o" % k, LINEAR_GRAD_MM_SOURCE, linear_deps, ["-DGEMM_LINEAR_GRAD_PART=%d" % k])
+                  for k in range(GEMM_LINEAR_GRAD_PARTS)]
         units += [obj(os.path.basename(f) + ".o", f, HEADERS) for f in LINEAR_SOURCES]
         jobs = [cmd for _, cmd in units if cmd]
         ceil_tmp = CEILING_LIB + ".tmp%d" % os.getpid()

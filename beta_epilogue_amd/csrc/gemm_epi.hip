@@ -22,7 +22,6 @@
 #include "gemm_epi.h"
 #include "gemm_epi_host.hpp"
 #include "gemm_epi_kernel.hpp"
-#include "gemm_epi_plan.hpp"
 #include "gemm_epi_launch.hpp"
 #include "gemm_epi_splitk.hpp"
 #include "gemm_epi_prep.hpp"
@@ -318,16 +317,57 @@ static bool variant_fits(const Variant& v, const gemm_epi_desc* d) {
   return v.ab == (widened(d) ? gemm_epi::T_F16 : exact_ab(d));
 }
 
-// The cost model's view of a problem (gemm_epi_plan.hpp).
-static PlanProblem plan_problem(const gemm_epi_desc* d) {
-  double bytes = 0.0;
-  for (int t : {d->c_dtype, d->x_dtype, d->d_dtype, d->y_dtype})
-    if (t != GEMM_EPI_NONE) bytes += elem_bytes(t);
-  return PlanProblem{d->M, d->N, d->K, d->L, bytes, d->ab_dtype != GEMM_EPI_U8};
+// Plan cost model (measured on MI355X, fp16 with C, X, D, Y; times in us).
+// A K tile of one output tile takes 1.1 us with 256x256 tiles; with the
+// smaller tiles their share of the work at a lower per-CU rate (192x256:
+// 0.75 at 0.9, 128x256: 0.5 at 0.67, 128x128: 0.25 at ~0.46).  The split-K
+// reduction costs 4 us plus its bytes (S partial-sum slots and C, X, D, Y
+// per split tile) at 5 TB/s.
+static double ktile_us(const Variant& v) {
+  if (v.bm == 256 && v.bn == 256) return 1.1;
+  if (v.bm == 192 && v.bn == 256) return 1.1 * 0.75 / 0.9;
+  if (v.bm == 128 && v.bn == 256) return 1.1 * 0.75;
+  return 0.6;
 }
 
+struct SplitChoice {
+  int64_t splits, tail;  // K slices of the split tiles (1: none), split tiles
+  double us;             // modelled time of the launch
+};
+
+// The library's split choice for variant v and the modelled time: when the
+// last round of tiles (tiles % cus, all of them with fewer tiles than CUs)
+// would leave at least half of the CUs idle, those tiles may run in S K
+// slices after whole-K rounds of the others; S (2 .. min(cus / last,
+// K tiles / 4, 16)) maximises the time saved in the last round,
+// (K tiles - ceil(K tiles / S)) K-tile times, less the reduction's cost; no S
+// with a positive balance, no split.
 static SplitChoice split_choice(const Variant& v, const gemm_epi_desc* d, int64_t cus) {
-  return split_choice(v.bm, v.bn, v.bk, plan_problem(d), cus);
+  const int64_t tiles = ((d->M + v.bm - 1) / v.bm) * ((d->N + v.bn - 1) / v.bn) * d->L;
+  const int64_t ktiles = (d->K + v.bk - 1) / v.bk;
+  const double tk = ktile_us(v);
+  const int64_t last = tiles % cus;
+  SplitChoice c{1, 0, (double)((tiles + cus - 1) / cus) * ktiles * tk};
+  if (last == 0 || last * 2 > cus || d->ab_dtype == GEMM_EPI_U8) return c;
+  const double slot_bytes = 4.0 * v.bm * v.bn;
+  double epi_bytes = 0.0;
+  for (int t : {d->c_dtype, d->x_dtype, d->d_dtype, d->y_dtype})
+    if (t != GEMM_EPI_NONE) epi_bytes += (double)elem_bytes(t) * v.bm * v.bn;
+  const int64_t smax = std::min<int64_t>(std::min<int64_t>(cus / last, ktiles / 4), 16);
+  double best = 0.0;
+  for (int64_t s = 2; s <= smax; ++s) {
+    const double saved_us = (double)(ktiles - (ktiles + s - 1) / s) * tk;
+    const double cost_us = 4.0 + (double)last * (s * slot_bytes + epi_bytes) / 5.0e6;
+    if (saved_us - cost_us > best) {
+      best = saved_us - cost_us;
+      c.splits = s;
+    }
+  }
+  if (c.splits > 1) {
+    c.tail = last;
+    c.us -= best;
+  }
+  return c;
 }
 
 extern "C" int gemm_epi_create_variant(const gemm_epi_desc* desc, int variant,
@@ -490,11 +530,10 @@ static bool integral_24(float v) {
   return std::isfinite(v) && std::nearbyint(v) == v && std::fabs(v) <= 16777216.0f;
 }
 
-// One fused GEMM; plans with a workspace use ext_ws if given, else the handle's
-// own (allocated here on first use) or, with use_static, the static scratch array.
+// One fused GEMM; split-K plans use the handle's workspace (allocated here on
+// first use) or, with use_static, the static scratch array.
 static int run_impl(const gemm_epi_handle* hc, const void* A, const void* B, const void* C, const void* X,
-                    void* D, void* Y, float alpha, float beta, float x_factor, void* stream, bool use_static,
-                    void* ext_ws = nullptr) {
+                    void* D, void* Y, float alpha, float beta, float x_factor, void* stream, bool use_static) {
   clear_error();
   if (!hc) return fail(GEMM_EPI_ERR_INVALID_ARG, "handle is NULL");
   gemm_epi_handle* h = const_cast<gemm_epi_handle*>(hc);  // only the lazily allocated workspace changes
@@ -564,9 +603,7 @@ static int run_impl(const gemm_epi_handle* hc, const void* A, const void* B, con
   p.u8_bias = 0;
   p.int_unit = int_path && p.ialpha == 1 && (p.ibeta == 1 || !use_c) && (p.ix == 1 || !use_x) ? 1 : 0;
   if (h->ws_bytes > 0) {
-    if (ext_ws) {
-      p.ws = ext_ws;
-    } else if (use_static) {
+    if (use_static) {
       if (h->ws_bytes > kScratchBytes)
         return fail(GEMM_EPI_ERR_UNSUPPORTED,
                     "workspace of %lld bytes exceeds the static scratch of %lld bytes",
@@ -671,13 +708,6 @@ extern "C" int gemm_epi_run_static(const gemm_epi_handle* h, const void* A, cons
                                    const void* X, void* D, void* Y, float alpha, float beta,
                                    float x_factor, void* stream) {
   return run_impl(h, A, B, C, X, D, Y, alpha, beta, x_factor, stream, true);
-}
-
-int64_t gemm_epi::handle_workspace(const gemm_epi_handle* h) { return h->ws_bytes; }
-
-int gemm_epi::run_with_workspace(const gemm_epi_handle* h, const void* A, const void* B, const void* C, void* D,
-                                 float beta, void* ws, void* stream) {
-  return run_impl(h, A, B, C, nullptr, D, nullptr, 1.0f, beta, 0.0f, stream, false, ws);
 }
 
 extern "C" int gemm_epi_destroy(gemm_epi_handle* h) {

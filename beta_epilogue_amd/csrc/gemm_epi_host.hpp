@@ -1,6 +1,5 @@
 // gemm_epi_host.hpp -- what the host-side translation units of the library
-// share: the thread's error text, type sizes, the device check, and running a
-// GEMM handle on a workspace that the caller owns.
+// share: the thread's error text, type sizes, and the checks every run makes.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -34,12 +33,6 @@ int check_workspace(const void* ws, int64_t have, int64_t need);
 
 // The status of the launch just made (hipGetLastError).
 int launched();
-
-// Workspace bytes of a handle's runs, and gemm_epi_run with the workspace ws
-// (at least that many bytes) in place of the handle's own.
-int64_t handle_workspace(const gemm_epi_handle* h);
-int run_with_workspace(const gemm_epi_handle* h, const void* A, const void* B, const void* C, void* D, float beta,
-                       void* ws, void* stream);
 
 inline int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
 

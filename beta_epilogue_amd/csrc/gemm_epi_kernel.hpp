@@ -246,15 +246,19 @@ template <> struct Mma<T_U8, 32> : Mma<T_I8, 32> {};
 //   DQ          two-stage ring: quarters of a K tile's DMA issued early in
 //               step 0 of the K tile before its use (see the mainloop)
 //   BLK         MFMA output block: 32 (32x32) or 16 (16x16)
-//   LIN         the linear layer's arguments, row strides and epilogue
-//               (K-major A and B, N-major D)
+//   LIN         1: the linear layer's arguments, row strides (of K-major
+//               operands) and epilogue (N-major D); 2: the same without bias,
+//               scales, activation and Z (its backward's products)
+//   OCC         workgroups meant to share a compute unit (bounds the registers)
 template <int AB_, bool A_KMAJOR_, bool B_KMAJOR_, bool CD_NMAJOR_, int BM_ = 256, int BN_ = 256,
           int ROWB_ = 128, int WAVES_M_ = 2, int WAVES_N_ = 2, int STAGES_ = 2, int DQ_ = 0,
-          int BLK_ = 32, bool LIN_ = false>
+          int BLK_ = 32, int LIN_ = 0, int OCC_ = 1>
 struct Cfg {
-  static constexpr bool LIN = LIN_;
-  static_assert(!LIN || (A_KMAJOR_ && B_KMAJOR_ && CD_NMAJOR_ && AB_ != T_U8), "layouts of the linear kernels");
-  using params_t = typename std::conditional<LIN_, LinParams, Params>::type;
+  static constexpr int OCC = OCC_;
+  static constexpr bool LIN = LIN_ != 0;
+  static constexpr bool LIN_ACT = LIN_ == 1;
+  static_assert(!LIN || (CD_NMAJOR_ && AB_ != T_U8), "what the linear kernels have");
+  using params_t = typename std::conditional<LIN_ != 0, LinParams, Params>::type;
   static constexpr int BLK = BLK_;
   using MM = Mma<AB_, BLK_>;
   static constexpr int DQ = DQ_;
@@ -973,14 +977,15 @@ __device__ void epilogue_linear(const LinParams& p, const ACC (&acc)[CF::FM][CF:
 // ---------------------------------------------------------------------------
 // The kernel
 // ---------------------------------------------------------------------------
+// The work of workgroup `bid` of `G` that share a problem, with the LDS array
+// `lds` of CF::LDS_BYTES (1 KiB aligned).
 template <class CF>
-__global__ __launch_bounds__(CF::THREADS, 1) void gemm_epi_kernel(typename CF::params_t p) {
+__device__ __forceinline__ void gemm_epi_body(const typename CF::params_t& p, char* lds, int bid, int G) {
   using MM = typename CF::MM;
   using acc_t = typename MM::acc_t;
   using frag_t = typename MM::frag_t;
   constexpr int ES = MM::ESIZE;
   constexpr int BM = CF::BM, BN = CF::BN, S = CF::STAGES;
-  __shared__ __attribute__((aligned(1024))) char lds[CF::LDS_BYTES];
   const uint32_t lds_u32 = (uint32_t)(uintptr_t)(lds_void_t*)lds;  // LDS address of the array
 
   const int tid = threadIdx.x;
@@ -988,8 +993,6 @@ __global__ __launch_bounds__(CF::THREADS, 1) void gemm_epi_kernel(typename CF::p
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave % CF::WAVES_M, wn = wave / CF::WAVES_M;
 
-  const int G = gridDim.x;
-  const int bid = blockIdx.x;
   const int g = p.xcd_remap ? (bid & 7) * (G >> 3) + (bid >> 3) : bid;
 
   using OpA = Operand<CF, BM, CF::WM, CF::A_KMAJOR>;
@@ -1025,10 +1028,10 @@ __global__ __launch_bounds__(CF::THREADS, 1) void gemm_epi_kernel(typename CF::p
 
     // ---- staging set-up --------------------------------------------------
     if constexpr (CF::LIN) {
-      // the row stride stands for the row length: chunks past K are masked
-      // by the K tile's guard, not by the extent
-      opa.setup((const char*)p.A, p.M, p.lda, kbeg, m0, wave, lane);
-      opb.setup((const char*)p.B, p.N, p.ldb, kbeg, n0, wave, lane);
+      // a K-major operand's row stride stands for its row length: chunks past
+      // K are masked by the K tile's guard, not by the extent
+      opa.setup((const char*)p.A, p.M, CF::A_KMAJOR ? p.lda : p.K, kbeg, m0, wave, lane);
+      opb.setup((const char*)p.B, p.N, CF::B_KMAJOR ? p.ldb : p.K, kbeg, n0, wave, lane);
     } else {
       opa.setup((const char*)p.A + (int64_t)l * p.M * p.K * ES, p.M, p.K, kbeg, m0, wave, lane);
       opb.setup((const char*)p.B + (int64_t)l * p.N * p.K * ES, p.N, p.K, kbeg, n0, wave, lane);
@@ -1272,6 +1275,12 @@ __global__ __launch_bounds__(CF::THREADS, 1) void gemm_epi_kernel(typename CF::p
     }
     barrier_lds();  // LDS is reused by the next tile's prologue
   }
+}
+
+template <class CF>
+__global__ __launch_bounds__(CF::THREADS, CF::OCC) void gemm_epi_kernel(typename CF::params_t p) {
+  __shared__ __attribute__((aligned(1024))) char lds[CF::LDS_BYTES];
+  gemm_epi_body<CF>(p, lds, blockIdx.x, gridDim.x);
 }
 
 }  // namespace gemm_epi

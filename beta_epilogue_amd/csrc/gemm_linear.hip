@@ -3,13 +3,13 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cstdint>
 #include <cstdio>
 #include <cstring>
 #include <new>
 
 #include "gemm_epi_host.hpp"
 #include "gemm_epi_linear.h"
-#include "gemm_epi_plan.hpp"
 #include "gemm_epi_prep.hpp"
 #include "gemm_linear.hpp"
 
@@ -19,17 +19,69 @@ namespace {
 
 struct LinearVariant {
   const char* name;
-  int part, ab, bm, bn, bk, lds;
+  int part, ab, bm, bn, bk, lds, occ;
 };
-#define X(PART, AB, BM, BN, BL, NAME) \
-  {NAME, PART, AB, BM, BN, LinearCfg<AB, BM, BN, BL>::BK, LinearCfg<AB, BM, BN, BL>::LDS_BYTES},
+#define X(PART, AB, BM, BN, S, OCC, BL, NAME) \
+  {NAME, PART, AB, BM, BN, LinearCfg<AB, BM, BN, S, OCC, BL>::BK, LinearCfg<AB, BM, BN, S, OCC, BL>::LDS_BYTES, OCC},
 const LinearVariant kLinear[] = {
 #include "gemm_linear_variants.inc"
 };
 #undef X
 constexpr int kTiles = (int)(sizeof kLinear / sizeof kLinear[0]);
 constexpr int kRowsVariant = kTiles;  // the few-row kernels, one entry
-constexpr int kThreads = 256, kRowsThreads = 512;
+constexpr int kThreads = 256;
+
+// The plan's cost model (us), fitted to forced plans of 75 shapes (M 90 to
+// 2048, N 1024 to 4096, K 1408 to 8192; 1 to 6 slices) per type: within 5 %
+// (fp16, bf16) and 8 % (8 bits) of the measured times.  An item (a tile or a K
+// slice of one) takes its K tiles times tk plus an epilogue of e0 + e1 * area
+// (in 256x256 tiles); rounds of items fill the compute units.  128x128 tiles
+// of which two share a compute unit take tk_pair together.  Slices add a
+// second launch, `join` us and their partial sums at bw TB/s.
+struct LinearCost {
+  double start, join, bw, e0, e1;
+  double tk256, tk192, tk128, tk_small, tk_pair;
+};
+constexpr LinearCost kCost16 = {0.5, 2.9, 9.4, 2.8, 7.2, 1.02, 0.81, 0.72, 0.54, 0.755};
+constexpr LinearCost kCostE4m3 = {3.5, 4.0, 7.6, 3.9, 3.4, 1.13, 0.76, 0.55, 0.31, 0.31};
+constexpr LinearCost kCostI8 = {4.35, 4.0, 7.7, 1.3, 5.1, 1.09, 0.84, 0.76, 0.56, 0.78};
+
+// Tiles of variant v: the first whole, the last `tail` in K slices of `kslice`.
+struct LinearCut {
+  int64_t tiles_m, tiles_n, tiles, tail, kslice;
+  int splits;
+  int64_t items() const { return tiles - tail + tail * splits; }
+};
+
+// all: every tile in slices; else those that whole rounds leave over.
+LinearCut cut_linear(const LinearVariant& v, const gemm_epi_linear_desc& d, int64_t splits, bool all, int64_t cus) {
+  LinearCut c;
+  const int64_t ktiles = (d.K + v.bk - 1) / v.bk;
+  c.tiles_m = (d.M + v.bm - 1) / v.bm;
+  c.tiles_n = (d.N + v.bn - 1) / v.bn;
+  c.tiles = c.tiles_m * c.tiles_n;
+  splits = std::max<int64_t>(1, std::min(splits, ktiles));
+  c.kslice = (ktiles + splits - 1) / splits * v.bk;
+  c.splits = (int)((d.K + c.kslice - 1) / c.kslice);
+  c.tail = c.splits == 1 ? 0 : all ? c.tiles : c.tiles % (cus * v.occ);
+  if (c.tail == 0) c.splits = 1, c.kslice = d.K;
+  return c;
+}
+
+double linear_time(const LinearVariant& v, const LinearCut& c, const gemm_epi_linear_desc& d, int64_t cus) {
+  const LinearCost& w = v.ab == T_E4M3 ? kCostE4m3 : v.ab == T_I8 ? kCostI8 : kCost16;
+  const double area = (double)v.bm * v.bn / 65536.0, epi = w.e0 + w.e1 * area;
+  auto rounds = [&](int64_t items, int64_t k) {
+    if (items == 0) return 0.0;
+    double tk = v.bm == 256 ? w.tk256 : v.bm == 192 ? w.tk192 : v.bn == 256 ? w.tk128 : w.tk_small;
+    int64_t slots = cus;
+    if (v.occ == 2 && items > cus) tk = w.tk_pair, slots = 2 * cus;
+    return (double)((items + slots - 1) / slots) * (tk * (double)((k + v.bk - 1) / v.bk) + epi);
+  };
+  double t = w.start + rounds(c.tiles - c.tail, d.K) + rounds(c.tail * c.splits, std::min(c.kslice, d.K));
+  if (c.tail) t += w.join + (double)c.tail * v.bm * v.bn * 4.0 * (2 * c.splits + 1) / (w.bw * 1e6);
+  return t;
+}
 
 typedef void (*part_fn)(int, const LinParams&, int, hipStream_t);
 const part_fn kParts[kLinearParts] = {launch_linear_part<0>, launch_linear_part<1>, launch_linear_part<2>,
@@ -64,7 +116,7 @@ bool flag_ok(int f) { return f == 0 || f == 1; }
 struct gemm_epi_linear_handle {
   gemm_epi_linear_desc d;  // strides filled in
   int variant, device, cus, grid;
-  int nb, rb;              // few rows: token and weight blocks
+  int nw;                  // few rows: waves per workgroup
   int64_t tiles_m, tiles_n, tiles, tail, kslice, items;
   int splits, group_m;
   bool widen;              // e4m3 runs as fp16 copies
@@ -122,31 +174,18 @@ extern "C" int gemm_epi_linear_create_variant(const gemm_epi_linear_desc* desc, 
   rc = device_query(&device, &cus);
   if (rc) return rc;
 
-  const PlanProblem pp{d.M, d.N, d.K, 1, (double)elem_bytes(d.d_dtype) * (1 + d.residual + d.z), true};
-  auto find_tile = [&](int bm, int bn) {
-    for (int i = 0; i < kTiles; ++i)
-      if (kLinear[i].bm == bm && kLinear[i].bn == bn && kLinear[i].ab == kernel_ab) return i;
-    return -1;
-  };
-  auto model = [&](int i) { return split_choice(kLinear[i].bm, kLinear[i].bn, kLinear[i].bk, pp, cus); };
-  if (variant == -1) {
-    if (d.M <= kRowsMax) {
-      variant = kRowsVariant;
-    } else {
-      // the GEMM plan's rule (gemm_epi_create) on the same tile shapes
-      variant = find_tile(256, 256);
-      const int64_t big = ((d.M + 255) / 256) * ((d.N + 255) / 256);
-      if (d.splits == 0 && big * 4 <= cus) {
-        variant = find_tile(128, 128);
-      } else if (d.splits == 0 && big % cus != 0) {
-        double best = 0.95 * model(variant).us;
-        for (const int cand : {find_tile(192, 256), find_tile(128, 256)}) {
-          const double t = model(cand).us;
-          if (t < best) {
-            best = t;
-            variant = cand;
-          }
-        }
+  LinearCut best = {};
+  if (variant == -1 && d.M <= kRowsMax) variant = kRowsVariant;
+  if (variant != kRowsVariant) {
+    // the tile shape and K split of the lowest modelled time
+    const int forced = variant;
+    double best_us = 0.0;
+    for (int i = 0; i < kTiles; ++i) {
+      if (kLinear[i].ab != kernel_ab || (forced != -1 && i != forced)) continue;
+      for (int64_t s = d.splits ? d.splits : 1; s <= (d.splits ? d.splits : 16); ++s) {
+        const LinearCut c = cut_linear(kLinear[i], d, s, d.splits != 0, cus);
+        const double us = linear_time(kLinear[i], c, d, cus);
+        if (variant == -1 || best.tiles == 0 || us < best_us) best_us = us, best = c, variant = i;
       }
     }
   }
@@ -159,44 +198,31 @@ extern "C" int gemm_epi_linear_create_variant(const gemm_epi_linear_desc* desc, 
   h->cus = cus;
   h->splits = 1;
   if (variant == kRowsVariant) {
-    h->nb = d.M <= 16 ? 1 : d.M <= 32 ? 2 : 4;
-    // two weight blocks halve the token traffic per weight byte, once there
-    // are workgroups for every compute unit
-    h->rb = (d.N + 31) / 32 >= cus ? 2 : 1;
+    // with more than 8 rows a workgroup of 8 waves takes a compute unit's LDS:
+    // 4 waves once there is more than one workgroup for each (16 e4m3 rows,
+    // K = N: 4096 7.7 us with 4 waves, 7.0 with 8; 8192 15.5 and 16.3)
+    h->nw = d.M <= 8 || (d.N + 15) / 16 <= cus ? 8 : 4;
     h->tiles_m = 1;
-    h->tiles_n = (d.N + 16 * h->rb - 1) / (16 * h->rb);
+    h->tiles_n = (d.N + 15) / 16;
     h->tiles = h->items = h->tiles_n;
     h->grid = (int)h->tiles_n;
     *out = h;
     return GEMM_EPI_OK;
   }
   const LinearVariant& v = kLinear[variant];
-  h->tiles_m = (d.M + v.bm - 1) / v.bm;
-  h->tiles_n = (d.N + v.bn - 1) / v.bn;
-  h->tiles = h->tiles_m * h->tiles_n;
+  h->tiles_m = best.tiles_m;
+  h->tiles_n = best.tiles_n;
+  h->tiles = best.tiles;
   h->group_m = h->tiles_n > 32 ? 8 : 4;
-  const int64_t ktiles = (d.K + v.bk - 1) / v.bk;
-  int64_t splits = 1;
-  if (d.splits >= 1) {
-    splits = std::min<int64_t>(d.splits, ktiles);
-    h->tail = h->tiles;
-  } else {
-    const SplitChoice c = model(variant);
-    splits = c.splits;
-    h->tail = c.tail;
-  }
-  h->kslice = ((ktiles + splits - 1) / splits) * v.bk;
-  h->splits = (int)((d.K + h->kslice - 1) / h->kslice);
-  if (h->splits == 1) {
-    h->kslice = d.K;
-    h->tail = 0;
-  }
-  h->items = h->tiles - h->tail + h->tail * h->splits;
+  h->splits = best.splits;
+  h->kslice = best.kslice;
+  h->tail = best.tail;
+  h->items = best.items();
   if (h->tiles >= (int64_t(1) << 31) || h->items >= (int64_t(1) << 31)) {
     delete h;
     return fail(GEMM_EPI_ERR_UNSUPPORTED, "2^31 or more work items (tiles and K slices)");
   }
-  h->grid = (int)std::min<int64_t>(h->items, cus);
+  h->grid = (int)std::min<int64_t>(h->items, (int64_t)cus * v.occ);
   h->ws_bytes = h->splits > 1 ? h->splits * h->tail * v.bm * v.bn * 4 : 0;
   h->widen = widened;
   h->prep_off = up256(h->ws_bytes);
@@ -254,7 +280,7 @@ extern "C" int gemm_epi_linear_run(const gemm_epi_linear_handle* h, const void* 
   hipStream_t s = (hipStream_t)stream;
   (void)hipGetLastError();  // clear a stale error so the checks below are ours
   if (h->variant == kRowsVariant) {
-    launch_linear_rows(d.ab_dtype, h->nb, h->rb, p, s);
+    launch_linear_rows(d.ab_dtype, h->nw, p, s);
     return launched();
   }
   const LinearVariant& v = kLinear[h->variant];
@@ -299,10 +325,9 @@ extern "C" int gemm_epi_linear_get_plan(const gemm_epi_linear_handle* h, gemm_ep
   std::memset(out, 0, sizeof *out);
   out->variant = h->variant;
   if (h->variant == kRowsVariant) {
-    out->tile_m = 16 * h->nb;
-    out->tile_n = 16 * h->rb;
-    out->threads = kRowsThreads;
-    out->lds_bytes = kRowsThreads * h->nb * h->rb * 16;
+    out->tile_m = kRowsMax;
+    out->tile_n = 16;
+    out->threads = h->nw * 64;
   } else {
     const LinearVariant& v = kLinear[h->variant];
     out->tile_m = v.bm;
@@ -331,12 +356,58 @@ extern "C" const char* gemm_epi_linear_variant_name(int variant) {
 // ---------------------------------------------------------------------------
 // Backward
 // ---------------------------------------------------------------------------
+namespace {
+
+// One product of the backward: M x N over K in tile x tile tiles.
+struct GradProduct {
+  bool on = false;
+  int64_t M = 0, N = 0, K = 0;
+  int64_t tiles_m = 0, tiles_n = 0, tiles = 0, kslice = 0;
+  int splits = 1;
+  int64_t items() const { return on ? tiles * splits : 0; }
+  int64_t slots(int tile) const { return on && splits > 1 ? tiles * splits * tile * tile * 4 : 0; }
+};
+
+constexpr int kGradKTile = 64;
+
+void cut(GradProduct* p, int tile, int64_t splits) {
+  if (!p->on) return;
+  const int64_t ktiles = (p->K + kGradKTile - 1) / kGradKTile;
+  p->tiles_m = (p->M + tile - 1) / tile;
+  p->tiles_n = (p->N + tile - 1) / tile;
+  p->tiles = p->tiles_m * p->tiles_n;
+  splits = std::max<int64_t>(1, std::min(splits, ktiles));
+  p->kslice = (ktiles + splits - 1) / splits * kGradKTile;
+  p->splits = (int)((p->K + p->kslice - 1) / p->kslice);
+}
+
+// Modelled time (us) of the launch and the join.  A K tile takes 1.2 us with
+// 256x256 tiles and 0.75 us with 128x128 ones (two workgroups per compute
+// unit, together), an item 3 us besides.
+double grad_time(const GradProduct& a, const GradProduct& b, int tile, int cus) {
+  const double tk = tile == 256 ? 1.2 : 0.75;
+  const double slots = (double)cus * grad_occ(tile);
+  double longest = 0.0, total = 0.0, join = 0.0;
+  for (const GradProduct* p : {&a, &b}) {
+    if (!p->on) continue;
+    const double item = 3.0 + tk * (double)((std::min(p->kslice, p->K) + kGradKTile - 1) / kGradKTile);
+    longest = std::max(longest, item);
+    total += item * (double)p->items();
+    if (p->splits > 1) join = std::max(join, 4.0) + 2.0 * (double)p->slots(tile) / 5.0e6;
+  }
+  const double t = (double)(a.items() + b.items()) <= slots ? longest : total / slots + 0.5 * longest;
+  return t + join;
+}
+
+}  // namespace
+
 struct gemm_epi_linear_grad_handle {
   gemm_epi_linear_grad_desc d;
-  int device;
-  int chunk;                          // rows per partial column sum
-  int64_t partial_bytes, ws_bytes;    // the products' workspace follows the partial sums
-  gemm_epi_handle *da = nullptr, *db = nullptr;
+  int device, cus;
+  int chunk;       // rows per partial column sum
+  int tile;
+  GradProduct a, b;  // dA, dB
+  int64_t ws_a, ws_b, ws_bytes;  // workspace: partial sums, then a's and b's slices
 };
 
 extern "C" int gemm_epi_linear_grad_create(const gemm_epi_linear_grad_desc* desc, gemm_epi_linear_grad_handle** out) {
@@ -358,50 +429,61 @@ extern "C" int gemm_epi_linear_grad_create(const gemm_epi_linear_grad_desc* desc
       return fail(GEMM_EPI_ERR_INVALID_ARG, "a gradient's type must be NONE, F16, BF16 or F32");
   if (d.da_dtype == GEMM_EPI_NONE && d.db_dtype == GEMM_EPI_NONE && d.dbias_dtype == GEMM_EPI_NONE)
     return fail(GEMM_EPI_ERR_INVALID_ARG, "no gradient is wanted");
-  int64_t mn, t;
-  if (!mul_ok(d.M, d.N, &mn) || !mul_ok(mn, 4, &t))
-    return fail(GEMM_EPI_ERR_INVALID_ARG, "tensor byte sizes overflow int64");
-  if (d.N % 8) return fail(GEMM_EPI_ERR_ALIGNMENT, "rows of dD (%lld elements) must be multiples of 16 bytes",
-                           (long long)d.N);
-  if (d.N >= (int64_t(1) << 31) - 512)
-    return fail(GEMM_EPI_ERR_UNSUPPORTED, "N must be below 2^31 - 512");
+  if (d.tile != 0 && d.tile != 128 && d.tile != 256)
+    return fail(GEMM_EPI_ERR_INVALID_ARG, "tile must be 0, 128 or 256 (got %d)", d.tile);
+  if (d.splits < 0) return fail(GEMM_EPI_ERR_INVALID_ARG, "splits must be >= 0 (got %d)", d.splits);
+  const bool da = d.da_dtype != GEMM_EPI_NONE, db = d.db_dtype != GEMM_EPI_NONE;
+  // every extent below 2^31 - 512 first, so that no product below overflows
+  const int64_t most = (int64_t(1) << 31) - 512;
+  if (d.M >= most || d.N >= most || d.K >= most)
+    return fail(GEMM_EPI_ERR_UNSUPPORTED, "M, N and K must be below 2^31 - 512");
+  if (d.N % 8 || ((da || db) && d.K % 8))
+    return fail(GEMM_EPI_ERR_ALIGNMENT, "rows of dD (%lld elements) and of A and B (%lld) must be multiples of 16 bytes",
+                (long long)d.N, (long long)d.K);
+  // 256 rows of an output or a K-major operand, and a whole operand that is
+  // read across its rows, are addressed with 31-bit byte offsets
+  if ((da || db) && (d.K * 4 * 256 > INT32_MAX || d.N * 4 * 256 > INT32_MAX))
+    return fail(GEMM_EPI_ERR_UNSUPPORTED, "rows too long for 31-bit tile offsets");
+  const int64_t pad = 2 * kGradKTile;
+  if ((da && (d.N + pad) * d.K * 2 > INT32_MAX) ||
+      (db && ((d.M + pad) * d.N * 2 > INT32_MAX || (d.M + pad) * d.K * 2 > INT32_MAX)))
+    return fail(GEMM_EPI_ERR_UNSUPPORTED, "an operand read across its rows is 2 GiB or larger");
+  int device = 0, cus = 0;
+  const int rc = device_query(&device, &cus);
+  if (rc) return rc;
 
   gemm_epi_linear_grad_handle* h = new (std::nothrow) gemm_epi_linear_grad_handle();
   if (!h) return fail(GEMM_EPI_ERR_HOST_ALLOC, "out of host memory");
   h->d = d;
+  h->device = device;
+  h->cus = cus;
   // 64 rows per partial sum; more where 2^16 chunks would not do (the grid's
   // second dimension)
-  const int64_t chunk = std::max<int64_t>(64, (d.M + 65534) / 65535);
-  int rc = GEMM_EPI_OK;
-  if (chunk >= (int64_t(1) << 30)) rc = fail(GEMM_EPI_ERR_UNSUPPORTED, "M is too large");
-  h->chunk = (int)chunk;
-  int64_t products = 0;
-  gemm_epi_desc g = {};
-  g.L = 1;
-  g.ab_dtype = d.ab_dtype;
-  g.cd_major = GEMM_EPI_MAJOR_N;
-  if (!rc && d.da_dtype != GEMM_EPI_NONE) {  // M x K over N: B holds its columns contiguous
-    g.M = d.M, g.N = d.K, g.K = d.N;
-    g.a_major = GEMM_EPI_MAJOR_K, g.b_major = GEMM_EPI_MAJOR_N;
-    g.c_dtype = GEMM_EPI_NONE, g.d_dtype = d.da_dtype;
-    rc = gemm_epi_create(&g, &h->da);
-    if (!rc) products = std::max(products, handle_workspace(h->da));
+  h->chunk = (int)std::max<int64_t>(64, (d.M + 65534) / 65535);
+  h->a.on = da;
+  h->a.M = d.M, h->a.N = d.K, h->a.K = d.N;
+  h->b.on = db;
+  h->b.M = d.N, h->b.N = d.K, h->b.K = d.M;
+  double best = 0.0;
+  for (const int tile : {256, 128}) {
+    if (d.tile != 0 && d.tile != tile) continue;
+    for (int64_t sa = 1; sa <= (da && !d.splits ? 16 : 1); ++sa)
+      for (int64_t sb = 1; sb <= (db && !d.splits ? 16 : 1); ++sb) {
+        GradProduct a = h->a, b = h->b;
+        cut(&a, tile, d.splits ? d.splits : sa);
+        cut(&b, tile, d.splits ? d.splits : sb);
+        const double t = grad_time(a, b, tile, cus);
+        if (h->tile == 0 || t < best) best = t, h->tile = tile, h->a = a, h->b = b;
+      }
   }
-  if (!rc && d.db_dtype != GEMM_EPI_NONE) {  // N x K over M: both operands contiguous along their rows
-    g.M = d.N, g.N = d.K, g.K = d.M;
-    g.a_major = GEMM_EPI_MAJOR_M, g.b_major = GEMM_EPI_MAJOR_N;
-    g.c_dtype = d.db_dtype, g.d_dtype = d.db_dtype;
-    rc = gemm_epi_create(&g, &h->db);
-    if (!rc) products = std::max(products, handle_workspace(h->db));
+  if (h->a.items() + h->b.items() + d.N / 32 >= most) {
+    delete h;
+    return fail(GEMM_EPI_ERR_UNSUPPORTED, "2^31 or more work items (tiles and K slices)");
   }
-  int cus = 0;
-  if (!rc) rc = device_query(&h->device, &cus);
-  if (rc) {
-    gemm_epi_linear_grad_destroy(h);
-    return rc;
-  }
-  if (d.dbias_dtype != GEMM_EPI_NONE) h->partial_bytes = up256((d.M + chunk - 1) / chunk * d.N * 4);
-  h->ws_bytes = h->partial_bytes + products;
+  const int64_t chunks = (d.M + h->chunk - 1) / h->chunk;
+  h->ws_a = d.dbias_dtype != GEMM_EPI_NONE && chunks > 1 ? up256(chunks * d.N * 4) : 0;
+  h->ws_b = h->ws_a + h->a.slots(h->tile);
+  h->ws_bytes = h->ws_b + h->b.slots(h->tile);
   *out = h;
   return GEMM_EPI_OK;
 }
@@ -416,9 +498,9 @@ extern "C" int gemm_epi_linear_grad_run(const gemm_epi_linear_grad_handle* h, co
   if (!dD) return fail(GEMM_EPI_ERR_INVALID_ARG, "dD is required");
   if ((Z != nullptr) != act || (dZ != nullptr) != act)
     return fail(GEMM_EPI_ERR_INVALID_ARG, "Z and dZ must be given exactly with an activation");
-  if ((dA != nullptr) != (h->da != nullptr) || (B != nullptr) != (h->da != nullptr))
+  if ((dA != nullptr) != h->a.on || (B != nullptr) != h->a.on)
     return fail(GEMM_EPI_ERR_INVALID_ARG, "dA and B must be given exactly when da_dtype is set");
-  if ((dB != nullptr) != (h->db != nullptr) || (A != nullptr) != (h->db != nullptr) || (dB_in && !dB))
+  if ((dB != nullptr) != h->b.on || (A != nullptr) != h->b.on || (dB_in && !dB))
     return fail(GEMM_EPI_ERR_INVALID_ARG, "dB and A (and dB_in) must be given exactly when db_dtype is set");
   if ((dbias != nullptr) != (d.dbias_dtype != GEMM_EPI_NONE))
     return fail(GEMM_EPI_ERR_INVALID_ARG, "dbias must be given exactly when dbias_dtype is set");
@@ -441,28 +523,65 @@ extern "C" int gemm_epi_linear_grad_run(const gemm_epi_linear_grad_handle* h, co
   if (rc) return rc;
 
   hipStream_t s = (hipStream_t)stream;
-  float* partial = dbias ? (float*)workspace : nullptr;
-  void* products = (char*)workspace + h->partial_bytes;
+  const int64_t chunks = (d.M + h->chunk - 1) / h->chunk;
+  float* partial = dbias && chunks > 1 ? (float*)workspace : nullptr;
   (void)hipGetLastError();  // clear a stale error so the checks below are ours
-  if (act || partial) {
-    launch_linear_dact(d.ab_dtype, d.act, dD, Z, dZ, partial, d.M, d.N, h->chunk, s);
+  if (act || dbias) {
+    launch_linear_dact(d.ab_dtype, d.act, dD, Z, dZ, partial, dbias, d.dbias_dtype, d.M, d.N, h->chunk, s);
     rc = launched();
-    if (!rc && partial) {
-      launch_colsum(partial, (d.M + h->chunk - 1) / h->chunk, d.N, dbias, d.dbias_dtype, s);
-      rc = launched();
-    }
+    if (rc) return rc;
+  }
+  if (!dA && !dB) {
+    if (partial) launch_colsum(partial, chunks, d.N, dbias, d.dbias_dtype, s);
+    return launched();
   }
   const void* g = act ? dZ : dD;
-  if (!rc && dA) rc = run_with_workspace(h->da, g, B, nullptr, dA, 0.0f, products, stream);
-  if (!rc && dB) rc = run_with_workspace(h->db, g, A, dB_in, dB, dB_in ? 1.0f : 0.0f, products, stream);
-  return rc;
+  GradParams p = {};
+  auto product = [&](LinParams* q, const GradProduct& w, const void* qa, const void* qb, const void* add, void* qd,
+                     int type, int64_t ws) {
+    q->A = qa;
+    q->B = qb;
+    q->D = qd;
+    q->R = add;
+    q->M = w.M;
+    q->N = w.N;
+    q->K = w.K;
+    q->lda = w.K;  // (of a K-major A; the other operands are packed)
+    q->ldd = q->ldr = q->ldz = w.N;
+    q->alpha = 1.0f;
+    q->d_dtype = type;
+    q->tiles_total = (int32_t)w.items();
+    q->L = 1;
+    q->tiles_m = (int32_t)w.tiles_m;
+    q->tiles_n = (int32_t)w.tiles_n;
+    q->group_m = w.tiles_n > 32 ? 8 : 4;
+    q->xcd_remap = w.items() % 8 == 0 ? 1 : 0;
+    q->splits = w.splits;
+    q->kslice = w.kslice;
+    q->tail_tiles = w.splits > 1 ? (int32_t)w.tiles : 0;
+    q->dp_tiles = (int32_t)w.tiles - q->tail_tiles;
+    q->ws = (char*)workspace + ws;
+  };
+  if (dA) product(&p.a, h->a, g, B, nullptr, dA, d.da_dtype, h->ws_a);
+  if (dB) product(&p.b, h->b, g, A, dB_in, dB, d.db_dtype, h->ws_b);
+  p.ga = p.a.tiles_total;
+  p.gb = p.b.tiles_total;
+  p.partial = partial;
+  p.P = chunks;
+  p.C = d.N;
+  p.dbias = dbias;
+  p.dbias_dtype = d.dbias_dtype;
+  if (d.ab_dtype == GEMM_EPI_F16)
+    h->tile == 256 ? launch_linear_grad_mm<T_F16, 256>(p, s) : launch_linear_grad_mm<T_F16, 128>(p, s);
+  else
+    h->tile == 256 ? launch_linear_grad_mm<T_BF16, 256>(p, s) : launch_linear_grad_mm<T_BF16, 128>(p, s);
+  rc = launched();
+  if (rc || (p.a.tail_tiles == 0 && p.b.tail_tiles == 0)) return rc;
+  launch_linear_grad_join(p.a, p.b, h->tile, (int64_t)h->cus * 8, s);
+  return launched();
 }
 
 extern "C" int gemm_epi_linear_grad_destroy(gemm_epi_linear_grad_handle* h) {
-  if (h) {
-    gemm_epi_destroy(h->da);
-    gemm_epi_destroy(h->db);
-  }
   delete h;
   return GEMM_EPI_OK;
 }

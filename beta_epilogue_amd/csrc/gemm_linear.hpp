@@ -27,10 +27,10 @@ struct LinParams : Params {
   int32_t act;           // ACT_*
 };
 
-// Tile kernels: K-major A and B, N-major D, 128-byte rows, 2 x 2 waves, two
+// Tile kernels: K-major A and B, N-major D, 128-byte rows, 2 x 2 waves, S
 // stages, LIN arguments and epilogue.
-template <int AB, int BM, int BN, int BLK>
-using LinearCfg = Cfg<AB, true, true, true, BM, BN, 128, 2, 2, 2, 0, BLK, true>;
+template <int AB, int BM, int BN, int S, int OCC, int BLK>
+using LinearCfg = Cfg<AB, true, true, true, BM, BN, 128, 2, 2, S, 0, BLK, 1, OCC>;
 
 constexpr int kLinearParts = 8;
 // Launches variant number `variant` of gemm_linear_variants.inc (one of part
@@ -38,24 +38,77 @@ constexpr int kLinearParts = 8;
 template <int PART>
 void launch_linear_part(int variant, const LinParams& p, int grid, hipStream_t s);
 
+// The backward's products, one launch for both:
+//   a: dA = dZ . B  (M x K over N: A = dZ K-major, B = B N-major)
+//   b: dB = dB_in + dZ^T . A  (N x K over M: A = dZ M-major, B = A N-major)
+// Workgroups 0 .. ga-1 run a, the next gb run b, the rest add the chunks'
+// column sums of dZ into dbias.  A problem that is not wanted has 0.
+constexpr int grad_occ(int tile) { return tile == 256 ? 1 : 2; }  // workgroups per compute unit
+template <int AB, int TILE>
+using GradCfgA = Cfg<AB, true, false, true, TILE, TILE, 128, 2, 2, 2, TILE == 256 ? 2 : 0, 32, 2, grad_occ(TILE)>;
+template <int AB, int TILE>
+using GradCfgB = Cfg<AB, false, false, true, TILE, TILE, 128, 2, 2, 2, TILE == 256 ? 2 : 0, 32, 2, grad_occ(TILE)>;
+struct GradParams {
+  LinParams a, b;
+  int32_t ga, gb;
+  const float* partial;  // [P][C], or NULL
+  int64_t P, C;
+  void* dbias;
+  int32_t dbias_dtype;
+};
+// TILE x TILE tiles (128 or 256) of type AB (T_F16 or T_BF16).
+template <int AB, int TILE>
+void launch_linear_grad_mm(const GradParams& p, hipStream_t s);
+
+// Adds the slices of split tiles of both products (tail_tiles 0: none).
+void launch_linear_grad_join(const LinParams& a, const LinParams& b, int tile, int64_t most_blocks, hipStream_t s);
+
 // The second kernel of a split-K plan: adds the slices' partial sums in slice
 // order and applies the epilogue.  int_path: int32 partial sums.
 void launch_linear_splitk(const LinParams& p, int tile_m, int tile_n, bool int_path, int grid, hipStream_t s);
 
-// Few rows: M <= 16 * nb (nb 1, 2 or 4); rb blocks of 16 weight rows per
-// workgroup (1 or 2).  ab: T_F16, T_BF16, T_E4M3 or T_I8.
+// Few rows: M <= kRowsMax, 16 weight rows per workgroup of nw waves (4 or 8;
+// up to 8 rows always 8).  ab: T_F16, T_BF16, T_E4M3 or T_I8.
 constexpr int kRowsMax = 64;
-void launch_linear_rows(int ab, int nb, int rb, const LinParams& p, hipStream_t s);
+void launch_linear_rows(int ab, int nw, const LinParams& p, hipStream_t s);
 
-// dZ = dD * act'(Z) (skipped with act == ACT_NONE) and, if partial is given,
-// the column sums of each chunk of `chunk` rows into partial[chunk][N].
-// Packed M x N tensors of type t (T_F16 or T_BF16), N a multiple of 8.
-void launch_linear_dact(int t, int act, const void* dD, const void* Z, void* dZ, float* partial, int64_t M, int64_t N,
-                        int chunk, hipStream_t s);
+// dZ = dD * act'(Z) (skipped with act == ACT_NONE) and, if wanted, the column
+// sums: of each chunk of `chunk` rows into partial[chunk][N], or with one chunk
+// straight into dbias (partial NULL).  Packed M x N tensors of type t (T_F16
+// or T_BF16), N a multiple of 8.
+void launch_linear_dact(int t, int act, const void* dD, const void* Z, void* dZ, float* partial, void* dbias,
+                        int dbias_dtype, int64_t M, int64_t N, int chunk, hipStream_t s);
 
-// out[c] = sum over p < P of partial[p][c], in a fixed order (a tree over 32
-// interleaved strands of ascending p), rounded to type t.
+// out[c] = sum over p < P of partial[p][c], in a fixed order (a tree over
+// strands of ascending p), rounded to type t.
 void launch_colsum(const float* partial, int64_t P, int64_t C, void* out, int t, hipStream_t s);
+
+__device__ __forceinline__ void store_as(void* out, int64_t i, int t, float v) {
+  if (t == T_F32) ((float*)out)[i] = v;
+  else if (t == T_F16) ((_Float16*)out)[i] = (_Float16)v;
+  else ((__bf16*)out)[i] = (__bf16)v;
+}
+
+// 32 columns per workgroup of 32 * STRANDS threads; red: STRANDS x 33 words.
+template <int STRANDS>
+__device__ __forceinline__ void colsum_block(const float* partial, int64_t P, int64_t C, void* out, int t,
+                                             int64_t block, float* red) {
+  const int cl = threadIdx.x & 31, pl = threadIdx.x >> 5;
+  const int64_t c = block * 32 + cl;
+  float s = 0.0f;
+  if (c < C) {
+#pragma unroll 8
+    for (int64_t p = pl; p < P; p += STRANDS) s += partial[p * C + c];
+  }
+  red[pl * 33 + cl] = s;
+  __syncthreads();
+#pragma unroll
+  for (int d = STRANDS / 2; d >= 1; d >>= 1) {
+    if (pl < d) red[pl * 33 + cl] += red[(pl + d) * 33 + cl];
+    __syncthreads();
+  }
+  if (pl == 0 && c < C) store_as(out, c, t, red[cl]);
+}
 
 }  // namespace gemm_epi
 

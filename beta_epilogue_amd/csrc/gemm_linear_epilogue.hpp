@@ -2,6 +2,7 @@
 // accumulator tile (included by gemm_linear.hpp):
 //   z = alpha * scale_a[m] * scale_b[n] * acc + bias[n]
 //   Z = z (if kept),  D = act(z) + R
+// (LIN 2: D = acc + R)
 // in fp32 on the unrounded accumulator (int32 sums are converted first),
 // rounded to nearest-even into the type T that D, R and Z share.
 //
@@ -56,7 +57,7 @@ __device__ __forceinline__ void epilogue_linear(const LinParams& p, const ACC (&
   auto fetch = [&](int pass, auto u_c) {
     constexpr int u = decltype(u_c)::value;
     if (p.R) res[u] = epi_ld<T>(rr, orr + (uint32_t)pass * sr);
-    if (p.scale_a)
+    if (CF::LIN_ACT && p.scale_a)
       sa[u] = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rsa, (pass * LPP + sub) * 4, 0, 0));
   };
   static_for<0, UN>([&](auto u_c) {
@@ -69,7 +70,7 @@ __device__ __forceinline__ void epilogue_linear(const LinParams& p, const ACC (&
   float bias[VEC], cs[VEC];
 #pragma unroll
   for (int i = 0; i < VEC; ++i) bias[i] = 0.0f, cs[i] = p.alpha;
-  if (lane_ok) {
+  if (CF::LIN_ACT && lane_ok) {
     if (p.scale_b) {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) cs[i] = p.alpha * p.scale_b[along + i];
@@ -109,13 +110,13 @@ __device__ __forceinline__ void epilogue_linear(const LinParams& p, const ACC (&
       const float s = sa[u];
       if (pass + UN < NP) fetch(pass + UN, u_c);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) v[i] = __builtin_fmaf(v[i], s * cs[i], bias[i]);
+      for (int i = 0; CF::LIN_ACT && i < VEC; ++i) v[i] = __builtin_fmaf(v[i], s * cs[i], bias[i]);
       auto pack = [&](const float (&x)[VEC]) {
         return epi_pack<T>(v4f{x[0], x[1], x[2], x[3]},
                            VEC == 8 ? v4f{x[VEC - 4], x[VEC - 3], x[VEC - 2], x[VEC - 1]} : v4f{});
       };
-      if (p.Z) epi_st<T>(rz, oz + (uint32_t)pass * sz, pack(v));
-      with_act(p.act, [&](auto act_c) {
+      if (CF::LIN_ACT && p.Z) epi_st<T>(rz, oz + (uint32_t)pass * sz, pack(v));
+      if constexpr (CF::LIN_ACT) with_act(p.act, [&](auto act_c) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) v[i] = act_value<decltype(act_c)::value>(v[i]);
       });

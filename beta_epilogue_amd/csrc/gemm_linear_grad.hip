@@ -1,5 +1,5 @@
 // gemm_linear_grad.hip -- the linear layer's backward outside its two matrix
-// products (which the GEMM kernels run: dA = dZ . B, dB = dZ^T . A):
+// products (gemm_linear_grad_mm.hip):
 //   dZ = dD * act'(Z), rounded to the operands' type (the MFMA reads it), and
 //   dbias[n] = sum over m of dZ[m][n], summed in fp32 before that rounding.
 // One pass reads dD and Z and writes dZ, with the column sums on the way:
@@ -23,7 +23,8 @@ __device__ __forceinline__ void decode8(v4u r, float (&v)[8]) {
 // HAS_Z: dZ is computed and stored; else dZ is dD and only summed.
 template <int T, bool HAS_Z>
 __global__ __launch_bounds__(256) void linear_dact_kernel(const uint16_t* dD, const uint16_t* Z, uint16_t* dZ,
-                                                          float* partial, int64_t M, int64_t N, int chunk, int act) {
+                                                          float* partial, void* dbias, int dbias_dtype, int64_t M,
+                                                          int64_t N, int chunk, int act) {
   __shared__ float red[8][256 + 4];
   const int cl = threadIdx.x & 31, rl = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 256 + cl * 8;
@@ -48,7 +49,7 @@ __global__ __launch_bounds__(256) void linear_dact_kernel(const uint16_t* dD, co
       }
     });
   }
-  if (!partial) return;
+  if (!partial && !dbias) return;
 #pragma unroll
   for (int k = 0; k < 8; ++k) red[rl][cl * 8 + k] = sum[k];
   __syncthreads();
@@ -57,51 +58,33 @@ __global__ __launch_bounds__(256) void linear_dact_kernel(const uint16_t* dD, co
   float s = 0.0f;
 #pragma unroll
   for (int k = 0; k < 8; ++k) s += red[k][threadIdx.x];
-  partial[(int64_t)blockIdx.y * N + n] = s;
+  if (partial) partial[(int64_t)blockIdx.y * N + n] = s;
+  else store_as(dbias, n, dbias_dtype, s);
 }
 
-// 32 columns by 32 strands of p per workgroup.
 __global__ __launch_bounds__(1024) void colsum_kernel(const float* partial, int64_t P, int64_t C, void* out, int t) {
-  __shared__ float red[32][33];
-  const int cl = threadIdx.x & 31, pl = threadIdx.x >> 5;
-  const int64_t c = (int64_t)blockIdx.x * 32 + cl;
-  float s = 0.0f;
-  if (c < C) {
-#pragma unroll 8
-    for (int64_t p = pl; p < P; p += 32) s += partial[p * C + c];
-  }
-  red[pl][cl] = s;
-  __syncthreads();
-#pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) {
-    if (pl < d) red[pl][cl] += red[pl + d][cl];
-    __syncthreads();
-  }
-  if (pl == 0 && c < C) {
-    if (t == T_F32) ((float*)out)[c] = red[0][cl];
-    else if (t == T_F16) ((_Float16*)out)[c] = (_Float16)red[0][cl];
-    else ((__bf16*)out)[c] = (__bf16)red[0][cl];
-  }
+  __shared__ float red[32 * 33];
+  colsum_block<32>(partial, P, C, out, t, blockIdx.x, red);
 }
 
 template <int T>
-void dact(int act, const void* dD, const void* Z, void* dZ, float* partial, int64_t M, int64_t N, int chunk,
-          hipStream_t s) {
+void dact(int act, const void* dD, const void* Z, void* dZ, float* partial, void* dbias, int dbias_dtype, int64_t M,
+          int64_t N, int chunk, hipStream_t s) {
   const dim3 grid((unsigned)((N + 255) / 256), (unsigned)((M + chunk - 1) / chunk));
   if (act != ACT_NONE)
     hipLaunchKernelGGL((linear_dact_kernel<T, true>), grid, dim3(256), 0, s, (const uint16_t*)dD, (const uint16_t*)Z,
-                       (uint16_t*)dZ, partial, M, N, chunk, act);
+                       (uint16_t*)dZ, partial, dbias, dbias_dtype, M, N, chunk, act);
   else
     hipLaunchKernelGGL((linear_dact_kernel<T, false>), grid, dim3(256), 0, s, (const uint16_t*)dD, nullptr, nullptr,
-                       partial, M, N, chunk, act);
+                       partial, dbias, dbias_dtype, M, N, chunk, act);
 }
 
 }  // namespace
 
-void launch_linear_dact(int t, int act, const void* dD, const void* Z, void* dZ, float* partial, int64_t M, int64_t N,
-                        int chunk, hipStream_t s) {
-  if (t == T_F16) dact<T_F16>(act, dD, Z, dZ, partial, M, N, chunk, s);
-  else dact<T_BF16>(act, dD, Z, dZ, partial, M, N, chunk, s);
+void launch_linear_dact(int t, int act, const void* dD, const void* Z, void* dZ, float* partial, void* dbias,
+                        int dbias_dtype, int64_t M, int64_t N, int chunk, hipStream_t s) {
+  if (t == T_F16) dact<T_F16>(act, dD, Z, dZ, partial, dbias, dbias_dtype, M, N, chunk, s);
+  else dact<T_BF16>(act, dD, Z, dZ, partial, dbias, dbias_dtype, M, N, chunk, s);
 }
 
 void launch_colsum(const float* partial, int64_t P, int64_t C, void* out, int t, hipStream_t s) {

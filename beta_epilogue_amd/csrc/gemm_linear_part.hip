@@ -21,7 +21,7 @@ void launch_if(bool wanted, const LinParams& p, int grid, hipStream_t s) {
 template <>
 void launch_linear_part<GEMM_LINEAR_PART>(int variant, const LinParams& p, int grid, hipStream_t s) {
   int i = 0;
-#define X(PART, AB, BM, BN, BL, NAME) launch_if<PART, LinearCfg<AB, BM, BN, BL>>(variant == i++, p, grid, s);
+#define X(PART, AB, BM, BN, S, OCC, BL, NAME) launch_if<PART, LinearCfg<AB, BM, BN, S, OCC, BL>>(variant == i++, p, grid, s);
 #include "gemm_linear_variants.inc"
 #undef X
 }

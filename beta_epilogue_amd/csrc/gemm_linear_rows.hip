@@ -3,17 +3,20 @@
 //
 // Few rows: D is M x N with M <= 64, so the time is the weight's: every byte
 // of B is read once and meets at most 64 tokens.  The MFMA's roles are turned
-// round: 16 (RB times) weight rows are the matrix core's rows, the tokens
-// (NB blocks of 16) its columns, so one weight fragment loaded from memory
-// feeds NB instructions.  Fragments go from global memory straight into
-// registers (a lane's 16 bytes are 16 / ES consecutive k of one row, the four
-// lane groups cover 64 consecutive bytes of each row): nothing of B is used
-// twice by a workgroup, so LDS would only add a copy.  The eight waves of a
-// workgroup split K in interleaved segments (each reads U * 64 bytes of a row
-// at a time, eight waves together a contiguous run) and join through LDS in
-// wave order; the token fragments come from L2, where all workgroups read the
-// same M x K.  e4m3 is widened to fp16 in registers (exact), so every type
-// has exact products and fp32 (int32) sums.
+// round: 16 weight rows are the matrix core's rows and the tokens (NB blocks of
+// 16) its columns, so a weight fragment feeds NB instructions.
+//
+// What bounds it is how the weights arrive.  Read straight into fragments (16
+// rows, 64 bytes each, per load) they come at 4.4 TB/s; the kernel has them
+// arrive in LDS by DMA in runs of 256 bytes per row, into a ring that belongs
+// to one wave, so waves never wait for one another: 5.1 TB/s for bf16 with one
+// token and K = N = 8192 (26.1 us; 30.8 before; runs of 512 and 1024 bytes are
+// 5 to 15 % slower, for each wave then has fewer rows in flight).  The tokens
+// take the same way.  The waves of a workgroup split K in interleaved runs and
+// join their sums through LDS in wave order.  Sixteen e4m3 tokens at 8192^2
+// take 15.5 us (4.3 TB/s), 64 bf16 ones at 4096^2 14.7 us (tiles: 18 us).
+// e4m3 is widened to fp16 in registers (exact), so every type has exact
+// products and fp32 (int32) sums.
 #include "gemm_linear.hpp"
 
 namespace gemm_epi {
@@ -110,87 +113,122 @@ struct Epi4 {
   }
 };
 
-constexpr int kRowsWaves = 8;
+// The DMA of the weights: as dma16s, with the streaming cache policy.
+template <uint32_t IMM>
+__device__ __forceinline__ void dma16s_nt(v4i rsrc, uint32_t sbase, uint32_t voff, uint32_t soff) {
+  asm volatile(
+      "s_add_u32 m0, %0, %4\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dwordx4 %1, %2, %3 offen nt lds"
+      :
+      : "s"(sbase), "v"(voff), "s"(rsrc), "s"(soff), "i"(IMM)
+      : "memory", "m0", "scc");
+}
 
-template <int AB, int NB, int RB, int U>
-__global__ __launch_bounds__(kRowsWaves * 64) void linear_rows_kernel(LinParams p) {
+// One stage of a wave's ring: 256 bytes of K of 16 weight rows, then of 4 * MB
+// token rows; 1 KiB (four rows) per DMA instruction.  The 16-byte chunk c of
+// row r lies at c ^ (r & 15), so a fragment read (16 rows, one chunk each) hits
+// 16 distinct bank groups.  NW waves, NS stages.
+constexpr int kSeg = 256;
+
+template <int AB, int MB, int NW, int NS>
+__global__ __launch_bounds__(NW * 64) void linear_rows_kernel(LinParams p) {
   using MM = RowsMma<AB>;
   constexpr int ES = AB == T_F16 || AB == T_BF16 ? 2 : 1;
-  __shared__ v4u part[kRowsWaves][RB * NB][64];
+  constexpr int NB = (MB + 3) / 4;               // token blocks of 16
+  constexpr int PER = 4 + MB;                    // DMA instructions (KiB) per stage
+  constexpr int RING = NW * NS * PER * 1024, JOIN = NW * NB * 1024;
+  static_assert(NS * PER < 64, "counted waits");
+  __shared__ __attribute__((aligned(1024))) char lds[RING > JOIN ? RING : JOIN];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * (16 * RB);
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
 
-  // Buffer resources: the workgroup's weight rows, and all tokens.  Rows past
-  // the matrix and bytes past K get an offset outside the extent and read 0.
+  // Rows past the matrix and chunks past K get an offset outside the
+  // resource's extent and arrive as zeros.
   const int64_t lda = p.lda * ES, ldb = p.ldb * ES;
   const uint32_t kbytes = (uint32_t)(p.K * ES);
-  const int brows = (int)min((int64_t)(16 * RB), p.N - n0);
-  const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)((const char*)p.B + n0 * ldb), (short)0, (int)((brows - 1) * ldb + kbytes), 0x00020000);
-  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)p.A, (short)0, (int)((p.M - 1) * lda + kbytes), 0x00020000);
-  uint32_t ob[RB], oa[NB];
+  const int brows = (int)min((int64_t)16, p.N - n0);
+  const v4i rb = make_rsrc((const char*)p.B + n0 * ldb, (uint32_t)((brows - 1) * ldb + kbytes));
+  const v4i ra = make_rsrc(p.A, (uint32_t)((p.M - 1) * lda + kbytes));
+  // DMA lane: row 4 * instruction + q, chunk position r
+  uint32_t ob[4], oa[MB], cb[4];
 #pragma unroll
-  for (int i = 0; i < RB; ++i) ob[i] = i * 16 + r < brows ? (uint32_t)((i * 16 + r) * ldb) : 0x80000000u;
+  for (int i = 0; i < 4; ++i) {
+    cb[i] = (uint32_t)((r ^ (4 * i + q)) * 16);  // logical chunk of row 4 i + q (mod 16)
+    ob[i] = 4 * i + q < brows ? (uint32_t)((4 * i + q) * ldb) + cb[i] : 0x80000000u;
+  }
 #pragma unroll
-  for (int j = 0; j < NB; ++j) oa[j] = j * 16 + r < p.M ? (uint32_t)((j * 16 + r) * lda) : 0x80000000u;
+  for (int i = 0; i < MB; ++i) oa[i] = 4 * i + q < p.M ? (uint32_t)((4 * i + q) * lda) + cb[i & 3] : 0x80000000u;
+  const uint32_t ring = (uint32_t)(uintptr_t)(lds_void_t*)lds + (uint32_t)wave * (NS * PER * 1024);
 
-  // The outputs this wave finishes: block `wave` of the RB * NB (weight
-  // block, token block) pairs; its bias, scales and residual are read ahead.
-  constexpr int PAIRS = RB * NB;
-  static_assert(PAIRS <= kRowsWaves, "a wave finishes at most one block");
-  const int64_t fm = (wave % NB) * 16 + r, fn = n0 + (wave / NB) * 16 + 4 * q;
-  const bool fin = wave < PAIRS && fm < p.M && fn < p.N;
+  // The outputs this wave finishes: token block `wave`, whose bias, scales and
+  // residual are read ahead.
+  static_assert(NB <= NW, "a wave finishes at most one block");
+  const int64_t fm = wave * 16 + r, fn = n0 + 4 * q;
+  const bool fin = wave < NB && fm < p.M && fn < p.N;
   Epi4 epi;
   if (fin) epi.load(p, fm, fn);
 
-  typename MM::acc_t acc[RB][NB];
+  typename MM::acc_t acc[NB];
 #pragma unroll
-  for (int i = 0; i < RB; ++i)
-#pragma unroll
-    for (int j = 0; j < NB; ++j) acc[i][j] = typename MM::acc_t{};
+  for (int j = 0; j < NB; ++j) acc[j] = typename MM::acc_t{};
 
-  for (uint32_t k0 = (uint32_t)wave * (U * 64); k0 < kbytes; k0 += kRowsWaves * U * 64) {
-    v4u fb[U][RB], fa[U][NB];
+  // Segment k (bytes) of every row into stage st.
+  auto issue = [&](int st, uint32_t k) {
+    const uint32_t base = ring + (uint32_t)(st * (PER * 1024));
+    static_for<0, 4>([&](auto i_c) {
+      constexpr int i = decltype(i_c)::value;
+      dma16s_nt<i * 1024u>(rb, base, k + cb[i] < kbytes ? ob[i] + k : 0x80000000u, 0);
+    });
+    static_for<0, MB>([&](auto i_c) {
+      constexpr int i = decltype(i_c)::value;
+      dma16s<(4 + i) * 1024u>(ra, base, k + cb[i & 3] < kbytes ? oa[i] + k : 0x80000000u, 0);
+    });
+  };
+  const uint32_t step = NW * kSeg;
+  uint32_t k = (uint32_t)wave * kSeg;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t k = k0 + u * 64 + q * 16;
-      const bool in = k < kbytes;
+  for (int st = 0; st < NS; ++st) issue(st, k + (uint32_t)st * step);
+  // (segments past K are issued too, without traffic, so the counts hold)
+  int st = 0;
+  for (; k < kbytes; k += step) {
+    wait_vmcnt<(NS - 1) * PER>();
+    asm volatile("" ::: "memory");
+    const char* sb = lds + wave * (NS * PER * 1024) + st * (PER * 1024);
+    v4u fb[4], fa[4][NB];
 #pragma unroll
-      for (int i = 0; i < RB; ++i)
-        fb[u][i] = __builtin_bit_cast(
-            v4u, __builtin_amdgcn_raw_buffer_load_b128(rb, (int)(in ? ob[i] + k : 0x80000000u), 0, EPI_NT));
+    for (int s = 0; s < 4; ++s) {
+      fb[s] = *(const v4u*)(sb + r * kSeg + (((s * 4 + q) ^ r) << 4));
 #pragma unroll
-      for (int j = 0; j < NB; ++j)
-        fa[u][j] = __builtin_bit_cast(
-            v4u, __builtin_amdgcn_raw_buffer_load_b128(ra, (int)(in ? oa[j] + k : 0x80000000u), 0, 0));
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      typename MM::frag_t a[NB];
-#pragma unroll
-      for (int j = 0; j < NB; ++j) a[j] = MM::prep(fa[u][j]);
-#pragma unroll
-      for (int i = 0; i < RB; ++i) {
-        const typename MM::frag_t b = MM::prep(fb[u][i]);
-#pragma unroll
-        for (int j = 0; j < NB; ++j) acc[i][j] = MM::mma(b, a[j], acc[i][j]);
+      for (int j = 0; j < NB; ++j) {
+        // (a block with fewer rows: lanes beyond them read a row again, into columns nobody reads)
+        const int row = (j * 16 + r) % (4 * MB);
+        fa[s][j] = *(const v4u*)(sb + 4096 + row * kSeg + (((s * 4 + q) ^ (row & 15)) << 4));
       }
     }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read out before it is filled again
+    issue(st, k + NS * step);
+    st = st + 1 == NS ? 0 : st + 1;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const typename MM::frag_t b = MM::prep(fb[s]);
+#pragma unroll
+      for (int j = 0; j < NB; ++j) acc[j] = MM::mma(b, MM::prep(fa[s][j]), acc[j]);
+    }
   }
-
+  wait_vmcnt<0>();  // no DMA may land in what follows
+  __syncthreads();
+  v4u(*part)[NB][64] = (v4u(*)[NB][64])lds;
 #pragma unroll
-  for (int i = 0; i < RB; ++i)
-#pragma unroll
-    for (int j = 0; j < NB; ++j) part[wave][i * NB + j][lane] = __builtin_bit_cast(v4u, acc[i][j]);
+  for (int j = 0; j < NB; ++j) part[wave][j][lane] = __builtin_bit_cast(v4u, acc[j]);
   __syncthreads();
   if (!fin) return;
   // lane (q, r) holds weight rows 4q .. 4q+3 of token r
   typename MM::acc_t sum = __builtin_bit_cast(typename MM::acc_t, part[0][wave][lane]);
 #pragma unroll
-  for (int w = 1; w < kRowsWaves; ++w) sum += __builtin_bit_cast(typename MM::acc_t, part[w][wave][lane]);
+  for (int w = 1; w < NW; ++w) sum += __builtin_bit_cast(typename MM::acc_t, part[w][wave][lane]);
   epi.finish(p, fm, fn, v4f{(float)sum[0], (float)sum[1], (float)sum[2], (float)sum[3]});
 }
 
@@ -200,11 +238,11 @@ __global__ __launch_bounds__(kRowsWaves * 64) void linear_rows_kernel(LinParams 
 // columns.
 // ---------------------------------------------------------------------------
 template <bool INT>
-__global__ __launch_bounds__(256) void linear_splitk_kernel(LinParams p, int tile_m, int tile_n) {
+__device__ __forceinline__ void join_slices(const LinParams& p, int tile_m, int tile_n, int64_t block, int64_t blocks) {
   const int64_t slot = (int64_t)tile_m * tile_n, per_tile = slot / 4;
   const int64_t groups = (int64_t)p.tail_tiles * per_tile;
-  const int64_t stride = (int64_t)gridDim.x * blockDim.x;
-  for (int64_t g = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; g < groups; g += stride) {
+  const int64_t stride = blocks * 256;
+  for (int64_t g = block * 256 + threadIdx.x; g < groups; g += stride) {
     const int j = (int)(g / per_tile);
     const int w = (int)(g - (int64_t)j * per_tile);
     const TileRC tc = raster_tile(p.dp_tiles + j, p.tiles_m, p.tiles_n, p.group_m);
@@ -215,52 +253,76 @@ __global__ __launch_bounds__(256) void linear_splitk_kernel(LinParams p, int til
     Epi4 epi;
     epi.load(p, m0 + row, n0 + col);
     const uint32_t* src = (const uint32_t*)p.ws + (int64_t)j * slot + (int64_t)row * cols + col;
-    v4f acc;
-    if constexpr (INT) {
-      v4u a = *(const v4u*)src;
-      for (int s = 1; s < p.splits; ++s) a += *(const v4u*)(src + (int64_t)s * p.tail_tiles * slot);
-      const v4i i = __builtin_bit_cast(v4i, a);
-      acc = v4f{(float)i.x, (float)i.y, (float)i.z, (float)i.w};
-    } else {
-      acc = *(const v4f*)src;
-      for (int s = 1; s < p.splits; ++s) acc += *(const v4f*)(src + (int64_t)s * p.tail_tiles * slot);
+    const int64_t step = (int64_t)p.tail_tiles * slot;
+    // slices are added in order, four loads in flight at a time
+    typedef typename std::conditional<INT, v4i, v4f>::type acc_t;
+    acc_t sum = {};
+    int s = 0;
+    for (; s + 4 <= p.splits; s += 4) {
+      acc_t v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = *(const acc_t*)(src + (s + u) * step);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) sum += v[u];
     }
+    acc_t v[3];
+#pragma unroll
+    for (int u = 0; u < 3; ++u)
+      if (s + u < p.splits) v[u] = *(const acc_t*)(src + (s + u) * step);
+#pragma unroll
+    for (int u = 0; u < 3; ++u)
+      if (s + u < p.splits) sum += v[u];
+    const v4f acc = {(float)sum[0], (float)sum[1], (float)sum[2], (float)sum[3]};
     epi.finish(p, m0 + row, n0 + col, acc);
   }
 }
 
-template <int AB, int NB, int RB>
+template <bool INT>
+__global__ __launch_bounds__(256) void linear_splitk_kernel(LinParams p, int tile_m, int tile_n) {
+  join_slices<INT>(p, tile_m, tile_n, blockIdx.x, gridDim.x);
+}
+
+// Both products of a backward: the first `ja` workgroups join a's tiles.
+__global__ __launch_bounds__(256) void linear_grad_join_kernel(LinParams a, LinParams b, int ja, int tile) {
+  if ((int)blockIdx.x < ja) join_slices<false>(a, tile, tile, blockIdx.x, ja);
+  else join_slices<false>(b, tile, tile, blockIdx.x - ja, gridDim.x - ja);
+}
+
+template <int AB, int MB, int NW, int NS>
 void rows(const LinParams& p, hipStream_t s) {
-  constexpr int U = NB * RB >= 4 ? 2 : 4;
-  const int64_t blocks = (p.N + 16 * RB - 1) / (16 * RB);
-  hipLaunchKernelGGL((linear_rows_kernel<AB, NB, RB, U>), dim3((unsigned)blocks), dim3(kRowsWaves * 64), 0, s, p);
+  hipLaunchKernelGGL((linear_rows_kernel<AB, MB, NW, NS>), dim3((unsigned)((p.N + 15) / 16)), dim3(NW * 64), 0, s, p);
 }
 
 template <int AB>
-void rows_ab(int nb, int rb, const LinParams& p, hipStream_t s) {
-  if (rb == 1) {
-    if (nb == 1) rows<AB, 1, 1>(p, s);
-    else if (nb == 2) rows<AB, 2, 1>(p, s);
-    else rows<AB, 4, 1>(p, s);
-  } else {
-    if (nb == 1) rows<AB, 1, 2>(p, s);
-    else if (nb == 2) rows<AB, 2, 2>(p, s);
-    else rows<AB, 4, 2>(p, s);
-  }
+void rows_ab(int nw, const LinParams& p, hipStream_t s) {
+  if (p.M <= 4) rows<AB, 1, 8, 2>(p, s);
+  else if (p.M <= 8) rows<AB, 2, 8, 2>(p, s);
+  else if (p.M <= 16) nw == 8 ? rows<AB, 4, 8, 2>(p, s) : rows<AB, 4, 4, 2>(p, s);
+  else if (p.M <= 32) nw == 8 ? rows<AB, 8, 8, 1>(p, s) : rows<AB, 8, 4, 1>(p, s);
+  else nw == 8 ? rows<AB, 16, 8, 1>(p, s) : rows<AB, 16, 4, 1>(p, s);
 }
 
 }  // namespace
 
-void launch_linear_rows(int ab, int nb, int rb, const LinParams& p, hipStream_t s) {
-  if (ab == T_F16) rows_ab<T_F16>(nb, rb, p, s);
-  else if (ab == T_BF16) rows_ab<T_BF16>(nb, rb, p, s);
-  else if (ab == T_E4M3) rows_ab<T_E4M3>(nb, rb, p, s);
-  else rows_ab<T_I8>(nb, rb, p, s);
+void launch_linear_rows(int ab, int nw, const LinParams& p, hipStream_t s) {
+  if (ab == T_F16) rows_ab<T_F16>(nw, p, s);
+  else if (ab == T_BF16) rows_ab<T_BF16>(nw, p, s);
+  else if (ab == T_E4M3) rows_ab<T_E4M3>(nw, p, s);
+  else rows_ab<T_I8>(nw, p, s);
 }
 
 void launch_linear_splitk(const LinParams& p, int tile_m, int tile_n, bool int_path, int grid, hipStream_t s) {
   if (int_path) hipLaunchKernelGGL(linear_splitk_kernel<true>, dim3(grid), dim3(256), 0, s, p, tile_m, tile_n);
   else hipLaunchKernelGGL(linear_splitk_kernel<false>, dim3(grid), dim3(256), 0, s, p, tile_m, tile_n);
+}
+
+void launch_linear_grad_join(const LinParams& a, const LinParams& b, int tile, int64_t most_blocks, hipStream_t s) {
+  auto blocks = [&](const LinParams& p) {
+    const int64_t n = ((int64_t)p.tail_tiles * tile * tile / 4 + 255) / 256;
+    return (int)(n < most_blocks ? n : most_blocks);
+  };
+  const int ja = blocks(a), jb = blocks(b);
+  hipLaunchKernelGGL(linear_grad_join_kernel, dim3(ja + jb), dim3(256), 0, s, a, b, ja, tile);
 }
 
 }  // namespace gemm_epi

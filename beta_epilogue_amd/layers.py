@@ -33,7 +33,7 @@ class gemm_epi_linear_desc(ctypes.Structure):
 
 class gemm_epi_linear_grad_desc(ctypes.Structure):
     _fields_ = [("M", _i64), ("N", _i64), ("K", _i64), ("ab_dtype", _i32), ("act", _i32), ("da_dtype", _i32),
-                ("db_dtype", _i32), ("dbias_dtype", _i32)]
+                ("db_dtype", _i32), ("dbias_dtype", _i32), ("tile", _i32), ("splits", _i32)]
 
 
 class gemm_epi_rmsnorm_desc(ctypes.Structure):
@@ -245,15 +245,16 @@ class FusedLinearGrad(_Plan):
     sums of dZ.  All tensors are packed; dD, Z, dZ, A and B have type ab (f16
     or bf16).  da, db, dbias: the gradients' types, None for one not wanted.
     Without an activation dD takes dZ's place and Z and dZ are not given.  The
-    residual's gradient is dD.
+    residual's gradient is dD.  tile (128 or 256) and splits force the products'
+    tile and K split.
     """
 
     _op = "linear_grad"
 
-    def __init__(self, M, N, K, *, ab="bf16", act="none", da=None, db=None, dbias=None):
+    def __init__(self, M, N, K, *, ab="bf16", act="none", da=None, db=None, dbias=None, tile=0, splits=0):
         super().__init__(gemm_epi_linear_grad_desc(
             M, N, K, _code(DTYPES, ab, "type"), _code(ACTIVATIONS, act, "activation"), _code(DTYPES, da, "type"),
-            _code(DTYPES, db, "type"), _code(DTYPES, dbias, "type")))
+            _code(DTYPES, db, "type"), _code(DTYPES, dbias, "type"), tile, splits))
         ab = TORCH_DTYPES[ab]
         da, db, dbias = (TORCH_DTYPES[t] if t else None for t in (da, db, dbias))
         m, v = self._matrix, self._vector

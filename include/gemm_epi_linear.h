@@ -68,8 +68,8 @@ typedef struct gemm_epi_linear_handle gemm_epi_linear_handle;
 
 /*
  * Validate a problem and plan it.  With M of at most 64 the plan is the
- * few-row kernel, which streams B once; otherwise a tile kernel, its tile
- * shape and K split chosen as in gemm_epi_create.  INVALID_ARG: sizes, codes,
+ * few-row kernel, which streams B once; otherwise a tile kernel, whose tile
+ * shape and K split a cost model chooses.  INVALID_ARG: sizes, codes,
  * flags other than 0 and 1, strides below the extent, a stride of a tensor
  * that is not used.  ALIGNMENT: the 16-byte rule.  UNSUPPORTED: e5m2 and uint8;
  * rows or row strides too long for the kernels' 31-bit tile offsets; 2^31 or
@@ -96,9 +96,9 @@ int gemm_epi_linear_run(const gemm_epi_linear_handle* h, const void* A, const vo
 /* Free a handle (NULL is fine). */
 int gemm_epi_linear_destroy(gemm_epi_linear_handle* h);
 
-/* What a handle launches, in gemm_epi_plan's terms (few rows: tile_m tokens by
- * tile_n weight rows per workgroup, tile_k 0; variant indexes the linear
- * table). */
+/* What a handle launches, in gemm_epi_plan's terms (variant indexes the linear
+ * table; few rows: up to tile_m tokens by tile_n weight rows per workgroup,
+ * tile_k and lds_bytes 0). */
 int gemm_epi_linear_get_plan(const gemm_epi_linear_handle* h, gemm_epi_plan* out);
 
 /* Number of linear kernels and the name of one (NULL out of range). */
@@ -112,16 +112,21 @@ typedef struct gemm_epi_linear_grad_desc {
   int32_t da_dtype;    /* NONE (no dA), F16, BF16 or F32 */
   int32_t db_dtype;    /* NONE (no dB), F16, BF16 or F32: dB and dB_in */
   int32_t dbias_dtype; /* NONE (no dbias), F16, BF16 or F32 */
+  int32_t tile;        /* 0: the plan's choice; 128 or 256: that tile */
+  int32_t splits;      /* 0: the plan's choice; n: every tile of both products
+                          in n K slices (fewer if K has fewer K tiles) */
 } gemm_epi_linear_grad_desc;
 
 typedef struct gemm_epi_linear_grad_handle gemm_epi_linear_grad_handle;
 
 /*
- * Validate and plan a backward: an elementwise pass (dZ, column sums) and one
- * or two matrix products of the GEMM kernels.  dZ is rounded to ab_dtype, the
- * type the matrix cores read; dbias is summed in fp32 before that rounding, in
- * a fixed order.  Errors as above and those of gemm_epi_create for the
- * products (dA: M x K over N; dB: N x K over M).  At least one gradient.
+ * Validate and plan a backward: an elementwise pass (dZ, column sums), then
+ * one launch for both matrix products (and one that joins K slices, where the
+ * plan has them).  dZ is rounded to ab_dtype, the type the matrix cores read;
+ * dbias is summed in fp32 before that rounding, in a fixed order.  Errors as
+ * above; at least one gradient must be wanted.  UNSUPPORTED as well: an
+ * operand that a product reads across its rows (dA: B; dB: A and dZ) of 2 GiB
+ * or more.
  */
 int gemm_epi_linear_grad_create(const gemm_epi_linear_grad_desc* desc, gemm_epi_linear_grad_handle** out);
 

@@ -75,8 +75,9 @@ GRAD_BAD = [
     (dict(M=0), INVALID), (dict(K=-5), INVALID), (dict(ab_dtype=0), INVALID), (dict(ab_dtype=T["e4m3"]), UNSUPPORTED),
     (dict(act=9), INVALID), (dict(da_dtype=T["i32"]), INVALID), (dict(dbias_dtype=T["e4m3"]), INVALID),
     (dict(da_dtype=0, db_dtype=0, dbias_dtype=0), INVALID), (dict(N=250), ALIGN), (dict(K=500, N=256), ALIGN),
-    (dict(M=1 << 62), INVALID), (dict(N=1 << 40, da_dtype=0, db_dtype=0), UNSUPPORTED),
-    (dict(M=1 << 20, N=1 << 12, da_dtype=0), UNSUPPORTED),  # an operand of 2 GiB or more
+    (dict(M=1 << 62), UNSUPPORTED), (dict(N=1 << 40, da_dtype=0, db_dtype=0), UNSUPPORTED),
+    (dict(tile=64), INVALID), (dict(splits=-2), INVALID), (dict(K=1 << 22), UNSUPPORTED),
+    (dict(M=1 << 20, N=1 << 12), UNSUPPORTED),  # an operand of 2 GiB or more
 ]
 
 
@@ -138,15 +139,18 @@ def test_null_arguments():
     assert L.gemm_epi_linear_grad_workspace(None) == -1 and L.gemm_epi_rmsnorm_grad_workspace(None) == -1
 
 
+NAMES = 17
+
+
 def test_variant_table():
     names = ge.linear_variant_names()
-    assert len(set(names)) == len(names) == 17 and names[-1] == "linear_rows"
+    assert len(set(names)) == len(names) == NAMES and names[-1] == "linear_rows"
     assert layers.lib().gemm_epi_linear_variant_name(-1) is None
-    assert layers.lib().gemm_epi_linear_variant_name(17) is None
+    assert layers.lib().gemm_epi_linear_variant_name(NAMES) is None
     d = layers.gemm_epi_linear_desc(**LINEAR)
     h = ctypes.c_void_p()
     create = layers.lib().gemm_epi_linear_create_variant
-    assert create(ctypes.byref(d), 17, ctypes.byref(h)) == INVALID
+    assert create(ctypes.byref(d), NAMES, ctypes.byref(h)) == INVALID
     assert create(ctypes.byref(d), names.index("linear_f16_256x256"), ctypes.byref(h)) == UNSUPPORTED
     assert create(ctypes.byref(d), names.index("linear_rows"), ctypes.byref(h)) == UNSUPPORTED  # 100 rows
 

@@ -300,13 +300,13 @@ def test_two_streams_at_once():
 
 
 # --- backward --------------------------------------------------------------
-def run_grad(M, N, K, ab="bf16", act="none", da=None, db=None, dbias=None, db_in=False, seed=1, alias=None):
+def run_grad(M, N, K, ab="bf16", act="none", da=None, db=None, dbias=None, db_in=False, seed=1, alias=None, tile=0, splits=0):
     g = torch.Generator().manual_seed(seed)
     T = ref.TORCH[ab]
     dD, Z = _draw(g, M, N, T), (_draw(g, M, N, T, 1.5) if act != "none" else None)
     A, B = _draw(g, M, K, T), _draw(g, N, K, T, K ** -0.5)
     C = _draw(g, N, K, ref.TORCH[db]) if db_in else None
-    op = ge.FusedLinearGrad(M, N, K, ab=ab, act=act, da=da, db=db, dbias=dbias)
+    op = ge.FusedLinearGrad(M, N, K, ab=ab, act=act, da=da, db=db, dbias=dbias, tile=tile, splits=splits)
     new = lambda r, c, t: Out(r, c, ref.TORCH[t]) if t else None  # noqa: E731
     dA, dB, dZ = new(M, K, da), new(N, K, db), new(M, N, ab if act != "none" else None)
     db1 = new(1, N, dbias)
@@ -317,7 +317,7 @@ def run_grad(M, N, K, ab="bf16", act="none", da=None, db=None, dbias=None, db_in
     if db_in and alias == "dD":  # the weight's gradient added up in place
         dB.t.copy_(Cd)
         Cd = dB.t
-    _say("case", M, N, K, ab, act, da, db, dbias, db_in, "ws", op.workspace_bytes)
+    _say("case", M, N, K, ab, act, da, db, dbias, db_in, "tile", tile, "splits", splits, "ws", op.workspace_bytes)
     op(dDd, A.cuda() if db else None, B.cuda() if da else None, Z=Zd, dB_in=Cd, dZ=dzt, dA=t(dA), dB=t(dB),
        dbias=db1.t[0] if db1 else None)
     torch.cuda.synchronize()
@@ -360,6 +360,15 @@ def test_grad(ab, act):
 def test_grad_sizes(M, N, K):
     run_grad(M, N, K, "bf16", "silu", da="bf16", db="f32", dbias="bf16")
     run_grad(M, N, K, "f16", "none", da="f32", db="f32", dbias="f32", db_in=True)
+
+
+@pytest.mark.parametrize("splits", [0, 1, 2, 5])
+@pytest.mark.parametrize("tile", [128, 256])
+@pytest.mark.parametrize("ab", ["bf16", "f16"])
+def test_grad_tiles(ab, tile, splits):
+    """Each tile, whole and in K slices, more tiles than fit at once."""
+    run_grad(333, 328, 456, ab, "gelu", da=ab, db="f32", dbias="f32", db_in=True, tile=tile, splits=splits)
+    run_grad(40, 1288, 2312, ab, "none", da="f32", db=ab, dbias="f32", tile=tile, splits=splits)
 
 
 def test_grad_parts():
