@@ -381,22 +381,24 @@ void cut(GradProduct* p, int tile, int64_t splits) {
   p->splits = (int)((p->K + p->kslice - 1) / p->kslice);
 }
 
-// Modelled time (us) of the launch and the join.  A K tile takes 1.2 us with
-// 256x256 tiles and 0.75 us with 128x128 ones (two workgroups per compute
-// unit, together), an item 3 us besides.
+// Modelled time (us) of the launch and the join, from forced runs of seven
+// shapes (M 64 to 6385): an item takes 1.1 us per K tile with 256x256 tiles and
+// 0.45 with 128x128 ones, or 0.85 for two that share a compute unit, and 8 or 4
+// us besides.
 double grad_time(const GradProduct& a, const GradProduct& b, int tile, int cus) {
-  const double tk = tile == 256 ? 1.2 : 0.75;
-  const double slots = (double)cus * grad_occ(tile);
+  const double items = (double)(a.items() + b.items());
+  const bool pairs = tile == 128 && items > cus;
+  const double slots = pairs ? 2.0 * cus : cus;
+  const double tk = tile == 256 ? 1.1 : pairs ? 0.85 : 0.45, fixed = tile == 256 ? 8.0 : 4.0;
   double longest = 0.0, total = 0.0, join = 0.0;
   for (const GradProduct* p : {&a, &b}) {
     if (!p->on) continue;
-    const double item = 3.0 + tk * (double)((std::min(p->kslice, p->K) + kGradKTile - 1) / kGradKTile);
+    const double item = fixed + tk * (double)((std::min(p->kslice, p->K) + kGradKTile - 1) / kGradKTile);
     longest = std::max(longest, item);
     total += item * (double)p->items();
     if (p->splits > 1) join = std::max(join, 4.0) + 2.0 * (double)p->slots(tile) / 5.0e6;
   }
-  const double t = (double)(a.items() + b.items()) <= slots ? longest : total / slots + 0.5 * longest;
-  return t + join;
+  return (items <= slots ? longest : total / slots + 0.5 * longest) + join;
 }
 
 }  // namespace
@@ -457,9 +459,13 @@ extern "C" int gemm_epi_linear_grad_create(const gemm_epi_linear_grad_desc* desc
   h->d = d;
   h->device = device;
   h->cus = cus;
-  // 64 rows per partial sum; more where 2^16 chunks would not do (the grid's
+  // rows per workgroup of the elementwise pass (and per partial sum): 64, fewer
+  // as long as there are under four workgroups for a compute unit (596 x 2592:
+  // 14.5 us with 64 rows), more where 2^16 chunks would not do (the grid's
   // second dimension)
-  h->chunk = (int)std::max<int64_t>(64, (d.M + 65534) / 65535);
+  int64_t chunk = 64;
+  while (chunk > 8 && (d.N + 255) / 256 * ((d.M + chunk - 1) / chunk) < 4 * cus) chunk /= 2;
+  h->chunk = (int)std::max<int64_t>(chunk, (d.M + 65534) / 65535);
   h->a.on = da;
   h->a.M = d.M, h->a.N = d.K, h->a.K = d.N;
   h->b.on = db;
@@ -571,10 +577,11 @@ extern "C" int gemm_epi_linear_grad_run(const gemm_epi_linear_grad_handle* h, co
   p.C = d.N;
   p.dbias = dbias;
   p.dbias_dtype = d.dbias_dtype;
-  if (d.ab_dtype == GEMM_EPI_F16)
-    h->tile == 256 ? launch_linear_grad_mm<T_F16, 256>(p, s) : launch_linear_grad_mm<T_F16, 128>(p, s);
-  else
-    h->tile == 256 ? launch_linear_grad_mm<T_BF16, 256>(p, s) : launch_linear_grad_mm<T_BF16, 128>(p, s);
+  const int kind = h->tile == 256 ? GRAD_256 : p.ga + p.gb > h->cus ? GRAD_128 : GRAD_128_DEEP;
+  static void (*const kLaunch[2][kGradKinds])(const GradParams&, hipStream_t) = {
+      {launch_linear_grad_mm<T_F16, 0>, launch_linear_grad_mm<T_F16, 1>, launch_linear_grad_mm<T_F16, 2>},
+      {launch_linear_grad_mm<T_BF16, 0>, launch_linear_grad_mm<T_BF16, 1>, launch_linear_grad_mm<T_BF16, 2>}};
+  kLaunch[d.ab_dtype == GEMM_EPI_BF16][kind](p, s);
   rc = launched();
   if (rc || (p.a.tail_tiles == 0 && p.b.tail_tiles == 0)) return rc;
   launch_linear_grad_join(p.a, p.b, h->tile, (int64_t)h->cus * 8, s);

@@ -43,11 +43,17 @@ void launch_linear_part(int variant, const LinParams& p, int grid, hipStream_t s
 //   b: dB = dB_in + dZ^T . A  (N x K over M: A = dZ M-major, B = A N-major)
 // Workgroups 0 .. ga-1 run a, the next gb run b, the rest add the chunks'
 // column sums of dZ into dbias.  A problem that is not wanted has 0.
-constexpr int grad_occ(int tile) { return tile == 256 ? 1 : 2; }  // workgroups per compute unit
-template <int AB, int TILE>
-using GradCfgA = Cfg<AB, true, false, true, TILE, TILE, 128, 2, 2, 2, TILE == 256 ? 2 : 0, 32, 2, grad_occ(TILE)>;
-template <int AB, int TILE>
-using GradCfgB = Cfg<AB, false, false, true, TILE, TILE, 128, 2, 2, 2, TILE == 256 ? 2 : 0, 32, 2, grad_occ(TILE)>;
+// Three kernels per type: 256x256 tiles; 128x128 tiles with two workgroups per
+// compute unit; 128x128 tiles with a ring of three stages, for grids of at most
+// one workgroup per compute unit, whose transposing reads have nobody else's
+// MFMAs to hide behind (dA of 64 x 4096 x 4096 37.7 -> 25.5 us; with 512 tiles,
+// 2048^3, the pair takes 35 us and the deep ring 39).
+enum : int { GRAD_256 = 0, GRAD_128 = 1, GRAD_128_DEEP = 2, kGradKinds = 3 };
+constexpr int grad_tile(int kind) { return kind == GRAD_256 ? 256 : 128; }
+constexpr int grad_occ(int kind) { return kind == GRAD_128 ? 2 : 1; }  // workgroups per compute unit
+template <int AB, bool A_KMAJOR, int KIND>
+using GradCfg = Cfg<AB, A_KMAJOR, false, true, grad_tile(KIND), grad_tile(KIND), 128, 2, 2,
+                    KIND == GRAD_128_DEEP ? 3 : 2, KIND == GRAD_256 ? 2 : 0, 32, 2, grad_occ(KIND)>;
 struct GradParams {
   LinParams a, b;
   int32_t ga, gb;
@@ -56,8 +62,8 @@ struct GradParams {
   void* dbias;
   int32_t dbias_dtype;
 };
-// TILE x TILE tiles (128 or 256) of type AB (T_F16 or T_BF16).
-template <int AB, int TILE>
+// Kernel KIND of type AB (T_F16 or T_BF16).
+template <int AB, int KIND>
 void launch_linear_grad_mm(const GradParams& p, hipStream_t s);
 
 // Adds the slices of split tiles of both products (tail_tiles 0: none).

@@ -1,6 +1,6 @@
 // gemm_linear_grad_mm.hip -- the two matrix products of the linear layer's
-// backward in one launch, compiled once per type and tile
-// (GEMM_LINEAR_GRAD_PART 0 .. 3).
+// backward in one launch, compiled once per type and kernel
+// (GEMM_LINEAR_GRAD_PART 0 .. 5).
 //
 // dA = dZ . B and dB = dB_in + dZ^T . A read what the elementwise pass left
 // and do not depend on one another, so their tiles (and K slices) share a
@@ -13,17 +13,17 @@
 #include "gemm_linear.hpp"
 
 #ifndef GEMM_LINEAR_GRAD_PART
-#error "GEMM_LINEAR_GRAD_PART must be defined (0 .. 3)"
+#error "GEMM_LINEAR_GRAD_PART must be defined (0 .. 5)"
 #endif
 
 namespace gemm_epi {
 
 namespace {
 
-template <int AB, int TILE>
-__global__ __launch_bounds__(256, grad_occ(TILE)) void linear_grad_mm_kernel(GradParams p) {
-  using CA = GradCfgA<AB, TILE>;
-  using CB = GradCfgB<AB, TILE>;
+template <int AB, int KIND>
+__global__ __launch_bounds__(256, grad_occ(KIND)) void linear_grad_mm_kernel(GradParams p) {
+  using CA = GradCfg<AB, true, KIND>;
+  using CB = GradCfg<AB, false, KIND>;
   __shared__ __attribute__((aligned(1024))) char lds[CA::LDS_BYTES > CB::LDS_BYTES ? CA::LDS_BYTES : CB::LDS_BYTES];
   const int bid = blockIdx.x;
   if (bid < p.ga) gemm_epi_body<CA>(p.a, lds, bid, p.ga);
@@ -33,12 +33,12 @@ __global__ __launch_bounds__(256, grad_occ(TILE)) void linear_grad_mm_kernel(Gra
 
 }  // namespace
 
-constexpr int kAb = GEMM_LINEAR_GRAD_PART % 2 ? T_BF16 : T_F16, kTile = GEMM_LINEAR_GRAD_PART / 2 ? 256 : 128;
+constexpr int kAb = GEMM_LINEAR_GRAD_PART % 2 ? T_BF16 : T_F16, kKind = GEMM_LINEAR_GRAD_PART / 2;
 
 template <>
-void launch_linear_grad_mm<kAb, kTile>(const GradParams& p, hipStream_t s) {
+void launch_linear_grad_mm<kAb, kKind>(const GradParams& p, hipStream_t s) {
   const int64_t sums = p.partial ? (p.C + 31) / 32 : 0;
-  hipLaunchKernelGGL((linear_grad_mm_kernel<kAb, kTile>), dim3((unsigned)(p.ga + p.gb + sums)), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((linear_grad_mm_kernel<kAb, kKind>), dim3((unsigned)(p.ga + p.gb + sums)), dim3(256), 0, s, p);
 }
 
 }  // namespace gemm_epi

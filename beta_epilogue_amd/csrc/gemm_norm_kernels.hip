@@ -29,32 +29,31 @@ template <> struct Elem<T_F16> { typedef _Float16 type; };
 template <> struct Elem<T_BF16> { typedef __bf16 type; };
 template <> struct Elem<T_F32> { typedef float type; };
 
-typedef v4u v4u_any __attribute__((aligned(2)));  // 16 bytes at element alignment
-typedef v4f v4f_any __attribute__((aligned(4)));
 typedef v2u v2u_any __attribute__((aligned(1)));
 
 typedef float v8f __attribute__((ext_vector_type(8)));
 
+// Eight elements as stored (16 bytes of a 2-byte type), and their values.
+template <int T> struct Group {
+  typedef typename Elem<T>::type type __attribute__((ext_vector_type(8)));
+  typedef type any __attribute__((aligned(sizeof(typename Elem<T>::type))));
+};
+template <class G>
+__device__ __forceinline__ v8f value8(G g) {
+  return __builtin_convertvector(g, v8f);
+}
+
 // Elements [c, c + 8) of a row that ends at cols; 0 past its end.
 template <int T>
-__device__ __forceinline__ v8f load8(const void* row, int64_t c, int64_t cols) {
+__device__ __forceinline__ typename Group<T>::type load8(const void* row, int64_t c, int64_t cols) {
   const typename Elem<T>::type* p = (const typename Elem<T>::type*)row + c;
-  v8f v = {};
+  typename Group<T>::type v = {};
   if (c + 8 <= cols) {
-    v4f lo, hi;
-    if constexpr (T == T_F32) {
-      lo = *(const v4f_any*)p;
-      hi = *(const v4f_any*)(p + 4);
-    } else {
-      const v4u r = *(const v4u_any*)p;
-      lo = epi_dec<T>(r, 0);
-      hi = epi_dec<T>(r, 1);
-    }
-    v = v8f{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    v = *(const typename Group<T>::any*)p;
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      if (c + k < cols) v[k] = (float)p[k];
+      if (c + k < cols) v[k] = p[k];
   }
   return v;
 }
@@ -63,16 +62,7 @@ template <int T>
 __device__ __forceinline__ void store8(void* row, int64_t c, int64_t cols, v8f v) {
   typename Elem<T>::type* p = (typename Elem<T>::type*)row + c;
   if (c + 8 <= cols) {
-    if constexpr (T == T_F32) {
-      *(v4f_any*)p = v4f{v[0], v[1], v[2], v[3]};
-      *(v4f_any*)(p + 4) = v4f{v[4], v[5], v[6], v[7]};
-    } else {
-      typedef typename Elem<T>::type vec8 __attribute__((ext_vector_type(8)));
-      vec8 o;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) o[k] = (typename Elem<T>::type)v[k];
-      *(v4u_any*)p = __builtin_bit_cast(v4u, o);
-    }
+    *(typename Group<T>::any*)p = __builtin_convertvector(v, typename Group<T>::type);
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
@@ -82,30 +72,32 @@ __device__ __forceinline__ void store8(void* row, int64_t c, int64_t cols, v8f v
 
 template <int T>
 __device__ __forceinline__ v8f load_weight8(const void* w, bool f32, int64_t c, int64_t cols) {
-  return f32 ? load8<T_F32>(w, c, cols) : load8<T>(w, c, cols);
+  return f32 ? load8<T_F32>(w, c, cols) : value8(load8<T>(w, c, cols));
 }
 
-// Rounds to nearest-even into 8 bits and stores.  A NaN stays NaN in e4m3
-// and becomes 0 in int8 (the row's scale is NaN then).
-template <int T>
+// Rounds to nearest-even into 8 bits and stores: values of at most QMAX (1 + 2^-21),
+// which round to QMAX, or NaN, which stays NaN in e4m3 and becomes 0 in int8
+// (the row's scale is NaN then).  int8: adding 1.5 * 2^23 leaves the rounded
+// integer in the low byte of the sum.  TX is the inputs' type: a NaN that comes
+// from 16-bit values has zeros there already.
+template <int T, int TX>
 __device__ __forceinline__ void store8_q(void* row, int64_t c, int64_t cols, v8f v) {
-  constexpr float QMAX = T == T_E4M3 ? 448.0f : 127.0f;
   uint32_t w[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    float q[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float x = v[4 * j + k];
-      q[k] = x > QMAX ? QMAX : (x < -QMAX ? -QMAX : x);
-    }
     if constexpr (T == T_E4M3) {
-      int b = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
-      w[j] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], b, true);
+      int b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * j], v[4 * j + 1], 0, false);
+      w[j] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * j + 2], v[4 * j + 3], b, true);
     } else {
-      w[j] = 0;
+      uint32_t b[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) w[j] |= ((uint32_t)(int)__builtin_rintf(q[k] == q[k] ? q[k] : 0.0f) & 0xffu) << (8 * k);
+      for (int k = 0; k < 4; ++k) {
+        const float x = v[4 * j + k];
+        b[k] = __float_as_uint((TX == T_F32 && x != x ? 0.0f : x) + 12582912.0f);
+      }
+      // byte 0 of each sum
+      const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u), hi = __builtin_amdgcn_perm(b[3], b[2], 0x0c0c0400u);
+      w[j] = __builtin_amdgcn_perm(hi, lo, 0x05040100u);
     }
   }
   uint8_t* p = (uint8_t*)row + c;
@@ -118,28 +110,37 @@ __device__ __forceinline__ void store8_q(void* row, int64_t c, int64_t cols, v8f
   }
 }
 
-// A sum (or maximum) over the TPR threads of a row, in a fixed order; every
-// thread gets it.  red: one word per wave and exchange, not reused before the
-// next barrier of the row.
+// Joins N values over the TPR threads of a row, in a fixed order; every thread
+// gets the results.  red: N words per wave, not written again before the next
+// barrier of the row.
 struct Sum {
+  typedef float type;
   static __device__ __forceinline__ float join(float a, float b) { return a + b; }
 };
-struct Max {  // a NaN wins
-  static __device__ __forceinline__ float join(float a, float b) { return b > a || b != b ? b : a; }
+struct Max {
+  typedef uint32_t type;
+  static __device__ __forceinline__ uint32_t join(uint32_t a, uint32_t b) { return a > b ? a : b; }
 };
-template <class OP, int TPR>
-__device__ __forceinline__ float row_join(float v, float* red) {
+template <class OP, int TPR, int N>
+__device__ __forceinline__ void row_join(typename OP::type (&v)[N], typename OP::type* red) {
 #pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v = OP::join(v, __shfl_xor(v, d, 64));
+  for (int d = 32; d >= 1; d >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = OP::join(v[i], __shfl_xor(v[i], d, 64));
   if constexpr (TPR > 64) {
     const int wave = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) red[wave] = v;
-    __syncthreads();
-    v = red[0];
+    if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-    for (int w = 1; w < TPR / 64; ++w) v = OP::join(v, red[w]);
+      for (int i = 0; i < N; ++i) red[wave * N + i] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = red[i];
+#pragma unroll
+    for (int w = 1; w < TPR / 64; ++w)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = OP::join(v[i], red[w * N + i]);
   }
-  return v;
 }
 
 template <int TPR> constexpr int block_threads() { return TPR > 256 ? TPR : 256; }
@@ -148,7 +149,8 @@ template <int TX, int TY, int TPR, int NV>
 __global__ __launch_bounds__(block_threads<TPR>()) void rmsnorm_kernel(NormParams p) {
   constexpr int RPB = block_threads<TPR>() / TPR;
   constexpr bool Q = TY == T_E4M3 || TY == T_I8;
-  __shared__ float red[2][TPR / 64];
+  __shared__ float red[TPR / 64];
+  __shared__ uint32_t redm[TPR / 64];
   const int t = threadIdx.x % TPR;
   const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
   if (row >= p.rows) return;  // whole waves, and whole workgroups where rows share barriers
@@ -156,65 +158,69 @@ __global__ __launch_bounds__(block_threads<TPR>()) void rmsnorm_kernel(NormParam
   const char* x = (const char*)p.x + row * p.ldx * XS;
   const char* r = p.r ? (const char*)p.r + row * p.ldr * XS : nullptr;
   v8f h[NV], w[NV];
-  float ss = 0.0f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int64_t c = (int64_t)(i * TPR + t) * 8;
-    h[i] = load8<TX>(x, c, p.cols);
-    if (r) h[i] += load8<TX>(r, c, p.cols);
+    h[i] = value8(load8<TX>(x, c, p.cols));
+    if (r) h[i] += value8(load8<TX>(r, c, p.cols));
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) w[i] = load_weight8<TX>(p.w, p.w_f32, (int64_t)(i * TPR + t) * 8, p.cols);
+  float ss[1] = {0.0f};
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) ss = __builtin_fmaf(h[i][k], h[i][k], ss);
+    for (int k = 0; k < 8; ++k) ss[0] = __builtin_fmaf(h[i][k], h[i][k], ss[0]);
   }
   if (p.h) {
     char* ho = (char*)p.h + row * p.ldh * XS;
 #pragma unroll
     for (int i = 0; i < NV; ++i) store8<TX>(ho, (int64_t)(i * TPR + t) * 8, p.cols, h[i]);
   }
-  ss = row_join<Sum, TPR>(ss, red[0]);
-  const float s = 1.0f / __builtin_sqrtf(ss / (float)p.cols + p.eps);
+  row_join<Sum, TPR>(ss, red);
+  const float s = 1.0f / __builtin_sqrtf(ss[0] / (float)p.cols + p.eps);
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) h[i][k] = h[i][k] * s * w[i][k];
+  for (int i = 0; i < NV; ++i) h[i] *= w[i];
   if constexpr (Q) {
-    float m = 0.0f;
+    // the largest |h w| as an integer: the order of non-negative floats, NaN on top
+    uint32_t m[1] = {0u};
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) m = Max::join(m, __builtin_fabsf(h[i][k]));
-    m = row_join<Max, TPR>(m, red[1]);
+      for (int k = 0; k < 8; ++k) m[0] = Max::join(m[0], __float_as_uint(h[i][k]) & 0x7fffffffu);
+    row_join<Max, TPR>(m, redm);
     constexpr float QMAX = TY == T_E4M3 ? 448.0f : 127.0f;
-    float scale = m / QMAX;
+    float scale = __uint_as_float(m[0]) * s / QMAX;
     scale = scale < 0x1p-126f ? 0x1p-126f : scale;  // (a NaN stays)
     const float inv = 1.0f / scale;
+    float f = s * inv;
+    if (f > 0x1.fffffep127f) {  // the smallest scales: in two steps (all-zero rows give 0)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) h[i] *= s;
+      f = inv;
+    }
     uint8_t* y = (uint8_t*)p.y + row * p.ldy;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) h[i][k] *= inv;
-      store8_q<TY>(y, (int64_t)(i * TPR + t) * 8, p.cols, h[i]);
-    }
+    for (int i = 0; i < NV; ++i) store8_q<TY, TX>(y, (int64_t)(i * TPR + t) * 8, p.cols, h[i] * f);
     if (t == 0) p.scale[row] = scale;
   } else {
     char* y = (char*)p.y + row * p.ldy * XS;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) store8<TX>(y, (int64_t)(i * TPR + t) * 8, p.cols, h[i]);
+    for (int i = 0; i < NV; ++i) store8<TX>(y, (int64_t)(i * TPR + t) * 8, p.cols, h[i] * s);
   }
 }
 
 // The backward: a workgroup walks rows blockIdx, blockIdx + grid, ... (RPB at
 // a time), keeps its weights and its part of dweight in registers, and leaves
-// one partial sum per column; colsum adds the workgroups in a fixed order.
+// one partial sum per column; colsum adds the workgroups in a fixed order.  The
+// next row is loaded before the sums of this one are joined (not with 1024
+// threads per row: 16 waves hide it by themselves, and the registers spill).
 template <int T, int TPR, int NV>
 __global__ __launch_bounds__(block_threads<TPR>()) void rmsnorm_grad_kernel(NormGradParams p) {
   constexpr int RPB = block_threads<TPR>() / TPR;
   constexpr int XS = sizeof(typename Elem<T>::type);
-  __shared__ float red[2][2][TPR / 64];
+  constexpr bool AHEAD = TPR < 1024;
+  __shared__ float red[2][2 * (TPR / 64)];
   __shared__ float joined[RPB > 1 ? RPB * TPR * NV * 8 : 1];
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
   v8f w[NV], dw[NV];
@@ -224,42 +230,57 @@ __global__ __launch_bounds__(block_threads<TPR>()) void rmsnorm_grad_kernel(Norm
     dw[i] = v8f{};
   }
   const float inv_cols = 1.0f / (float)p.cols;
-  int flip = 0;
-  for (int64_t row = (int64_t)blockIdx.x * RPB + sub; row < p.rows; row += (int64_t)gridDim.x * RPB) {
+  typedef typename Group<T>::type group;
+  group h1[NV], g1[NV], d1[NV];
+  auto fetch = [&](int64_t row) {
     const char* hp = (const char*)p.h + row * p.ldh * XS;
     const char* gp = (const char*)p.dy + row * p.ldy * XS;
-    v8f h[NV], g[NV];
-    float ss = 0.0f, gh = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      h[i] = load8<T>(hp, (int64_t)(i * TPR + t) * 8, p.cols);
-      g[i] = load8<T>(gp, (int64_t)(i * TPR + t) * 8, p.cols);
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        ss = __builtin_fmaf(h[i][k], h[i][k], ss);
-        gh = __builtin_fmaf(g[i][k] * w[i][k], h[i][k], gh);
-      }
-    ss = row_join<Sum, TPR>(ss, red[flip][0]);
-    gh = row_join<Sum, TPR>(gh, red[flip][1]);
-    flip ^= 1;  // the next row's words are others: one barrier separates reuse
-    const float s = 1.0f / __builtin_sqrtf(ss * inv_cols + p.eps);
-    const float f = s * s * s * (gh * inv_cols);
-    char* op = (char*)p.dh + row * p.ldo * XS;
     const char* ip = p.dh_in ? (const char*)p.dh_in + row * p.ldi * XS : nullptr;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int64_t c = (int64_t)(i * TPR + t) * 8;
-      v8f d = {};
-      if (ip) d = load8<T>(ip, c, p.cols);
+      h1[i] = load8<T>(hp, c, p.cols);
+      g1[i] = load8<T>(gp, c, p.cols);
+      d1[i] = group{};
+      if (ip) d1[i] = load8<T>(ip, c, p.cols);
+    }
+  };
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  int64_t row = (int64_t)blockIdx.x * RPB + sub;
+  if (AHEAD && row < p.rows) fetch(row);
+  int flip = 0;
+  for (; row < p.rows; row += step) {
+    if (!AHEAD) fetch(row);
+    group hr[NV], gr[NV], dr[NV];
+    float sums[2] = {0.0f, 0.0f};  // h^2, g w h
+#pragma unroll
+    for (int i = 0; i < NV; ++i) hr[i] = h1[i], gr[i] = g1[i], dr[i] = d1[i];
+    // (dH may be an input itself: only rows not yet written are read)
+    if (AHEAD && row + step < p.rows) fetch(row + step);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const v8f h = value8(hr[i]), g = value8(gr[i]);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        dw[i][k] = __builtin_fmaf(g[i][k] * s, h[i][k], dw[i][k]);
-        d[k] += __builtin_fmaf(g[i][k] * w[i][k], s, -(h[i][k] * f));
+        sums[0] = __builtin_fmaf(h[k], h[k], sums[0]);
+        sums[1] = __builtin_fmaf(g[k] * w[i][k], h[k], sums[1]);
       }
-      store8<T>(op, c, p.cols, d);
+    }
+    row_join<Sum, TPR>(sums, red[flip]);
+    flip ^= 1;  // the next row's words are others: one barrier separates reuse
+    const float s = 1.0f / __builtin_sqrtf(sums[0] * inv_cols + p.eps);
+    const float f = s * s * s * (sums[1] * inv_cols);
+    char* op = (char*)p.dh + row * p.ldo * XS;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const v8f h = value8(hr[i]), g = value8(gr[i]);
+      v8f d = value8(dr[i]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        dw[i][k] = __builtin_fmaf(g[k] * s, h[k], dw[i][k]);
+        d[k] += __builtin_fmaf(g[k] * w[i][k], s, -(h[k] * f));
+      }
+      store8<T>(op, (int64_t)(i * TPR + t) * 8, p.cols, d);
     }
   }
   if (!p.partial) return;
@@ -317,7 +338,7 @@ void grad_cols(const NormGradParams& p, int grid, hipStream_t s) {
   else if (p.cols <= 1024) grad<T, 64, 2>(p, grid, s);
   else if (p.cols <= 2048) grad<T, 256, 1>(p, grid, s);
   else if (p.cols <= 4096) grad<T, 256, 2>(p, grid, s);
-  else if (p.cols <= 8192) grad<T, 256, 4>(p, grid, s);
+  else if (p.cols <= 8192) grad<T, 512, 2>(p, grid, s);
   else grad<T, 1024, 2>(p, grid, s);
 }
 
