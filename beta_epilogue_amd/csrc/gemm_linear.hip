@@ -487,7 +487,8 @@ extern "C" int gemm_epi_linear_grad_create(const gemm_epi_linear_grad_desc* desc
     return fail(GEMM_EPI_ERR_UNSUPPORTED, "2^31 or more work items (tiles and K slices)");
   }
   const int64_t chunks = (d.M + h->chunk - 1) / h->chunk;
-  h->ws_a = d.dbias_dtype != GEMM_EPI_NONE && chunks > 1 ? up256(chunks * d.N * 4) : 0;
+  const bool sum_rows = d.act == GEMM_EPI_ACT_NONE && (da || db);
+  h->ws_a = d.dbias_dtype != GEMM_EPI_NONE && !sum_rows && chunks > 1 ? up256(chunks * d.N * 4) : 0;
   h->ws_b = h->ws_a + h->a.slots(h->tile);
   h->ws_bytes = h->ws_b + h->b.slots(h->tile);
   *out = h;
@@ -530,14 +531,16 @@ extern "C" int gemm_epi_linear_grad_run(const gemm_epi_linear_grad_handle* h, co
 
   hipStream_t s = (hipStream_t)stream;
   const int64_t chunks = (d.M + h->chunk - 1) / h->chunk;
-  float* partial = dbias && chunks > 1 ? (float*)workspace : nullptr;
+  const bool products = dA || dB;
+  const bool sum_rows = dbias && !act && products;  // the products' launch sums dD itself
+  float* partial = dbias && !sum_rows && chunks > 1 ? (float*)workspace : nullptr;
   (void)hipGetLastError();  // clear a stale error so the checks below are ours
-  if (act || dbias) {
+  if (act || (dbias && !sum_rows)) {
     launch_linear_dact(d.ab_dtype, d.act, dD, Z, dZ, partial, dbias, d.dbias_dtype, d.M, d.N, h->chunk, s);
     rc = launched();
     if (rc) return rc;
   }
-  if (!dA && !dB) {
+  if (!products) {
     if (partial) launch_colsum(partial, chunks, d.N, dbias, d.dbias_dtype, s);
     return launched();
   }
@@ -573,7 +576,8 @@ extern "C" int gemm_epi_linear_grad_run(const gemm_epi_linear_grad_handle* h, co
   p.ga = p.a.tiles_total;
   p.gb = p.b.tiles_total;
   p.partial = partial;
-  p.P = chunks;
+  p.rows = sum_rows ? dD : nullptr;
+  p.P = sum_rows ? d.M : chunks;
   p.C = d.N;
   p.dbias = dbias;
   p.dbias_dtype = d.dbias_dtype;

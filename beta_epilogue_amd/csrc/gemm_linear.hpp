@@ -41,8 +41,9 @@ void launch_linear_part(int variant, const LinParams& p, int grid, hipStream_t s
 // The backward's products, one launch for both:
 //   a: dA = dZ . B  (M x K over N: A = dZ K-major, B = B N-major)
 //   b: dB = dB_in + dZ^T . A  (N x K over M: A = dZ M-major, B = A N-major)
-// Workgroups 0 .. ga-1 run a, the next gb run b, the rest add the chunks'
-// column sums of dZ into dbias.  A problem that is not wanted has 0.
+// Workgroups 0 .. ga-1 run a, the next gb run b, the rest make dbias: of the
+// chunks' column sums in partial, or without an activation of dZ = dD itself.
+// A problem that is not wanted has 0.
 // Three kernels per type: 256x256 tiles; 128x128 tiles with two workgroups per
 // compute unit; 128x128 tiles with a ring of three stages, for grids of at most
 // one workgroup per compute unit, whose transposing reads have nobody else's
@@ -58,6 +59,7 @@ struct GradParams {
   LinParams a, b;
   int32_t ga, gb;
   const float* partial;  // [P][C], or NULL
+  const void* rows;      // [P][C] of type AB to be summed (NULL: none)
   int64_t P, C;
   void* dbias;
   int32_t dbias_dtype;

@@ -8,10 +8,10 @@
 //
 // Same re-layout through LDS as the one-type epilogue: a lane keeps the same
 // VEC columns through all passes, so bias[n] and alpha * scale_b[n] are read
-// once per tile into registers; residual and row scales are loaded four
-// passes ahead of their use.  The passes of a block run in a loop of four:
-// the five activations expanded in every pass of a tile would take several
-// times the 64 KiB instruction cache.  (A loop over the blocks as well makes
+// once per tile into registers; residual and row scales are loaded four or
+// eight passes ahead of their use.  With activations the passes of a large
+// tile's block run in a loop of four: the five expanded in every pass would
+// take several times the 64 KiB instruction cache.  (A loop over the blocks as well makes
 // the accumulators loop-carried, and they spill.)
 #pragma once
 
@@ -49,18 +49,21 @@ __device__ __forceinline__ void epilogue_linear(const LinParams& p, const ACC (&
   const __amdgpu_buffer_rsrc_t rsa = __builtin_amdgcn_make_buffer_rsrc(
       p.scale_a ? (void*)(p.scale_a + mw) : (void*)p.D, (short)0, p.scale_a ? (int)(lines * 4) : 0, 0x00020000);
 
-  // residual and row scales run UN passes ahead
-  constexpr int NP = NBLK * PASSES, UN = 4;
+  // The passes of a block run in a loop of UN, or unrolled where that stays
+  // small; residual and row scales run AHEAD passes ahead.
+  constexpr int NP = NBLK * PASSES;
+  constexpr int UN = CF::LIN_ACT && NBLK > 2 ? 4 : PASSES < 8 ? PASSES : 8;
+  constexpr int AHEAD = PASSES == UN ? (NP < 8 ? NP : 8) : UN;
   static_assert(PASSES % UN == 0, "passes in groups");
-  v4u res[UN];
-  float sa[UN];
+  v4u res[AHEAD];
+  float sa[AHEAD];
   auto fetch = [&](int pass, auto u_c) {
     constexpr int u = decltype(u_c)::value;
     if (p.R) res[u] = epi_ld<T>(rr, orr + (uint32_t)pass * sr);
     if (CF::LIN_ACT && p.scale_a)
       sa[u] = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rsa, (pass * LPP + sub) * 4, 0, 0));
   };
-  static_for<0, UN>([&](auto u_c) {
+  static_for<0, AHEAD>([&](auto u_c) {
     res[decltype(u_c)::value] = v4u{};
     sa[decltype(u_c)::value] = 1.0f;
     fetch(decltype(u_c)::value, u_c);
@@ -106,9 +109,10 @@ __device__ __forceinline__ void epilogue_linear(const LinParams& p, const ACC (&
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[i + j] = CF::INT ? (float)__float_as_int(w[j]) : w[j];
       }
-      const v4u r = res[u];
-      const float s = sa[u];
-      if (pass + UN < NP) fetch(pass + UN, u_c);
+      constexpr int slot = PASSES == UN ? (blk * PASSES + u) % AHEAD : u;
+      const v4u r = res[slot];
+      const float s = sa[slot];
+      if (pass + AHEAD < NP) fetch(pass + AHEAD, IntC<slot>{});
 #pragma unroll
       for (int i = 0; CF::LIN_ACT && i < VEC; ++i) v[i] = __builtin_fmaf(v[i], s * cs[i], bias[i]);
       auto pack = [&](const float (&x)[VEC]) {

@@ -213,22 +213,30 @@ __global__ __launch_bounds__(block_threads<TPR>()) void rmsnorm_kernel(NormParam
 // The backward: a workgroup walks rows blockIdx, blockIdx + grid, ... (RPB at
 // a time), keeps its weights and its part of dweight in registers, and leaves
 // one partial sum per column; colsum adds the workgroups in a fixed order.  The
-// next row is loaded before the sums of this one are joined (not with 1024
-// threads per row: 16 waves hide it by themselves, and the registers spill).
+// next row is loaded before the sums of this one are joined (8192 x 4096 bf16:
+// 68 us without, 41.5 with).  1024 threads have 128 registers each: their
+// weights stay in LDS.
 template <int T, int TPR, int NV>
 __global__ __launch_bounds__(block_threads<TPR>()) void rmsnorm_grad_kernel(NormGradParams p) {
   constexpr int RPB = block_threads<TPR>() / TPR;
   constexpr int XS = sizeof(typename Elem<T>::type);
-  constexpr bool AHEAD = TPR < 1024;
+  constexpr bool W_LDS = TPR == 1024;
   __shared__ float red[2][2 * (TPR / 64)];
   __shared__ float joined[RPB > 1 ? RPB * TPR * NV * 8 : 1];
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
-  v8f w[NV], dw[NV];
+  __shared__ v8f wl[W_LDS ? NV * TPR : 1];
+  v8f wr[W_LDS ? 1 : NV], dw[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    w[i] = load_weight8<T>(p.w, p.w_f32, (int64_t)(i * TPR + t) * 8, p.cols);
+    const v8f v = load_weight8<T>(p.w, p.w_f32, (int64_t)(i * TPR + t) * 8, p.cols);
+    if constexpr (W_LDS) wl[i * TPR + t] = v;  // read by this thread alone
+    else wr[i] = v;
     dw[i] = v8f{};
   }
+  auto weight = [&](int i) {
+    if constexpr (W_LDS) return wl[i * TPR + t];
+    else return wr[i];
+  };
   const float inv_cols = 1.0f / (float)p.cols;
   typedef typename Group<T>::type group;
   group h1[NV], g1[NV], d1[NV];
@@ -247,23 +255,22 @@ __global__ __launch_bounds__(block_threads<TPR>()) void rmsnorm_grad_kernel(Norm
   };
   const int64_t step = (int64_t)gridDim.x * RPB;
   int64_t row = (int64_t)blockIdx.x * RPB + sub;
-  if (AHEAD && row < p.rows) fetch(row);
+  if (row < p.rows) fetch(row);
   int flip = 0;
   for (; row < p.rows; row += step) {
-    if (!AHEAD) fetch(row);
     group hr[NV], gr[NV], dr[NV];
     float sums[2] = {0.0f, 0.0f};  // h^2, g w h
 #pragma unroll
     for (int i = 0; i < NV; ++i) hr[i] = h1[i], gr[i] = g1[i], dr[i] = d1[i];
     // (dH may be an input itself: only rows not yet written are read)
-    if (AHEAD && row + step < p.rows) fetch(row + step);
+    if (row + step < p.rows) fetch(row + step);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const v8f h = value8(hr[i]), g = value8(gr[i]);
+      const v8f h = value8(hr[i]), g = value8(gr[i]), w = weight(i);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         sums[0] = __builtin_fmaf(h[k], h[k], sums[0]);
-        sums[1] = __builtin_fmaf(g[k] * w[i][k], h[k], sums[1]);
+        sums[1] = __builtin_fmaf(g[k] * w[k], h[k], sums[1]);
       }
     }
     row_join<Sum, TPR>(sums, red[flip]);
@@ -273,12 +280,12 @@ __global__ __launch_bounds__(block_threads<TPR>()) void rmsnorm_grad_kernel(Norm
     char* op = (char*)p.dh + row * p.ldo * XS;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const v8f h = value8(hr[i]), g = value8(gr[i]);
+      const v8f h = value8(hr[i]), g = value8(gr[i]), w = weight(i);
       v8f d = value8(dr[i]);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         dw[i][k] = __builtin_fmaf(g[k] * s, h[k], dw[i][k]);
-        d[k] += __builtin_fmaf(g[k] * w[i][k], s, -(h[k] * f));
+        d[k] += __builtin_fmaf(g[k] * w[k], s, -(h[k] * f));
       }
       store8<T>(op, (int64_t)(i * TPR + t) * 8, p.cols, d);
     }
@@ -352,7 +359,8 @@ void launch_rmsnorm(int x_dtype, int y_dtype, const NormParams& p, hipStream_t s
 
 int rmsnorm_grad_grid(int64_t rows, int64_t cols, int cus) {
   const int64_t groups = cols <= 1024 ? (rows + 3) / 4 : rows;
-  const int64_t most = (int64_t)cus * (cols > 8192 ? 1 : 2);
+  // workgroups that a compute unit holds: short rows need more of them in flight
+  const int64_t most = (int64_t)cus * (cols > 8192 ? 1 : cols > 2048 ? 2 : 4);
   return (int)(groups < most ? groups : most);
 }
 

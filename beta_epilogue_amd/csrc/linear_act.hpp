@@ -11,9 +11,10 @@
 // exp(-a^2 / 2) and t = 1 / (1 + 0.36 a): P is a polynomial of degree 6 fitted
 // to Q / (E t) on [0, 14] by iteratively reweighted least squares of the
 // relative error (largest 8.8e-7; fp32 evaluation adds 3e-7), so the
-// far negative side keeps its relative precision.  Arguments are clamped to
-// |z| <= 20, where E is 0 in fp32, so an infinity times 0 does not arise; a
-// NaN passes the clamps (they compare).
+// far negative side keeps its relative precision.  The slopes clamp their
+// argument to |z| <= 20, where E is 0 in fp32, so an infinity times 0 does not
+// arise; a NaN passes the clamps (they compare).  z = -infinity gives NaN, as
+// -infinity * 0 in the formula, with gelu, gelu_tanh and silu.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -33,7 +34,7 @@ constexpr float kLog2e = 1.44269504088896340736f;
 // sigmoid(x) = 1 / (1 + exp(-x)); exp overflows to infinity, whose reciprocal is 0
 __device__ __forceinline__ float sigmoid(float x) { return rcp_hw(1.0f + exp2_hw(-kLog2e * x)); }
 
-// E = exp(-a^2 / 2) and Q = Phi(-a) for 0 <= a <= 20
+// E = exp(-a^2 / 2) and Q = Phi(-a) for a >= 0
 __device__ __forceinline__ void normal_tail(float a, float& E, float& Q) {
   E = exp2_hw(a * a * (-0.5f * kLog2e));
   const float t = rcp_hw(__builtin_fmaf(0.36f, a, 1.0f));
@@ -55,10 +56,9 @@ __device__ __forceinline__ float act_value(float z) {
   if constexpr (ACT == ACT_RELU) {
     return z < 0.0f ? 0.0f : z;
   } else if constexpr (ACT == ACT_GELU) {
-    float a = __builtin_fabsf(z), E, Q;
-    a = a > 20.0f ? 20.0f : a;
-    normal_tail(a, E, Q);
-    return __builtin_fmaf(-a, Q, z < 0.0f ? 0.0f : z);
+    float E, Q;
+    normal_tail(__builtin_fabsf(z), E, Q);
+    return z * (z > 0.0f ? 1.0f - Q : Q);
   } else if constexpr (ACT == ACT_GELU_TANH) {
     const float u = kTanhC * z * __builtin_fmaf(kTanhK * z, z, 1.0f);
     return z * sigmoid(2.0f * u);
