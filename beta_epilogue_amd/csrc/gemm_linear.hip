@@ -10,7 +10,6 @@
 
 #include "gemm_epi_host.hpp"
 #include "gemm_epi_linear.h"
-#include "gemm_epi_prep.hpp"
 #include "gemm_linear.hpp"
 
 using namespace gemm_epi;
@@ -44,6 +43,7 @@ struct LinearCost {
 };
 constexpr LinearCost kCost16 = {0.5, 2.9, 9.4, 2.8, 7.2, 1.02, 0.81, 0.72, 0.54, 0.755};
 constexpr LinearCost kCostE4m3 = {3.5, 4.0, 7.6, 3.9, 3.4, 1.13, 0.76, 0.55, 0.31, 0.31};
+constexpr LinearCost kCostWide = {3.0, 4.0, 9.4, 2.8, 7.2, 0.0, 0.0, 0.0, 0.8, 1.5};  // 128x128 only
 constexpr LinearCost kCostI8 = {4.35, 4.0, 7.7, 1.3, 5.1, 1.09, 0.84, 0.76, 0.56, 0.78};
 
 // Tiles of variant v: the first whole, the last `tail` in K slices of `kslice`.
@@ -69,7 +69,7 @@ LinearCut cut_linear(const LinearVariant& v, const gemm_epi_linear_desc& d, int6
 }
 
 double linear_time(const LinearVariant& v, const LinearCut& c, const gemm_epi_linear_desc& d, int64_t cus) {
-  const LinearCost& w = v.ab == T_E4M3 ? kCostE4m3 : v.ab == T_I8 ? kCostI8 : kCost16;
+  const LinearCost& w = v.ab == T_E4M3 ? kCostE4m3 : v.ab == T_I8 ? kCostI8 : v.ab == T_E4M3_WIDE ? kCostWide : kCost16;
   const double area = (double)v.bm * v.bn / 65536.0, epi = w.e0 + w.e1 * area;
   auto rounds = [&](int64_t items, int64_t k) {
     if (items == 0) return 0.0;
@@ -119,8 +119,7 @@ struct gemm_epi_linear_handle {
   int nw;                  // few rows: waves per workgroup
   int64_t tiles_m, tiles_n, tiles, tail, kslice, items;
   int splits, group_m;
-  bool widen;              // e4m3 runs as fp16 copies
-  int64_t prep_off, ws_bytes;
+  int64_t ws_bytes;
 };
 
 static int validate_linear(gemm_epi_linear_desc* d) {
@@ -139,7 +138,6 @@ static int validate_linear(gemm_epi_linear_desc* d) {
   if (!flag_ok(d->residual) || !flag_ok(d->z) || !flag_ok(d->scale_a) || !flag_ok(d->scale_b))
     return fail(GEMM_EPI_ERR_INVALID_ARG, "residual, z, scale_a and scale_b must be 0 or 1");
   if (d->splits < 0) return fail(GEMM_EPI_ERR_INVALID_ARG, "splits must be >= 0 (got %d)", d->splits);
-  // (e4m3 operands may be widened to two bytes)
   const int es = elem_bytes(d->ab_dtype), ds = elem_bytes(d->d_dtype);
   int rc = check_stride("a", &d->lda, d->K, es, true);
   if (!rc) rc = check_stride("b", &d->ldb, d->K, es, true);
@@ -147,8 +145,6 @@ static int validate_linear(gemm_epi_linear_desc* d) {
   if (!rc) rc = check_stride("r", &d->ldr, d->N, ds, d->residual);
   if (!rc) rc = check_stride("z", &d->ldz, d->N, ds, d->z);
   if (rc) return rc;
-  if (std::max(d->lda, d->ldb) >= (int64_t(1) << 31) / 256 / 2)
-    return fail(GEMM_EPI_ERR_UNSUPPORTED, "K too large for 31-bit tile offsets");
   // partial sums are fp32 rows of a tile; row and column numbers are 32-bit
   if (d->M >= (int64_t(1) << 31) - 512 || d->N >= (int64_t(1) << 31) - 512)
     return fail(GEMM_EPI_ERR_UNSUPPORTED, "M and N must be below 2^31 - 512");
@@ -166,8 +162,9 @@ extern "C" int gemm_epi_linear_create_variant(const gemm_epi_linear_desc* desc, 
   if (rc) return rc;
   if (variant < -1 || variant > kRowsVariant)
     return fail(GEMM_EPI_ERR_INVALID_ARG, "variant %d out of range", variant);
+  // (the fp8 MFMA sums a group of products with fewer bits than fp32 keeps)
   const bool widened = d.ab_dtype == GEMM_EPI_E4M3 && d.d_dtype == GEMM_EPI_F32;
-  const int kernel_ab = widened ? (int)GEMM_EPI_F16 : d.ab_dtype;
+  const int kernel_ab = widened ? (int)T_E4M3_WIDE : d.ab_dtype;
   if (variant == kRowsVariant ? d.M > kRowsMax : variant >= 0 && kLinear[variant].ab != kernel_ab)
     return fail(GEMM_EPI_ERR_UNSUPPORTED, "variant %s cannot run this problem", gemm_epi_linear_variant_name(variant));
   int device = 0, cus = 0;
@@ -224,10 +221,6 @@ extern "C" int gemm_epi_linear_create_variant(const gemm_epi_linear_desc* desc, 
   }
   h->grid = (int)std::min<int64_t>(h->items, (int64_t)cus * v.occ);
   h->ws_bytes = h->splits > 1 ? h->splits * h->tail * v.bm * v.bn * 4 : 0;
-  h->widen = widened;
-  h->prep_off = up256(h->ws_bytes);
-  // copies keep the row strides
-  if (widened) h->ws_bytes = h->prep_off + up256(d.M * d.lda * 2) + up256(d.N * d.ldb * 2);
   *out = h;
   return GEMM_EPI_OK;
 }
@@ -284,16 +277,6 @@ extern "C" int gemm_epi_linear_run(const gemm_epi_linear_handle* h, const void* 
     return launched();
   }
   const LinearVariant& v = kLinear[h->variant];
-  if (h->widen) {
-    // fp16 copies (exact) from the first row's first byte to the last row's
-    // last one; what lies between the rows is copied along and never used
-    uint16_t* wa = (uint16_t*)((char*)workspace + h->prep_off);
-    uint16_t* wb = (uint16_t*)((char*)wa + up256(d.M * d.lda * 2));
-    launch_f8_widen((const uint8_t*)A, (d.M - 1) * d.lda + d.K, false, wa, s);
-    launch_f8_widen((const uint8_t*)B, (d.N - 1) * d.ldb + d.K, false, wb, s);
-    p.A = wa;
-    p.B = wb;
-  }
   p.tiles_total = (int32_t)h->items;
   p.L = 1;
   p.tiles_m = (int32_t)h->tiles_m;

@@ -27,6 +27,29 @@ struct LinParams : Params {
   int32_t act;           // ACT_*
 };
 
+// e4m3 operands with an fp32 D: a fragment is widened to fp16 in registers
+// (exact; every e4m3 value is an fp16 value) and multiplied by fp16 MFMAs, whose
+// sums keep fp32's precision.  Which eight of a lane's sixteen k an MFMA takes
+// does not matter as long as both operands agree.
+enum : int { T_E4M3_WIDE = 15 };
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ v8h widen8(uint32_t a, uint32_t b) {
+  const v2h p0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, false);
+  const v2h p1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, true);
+  const v2h p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, false);
+  const v2h p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, true);
+  return v8h{p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
+}
+template <> struct Mma<T_E4M3_WIDE, 16> : MmaLayout16 {
+  typedef v4f acc_t;
+  typedef v4i frag_t;
+  static constexpr int ESIZE = 1, KSB = 64;
+  static __device__ __forceinline__ acc_t mma(frag_t a, frag_t b, acc_t c) {
+    c = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen8(a[0], a[1]), widen8(b[0], b[1]), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(widen8(a[2], a[3]), widen8(b[2], b[3]), c, 0, 0, 0);
+  }
+};
+
 // Tile kernels: K-major A and B, N-major D, 128-byte rows, 2 x 2 waves, S
 // stages, LIN arguments and epilogue.
 template <int AB, int BM, int BN, int S, int OCC, int BLK>

@@ -23,17 +23,6 @@ namespace gemm_epi {
 
 namespace {
 
-typedef _Float16 v2h __attribute__((ext_vector_type(2)));
-
-// Eight e4m3 values (two words) as fp16.
-__device__ __forceinline__ v8h widen8(uint32_t a, uint32_t b) {
-  const v2h p0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, false);
-  const v2h p1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, true);
-  const v2h p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, false);
-  const v2h p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, true);
-  return v8h{p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
-}
-
 // 16x16 blocks; a fragment is 16 bytes per lane (64 bytes of K per row).
 template <int AB> struct RowsMma {
   typedef v4f acc_t;

@@ -161,7 +161,8 @@ extern "C" int gemm_epi_rmsnorm_grad_create(const gemm_epi_rmsnorm_grad_desc* de
   if (!rc) rc = device_query(&device, &cus);
   if (rc) return rc;
   const int grid = rmsnorm_grad_grid(d.rows, d.cols, cus);
-  const int64_t ws = d.dweight_dtype == GEMM_EPI_NONE ? 0 : (int64_t)grid * d.cols * 4;
+  const bool direct = grid == 1 && d.dweight_dtype == GEMM_EPI_F32;  // the only workgroup's sums are dweight
+  const int64_t ws = d.dweight_dtype == GEMM_EPI_NONE || direct ? 0 : (int64_t)grid * d.cols * 4;
   gemm_epi_rmsnorm_grad_handle* h = new (std::nothrow) gemm_epi_rmsnorm_grad_handle{d, device, grid, ws};
   if (!h) return fail(GEMM_EPI_ERR_HOST_ALLOC, "out of host memory");
   *out = h;
@@ -198,7 +199,8 @@ extern "C" int gemm_epi_rmsnorm_grad_run(const gemm_epi_rmsnorm_grad_handle* h, 
   p.w = weight;
   p.dh_in = dH_in;
   p.dh = dH;
-  p.partial = dweight ? (float*)workspace : nullptr;
+  const bool direct = dweight && h->ws_bytes == 0;
+  p.partial = direct ? (float*)dweight : dweight ? (float*)workspace : nullptr;
   p.rows = d.rows;
   p.cols = d.cols;
   p.ldy = d.ldy;
@@ -210,7 +212,7 @@ extern "C" int gemm_epi_rmsnorm_grad_run(const gemm_epi_rmsnorm_grad_handle* h, 
   (void)hipGetLastError();  // clear a stale error so the checks below are ours
   launch_rmsnorm_grad(d.x_dtype, p, h->grid, (hipStream_t)stream);
   rc = launched();
-  if (rc || !dweight) return rc;
+  if (rc || !dweight || direct) return rc;
   launch_colsum(p.partial, h->grid, d.cols, dweight, d.dweight_dtype, (hipStream_t)stream);
   return launched();
 }

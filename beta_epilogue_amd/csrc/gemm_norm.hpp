@@ -28,7 +28,7 @@ struct NormGradParams {
   const void* w;
   const void* dh_in;  // gradient that reaches h by other ways, or NULL
   void* dh;
-  float* partial;     // [grid][cols] sums for dweight, or NULL
+  float* partial;     // [grid][cols] sums for dweight (grid 1: dweight), or NULL
   int64_t rows, cols;
   int64_t ldy, ldh, ldi, ldo;
   int32_t w_f32;

@@ -359,6 +359,9 @@ void launch_rmsnorm(int x_dtype, int y_dtype, const NormParams& p, hipStream_t s
 
 int rmsnorm_grad_grid(int64_t rows, int64_t cols, int cus) {
   const int64_t groups = cols <= 1024 ? (rows + 3) / 4 : rows;
+  // a few rows: one workgroup walks them, and its sums are the result (2 us a
+  // row against a second launch of 5)
+  if (groups <= 2) return 1;
   // workgroups that a compute unit holds: short rows need more of them in flight
   const int64_t most = (int64_t)cus * (cols > 8192 ? 1 : cols > 2048 ? 2 : 4);
   return (int)(groups < most ? groups : most);

@@ -19,8 +19,8 @@
  * Types: A and B fp16, bf16, e4m3 or int8 (one type); D, R and Z one type of
  * fp16, bf16, fp32.  Products are summed in fp32 (int8: int32), the epilogue
  * is fp32, and each output is rounded once, to nearest-even.  e4m3 with an
- * fp32 D runs on exact fp16 copies of A and B (in the workspace), as in
- * gemm_epi_create.  Scales are meant for the 8-bit types but allowed for all.
+ * fp32 D is widened (exactly) and runs on the fp16 matrix instructions, whose
+ * sums keep fp32's precision.  Scales are meant for the 8-bit types but allowed for all.
  *
  * Conventions as in gemm_epi.h: status codes and gemm_epi_last_error();
  * everything that needs no device is checked at create; contiguous extents
