@@ -30,21 +30,22 @@ constexpr int kTiles = (int)(sizeof kLinear / sizeof kLinear[0]);
 constexpr int kRowsVariant = kTiles;  // the few-row kernels, one entry
 constexpr int kThreads = 256;
 
-// The plan's cost model (us), fitted to forced plans of 75 shapes (M 90 to
-// 2048, N 1024 to 4096, K 1408 to 8192; 1 to 6 slices) per type: within 5 %
-// (fp16, bf16) and 8 % (8 bits) of the measured times.  An item (a tile or a K
-// slice of one) takes its K tiles times tk plus an epilogue of e0 + e1 * area
-// (in 256x256 tiles); rounds of items fill the compute units.  128x128 tiles
-// of which two share a compute unit take tk_pair together.  Slices add a
-// second launch, `join` us and their partial sums at bw TB/s.
+// The plan's cost model (us), fitted per type to 663 forced plans (11 shapes, M
+// 90 to 4096, N 1024 to 6528, K 512 to 8192; every tile, 1 to 6 slices): 6 to 9 %
+// rms from the measured times, and the plans that it chooses take 0 to 2 % longer
+// than the best measured ones.  An item (a tile or a K slice of one) takes its
+// K tiles times tk plus an epilogue of e0 + e1 * area (in 256x256 tiles); rounds
+// of items fill the compute units.  Smaller tiles of which two or three share a
+// compute unit take pair or three together.  Slices add a second launch, `join`
+// us and their partial sums at bw TB/s.
 struct LinearCost {
   double start, join, bw, e0, e1;
-  double tk256, tk192, tk128, tk_small, tk_pair;
+  double tk256, tk192, tk128x256, tk128, tk64, pair128, pair64, three64;
 };
-constexpr LinearCost kCost16 = {0.5, 2.9, 9.4, 2.8, 7.2, 1.02, 0.81, 0.72, 0.54, 0.755};
-constexpr LinearCost kCostE4m3 = {3.5, 4.0, 7.6, 3.9, 3.4, 1.13, 0.76, 0.55, 0.31, 0.31};
-constexpr LinearCost kCostWide = {3.0, 4.0, 9.4, 2.8, 7.2, 0.0, 0.0, 0.0, 0.8, 1.5};  // 128x128 only
-constexpr LinearCost kCostI8 = {4.35, 4.0, 7.7, 1.3, 5.1, 1.09, 0.84, 0.76, 0.56, 0.78};
+constexpr LinearCost kCost16 = {3.465, 2.297, 10.97, 2.054, 6.275, 1.029, 0.828, 0.743, 0.517, 0.182, 0.78, 0.31, 0.0};
+constexpr LinearCost kCostE4m3 = {4.475, 2.042, 9.057, 1.92, 5.632, 1.138, 0.774, 0.586, 0.386, 0.146, 0.0, 0.277, 0.0};
+constexpr LinearCost kCostI8 = {4.458, 2.078, 9.178, 1.796, 5.074, 1.11, 0.866, 0.781, 0.556, 0.195, 0.858, 0.323, 0.454};
+constexpr LinearCost kCostWide = {4.276, 2.849, 8.637, 1.004, 7.77, 0.0, 0.0, 0.0, 0.812, 0.334, 1.401, 0.526, 0.0};
 
 // Tiles of variant v: the first whole, the last `tail` in K slices of `kslice`.
 struct LinearCut {
@@ -68,14 +69,26 @@ LinearCut cut_linear(const LinearVariant& v, const gemm_epi_linear_desc& d, int6
   return c;
 }
 
+// The few-row kernel's time (us): its waves stream runs of 256 bytes of K, and a
+// run costs its latency (first figure) or, with all compute units at work, its
+// share of the bandwidth and of the products (second); fitted at N and K of 512
+// to 8192, 16 and 8 bits, within 15 %.
+double rows_time(const gemm_epi_linear_desc& d, int64_t cus) {
+  const int64_t runs = (d.K * elem_bytes(d.ab_dtype) + 8 * 256 - 1) / (8 * 256), blocks = (d.N + 15) / 16;
+  const double per_cu = blocks < cus ? (double)blocks / (double)cus : (double)((blocks + cus - 1) / cus);
+  const double latency = d.M <= 32 ? 1.2 : 1.9, busy = d.M <= 32 ? 1.9 : d.M <= 48 ? 2.3 : 2.55;
+  return std::max(4.5 + (double)runs * latency, 3.0 + (double)runs * per_cu * busy);
+}
+
 double linear_time(const LinearVariant& v, const LinearCut& c, const gemm_epi_linear_desc& d, int64_t cus) {
   const LinearCost& w = v.ab == T_E4M3 ? kCostE4m3 : v.ab == T_I8 ? kCostI8 : v.ab == T_E4M3_WIDE ? kCostWide : kCost16;
   const double area = (double)v.bm * v.bn / 65536.0, epi = w.e0 + w.e1 * area;
   auto rounds = [&](int64_t items, int64_t k) {
     if (items == 0) return 0.0;
-    double tk = v.bm == 256 ? w.tk256 : v.bm == 192 ? w.tk192 : v.bn == 256 ? w.tk128 : w.tk_small;
+    double tk = v.bm == 256 ? w.tk256 : v.bm == 192 ? w.tk192 : v.bn == 256 ? w.tk128x256 : v.bm == 128 ? w.tk128 : w.tk64;
     int64_t slots = cus;
-    if (v.occ == 2 && items > cus) tk = w.tk_pair, slots = 2 * cus;
+    if (v.occ >= 2 && items > cus) tk = v.bm == 128 ? w.pair128 : w.pair64, slots = 2 * cus;
+    if (v.occ >= 3 && items > 2 * cus) tk = w.three64, slots = 3 * cus;
     return (double)((items + slots - 1) / slots) * (tk * (double)((k + v.bk - 1) / v.bk) + epi);
   };
   double t = w.start + rounds(c.tiles - c.tail, d.K) + rounds(c.tail * c.splits, std::min(c.kslice, d.K));
@@ -172,7 +185,6 @@ extern "C" int gemm_epi_linear_create_variant(const gemm_epi_linear_desc* desc, 
   if (rc) return rc;
 
   LinearCut best = {};
-  if (variant == -1 && d.M <= kRowsMax) variant = kRowsVariant;
   if (variant != kRowsVariant) {
     // the tile shape and K split of the lowest modelled time
     const int forced = variant;
@@ -182,9 +194,14 @@ extern "C" int gemm_epi_linear_create_variant(const gemm_epi_linear_desc* desc, 
       for (int64_t s = d.splits ? d.splits : 1; s <= (d.splits ? d.splits : 16); ++s) {
         const LinearCut c = cut_linear(kLinear[i], d, s, d.splits != 0, cus);
         const double us = linear_time(kLinear[i], c, d, cus);
-        if (variant == -1 || best.tiles == 0 || us < best_us) best_us = us, best = c, variant = i;
+        if (best.tiles == 0 || us < best_us) best_us = us, best = c, variant = i;
       }
     }
+    // few rows: up to 16 always (the tiles would be mostly empty), up to 64
+    // where the model says so (32 bf16 rows: N = K = 4096 11 us against 17 as
+    // tiles, 8192 38 against 29)
+    if (forced == -1 && d.splits == 0 && (d.M <= 16 || (d.M <= kRowsMax && rows_time(d, cus) < best_us)))
+      variant = kRowsVariant;
   }
 
   gemm_epi_linear_handle* h = new (std::nothrow) gemm_epi_linear_handle();

@@ -61,15 +61,16 @@ typedef struct gemm_epi_linear_desc {
   int32_t z;            /* 1: Z is written */
   int32_t scale_a;      /* 1: M fp32 row scales */
   int32_t scale_b;      /* 1: N fp32 column scales */
-  int32_t splits;       /* K split, as in gemm_epi_desc (ignored for few rows) */
+  int32_t splits;       /* 0: the plan's choice; n: a tile kernel with every
+                           tile in n K slices (fewer if K has fewer K tiles) */
 } gemm_epi_linear_desc;
 
 typedef struct gemm_epi_linear_handle gemm_epi_linear_handle;
 
 /*
- * Validate a problem and plan it.  With M of at most 64 the plan is the
- * few-row kernel, which streams B once; otherwise a tile kernel, whose tile
- * shape and K split a cost model chooses.  INVALID_ARG: sizes, codes,
+ * Validate a problem and plan it: the few-row kernel, which streams B once (M
+ * of at most 16, and up to 64 where a cost model prefers it), or a tile kernel
+ * whose tile shape and K split the model chooses.  INVALID_ARG: sizes, codes,
  * flags other than 0 and 1, strides below the extent, a stride of a tensor
  * that is not used.  ALIGNMENT: the 16-byte rule.  UNSUPPORTED: e5m2 and uint8;
  * rows or row strides too long for the kernels' 31-bit tile offsets; 2^31 or
