@@ -14,8 +14,7 @@
 // those of the outputs (y and h are both rounded from the fp32 values).
 // Groups of 8 are loaded and stored as 16-byte (8-bit: 8-byte) accesses at
 // element alignment (gfx950 takes unaligned global accesses), so odd row
-// lengths and strides run the same path; a group that the row's end cuts is
-// moved element by element.
+// lengths and strides run the same path.
 #include "gemm_norm.hpp"
 
 #include "gemm_epi_kernel.hpp"
@@ -43,36 +42,63 @@ __device__ __forceinline__ v8f value8(G g) {
   return __builtin_convertvector(g, v8f);
 }
 
-// Elements [c, c + 8) of a row that ends at cols; 0 past its end.
+// A thread's group of a row.  The group that the row's end cuts, and those past
+// it, lie on the row's last 8 elements, of which the first `dead` belong to other
+// threads: they are loaded with the rest, count as 0 and are not stored.  So a
+// load is one access without a branch, and the loads of all tensors are in
+// flight together (backward of 14545 rows of 2461 fp16: 134 us with the cut groups
+// loaded element by element, 70 so).  Rows of less than 8 elements are one group
+// with `live` of them.
+struct Span {
+  int64_t at;
+  int dead, live;  // elements [dead, live) are the thread's
+};
+__device__ __forceinline__ Span span_of(int64_t c, int64_t cols) {
+  if (cols < 8) return {0, c == 0 ? 0 : 8, (int)cols};
+  const int64_t at = c + 8 <= cols ? c : cols - 8;
+  return {at, (int)(c - at < 8 ? c - at : 8), 8};
+}
+__device__ __forceinline__ bool whole(const Span& g) { return g.dead == 0 && g.live == 8; }
+
+// The group's elements, the dead ones among them.
 template <int T>
-__device__ __forceinline__ typename Group<T>::type load8(const void* row, int64_t c, int64_t cols) {
-  const typename Elem<T>::type* p = (const typename Elem<T>::type*)row + c;
+__device__ __forceinline__ typename Group<T>::type load8(const void* row, const Span& g) {
+  const typename Elem<T>::type* p = (const typename Elem<T>::type*)row + g.at;
   typename Group<T>::type v = {};
-  if (c + 8 <= cols) {
+  if (g.live == 8) {  // (the same for all threads)
     v = *(const typename Group<T>::any*)p;
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (c + k < cols) v[k] = p[k];
+    for (int k = 0; k < 7; ++k)
+      if (k < g.live) v[k] = p[k];
   }
   return v;
 }
 
-template <int T>
-__device__ __forceinline__ void store8(void* row, int64_t c, int64_t cols, v8f v) {
-  typename Elem<T>::type* p = (typename Elem<T>::type*)row + c;
-  if (c + 8 <= cols) {
-    *(typename Group<T>::any*)p = __builtin_convertvector(v, typename Group<T>::type);
-  } else {
+// 0 in the dead places.
+template <class V>
+__device__ __forceinline__ void bury(const Span& g, V& v) {
+  if (g.dead) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (c + k < cols) p[k] = (typename Elem<T>::type)v[k];
+    for (int k = 0; k < 8; ++k) v[k] = k < g.dead ? 0 : v[k];
   }
 }
 
 template <int T>
-__device__ __forceinline__ v8f load_weight8(const void* w, bool f32, int64_t c, int64_t cols) {
-  return f32 ? load8<T_F32>(w, c, cols) : value8(load8<T>(w, c, cols));
+__device__ __forceinline__ void store8(void* row, const Span& g, v8f v) {
+  typename Elem<T>::type* p = (typename Elem<T>::type*)row + g.at;
+  if (whole(g)) {
+    *(typename Group<T>::any*)p = __builtin_convertvector(v, typename Group<T>::type);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k >= g.dead && k < g.live) p[k] = (typename Elem<T>::type)v[k];
+  }
+}
+
+template <int T>
+__device__ __forceinline__ v8f load_weight8(const void* w, bool f32, const Span& g) {
+  return f32 ? load8<T_F32>(w, g) : value8(load8<T>(w, g));
 }
 
 // Rounds to nearest-even into 8 bits and stores: values of at most QMAX (1 + 2^-21),
@@ -81,7 +107,7 @@ __device__ __forceinline__ v8f load_weight8(const void* w, bool f32, int64_t c, 
 // integer in the low byte of the sum.  TX is the inputs' type: a NaN that comes
 // from 16-bit values has zeros there already.
 template <int T, int TX>
-__device__ __forceinline__ void store8_q(void* row, int64_t c, int64_t cols, v8f v) {
+__device__ __forceinline__ void store8_q(void* row, const Span& g, v8f v) {
   uint32_t w[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
@@ -100,13 +126,13 @@ __device__ __forceinline__ void store8_q(void* row, int64_t c, int64_t cols, v8f
       w[j] = __builtin_amdgcn_perm(hi, lo, 0x05040100u);
     }
   }
-  uint8_t* p = (uint8_t*)row + c;
-  if (c + 8 <= cols) {
+  uint8_t* p = (uint8_t*)row + g.at;
+  if (whole(g)) {
     *(v2u_any*)p = v2u{w[0], w[1]};
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      if (c + k < cols) p[k] = (uint8_t)(w[k / 4] >> (8 * (k % 4)));
+      if (k >= g.dead && k < g.live) p[k] = (uint8_t)(w[k / 4] >> (8 * (k % 4)));
   }
 }
 
@@ -157,15 +183,25 @@ __global__ __launch_bounds__(block_threads<TPR>()) void rmsnorm_kernel(NormParam
   constexpr int XS = sizeof(typename Elem<TX>::type);
   const char* x = (const char*)p.x + row * p.ldx * XS;
   const char* r = p.r ? (const char*)p.r + row * p.ldr * XS : nullptr;
+  Span at[NV];
+  typename Group<TX>::type xg[NV], rg[NV];
   v8f h[NV], w[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int64_t c = (int64_t)(i * TPR + t) * 8;
-    h[i] = value8(load8<TX>(x, c, p.cols));
-    if (r) h[i] += value8(load8<TX>(r, c, p.cols));
+    at[i] = span_of((int64_t)(i * TPR + t) * 8, p.cols);
+    xg[i] = load8<TX>(x, at[i]);
+    rg[i] = typename Group<TX>::type{};
+    if (r) rg[i] = load8<TX>(r, at[i]);
   }
 #pragma unroll
-  for (int i = 0; i < NV; ++i) w[i] = load_weight8<TX>(p.w, p.w_f32, (int64_t)(i * TPR + t) * 8, p.cols);
+  for (int i = 0; i < NV; ++i) w[i] = load_weight8<TX>(p.w, p.w_f32, at[i]);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    h[i] = value8(xg[i]);
+    if (r) h[i] += value8(rg[i]);
+    bury(at[i], h[i]);
+    bury(at[i], w[i]);
+  }
   float ss[1] = {0.0f};
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -175,7 +211,7 @@ __global__ __launch_bounds__(block_threads<TPR>()) void rmsnorm_kernel(NormParam
   if (p.h) {
     char* ho = (char*)p.h + row * p.ldh * XS;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) store8<TX>(ho, (int64_t)(i * TPR + t) * 8, p.cols, h[i]);
+    for (int i = 0; i < NV; ++i) store8<TX>(ho, at[i], h[i]);
   }
   row_join<Sum, TPR>(ss, red);
   const float s = 1.0f / __builtin_sqrtf(ss[0] / (float)p.cols + p.eps);
@@ -201,12 +237,12 @@ __global__ __launch_bounds__(block_threads<TPR>()) void rmsnorm_kernel(NormParam
     }
     uint8_t* y = (uint8_t*)p.y + row * p.ldy;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) store8_q<TY, TX>(y, (int64_t)(i * TPR + t) * 8, p.cols, h[i] * f);
+    for (int i = 0; i < NV; ++i) store8_q<TY, TX>(y, at[i], h[i] * f);
     if (t == 0) p.scale[row] = scale;
   } else {
     char* y = (char*)p.y + row * p.ldy * XS;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) store8<TX>(y, (int64_t)(i * TPR + t) * 8, p.cols, h[i] * s);
+    for (int i = 0; i < NV; ++i) store8<TX>(y, at[i], h[i] * s);
   }
 }
 
@@ -215,20 +251,24 @@ __global__ __launch_bounds__(block_threads<TPR>()) void rmsnorm_kernel(NormParam
 // one partial sum per column; colsum adds the workgroups in a fixed order.  The
 // next row is loaded before the sums of this one are joined (8192 x 4096 bf16:
 // 68 us without, 41.5 with).  1024 threads have 128 registers each: their
-// weights stay in LDS.
+// weights stay in LDS, and an fp32 dh_in is loaded with its own row.
 template <int T, int TPR, int NV>
 __global__ __launch_bounds__(block_threads<TPR>()) void rmsnorm_grad_kernel(NormGradParams p) {
   constexpr int RPB = block_threads<TPR>() / TPR;
   constexpr int XS = sizeof(typename Elem<T>::type);
   constexpr bool W_LDS = TPR == 1024;
+  constexpr bool D_AHEAD = !(W_LDS && T == T_F32);
   __shared__ float red[2][2 * (TPR / 64)];
   __shared__ float joined[RPB > 1 ? RPB * TPR * NV * 8 : 1];
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
   __shared__ v8f wl[W_LDS ? NV * TPR : 1];
   v8f wr[W_LDS ? 1 : NV], dw[NV];
+  Span at[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const v8f v = load_weight8<T>(p.w, p.w_f32, (int64_t)(i * TPR + t) * 8, p.cols);
+    at[i] = span_of((int64_t)(i * TPR + t) * 8, p.cols);
+    v8f v = load_weight8<T>(p.w, p.w_f32, at[i]);
+    bury(at[i], v);
     if constexpr (W_LDS) wl[i * TPR + t] = v;  // read by this thread alone
     else wr[i] = v;
     dw[i] = v8f{};
@@ -240,18 +280,23 @@ __global__ __launch_bounds__(block_threads<TPR>()) void rmsnorm_grad_kernel(Norm
   const float inv_cols = 1.0f / (float)p.cols;
   typedef typename Group<T>::type group;
   group h1[NV], g1[NV], d1[NV];
-  auto fetch = [&](int64_t row) {
-    const char* hp = (const char*)p.h + row * p.ldh * XS;
-    const char* gp = (const char*)p.dy + row * p.ldy * XS;
+  auto fetch_in = [&](int64_t row, group (&d)[NV]) {
     const char* ip = p.dh_in ? (const char*)p.dh_in + row * p.ldi * XS : nullptr;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int64_t c = (int64_t)(i * TPR + t) * 8;
-      h1[i] = load8<T>(hp, c, p.cols);
-      g1[i] = load8<T>(gp, c, p.cols);
-      d1[i] = group{};
-      if (ip) d1[i] = load8<T>(ip, c, p.cols);
+      d[i] = group{};
+      if (ip) d[i] = load8<T>(ip, at[i]);
     }
+  };
+  auto fetch = [&](int64_t row) {
+    const char* hp = (const char*)p.h + row * p.ldh * XS;
+    const char* gp = (const char*)p.dy + row * p.ldy * XS;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      h1[i] = load8<T>(hp, at[i]);
+      g1[i] = load8<T>(gp, at[i]);
+    }
+    if constexpr (D_AHEAD) fetch_in(row, d1);
   };
   const int64_t step = (int64_t)gridDim.x * RPB;
   int64_t row = (int64_t)blockIdx.x * RPB + sub;
@@ -261,8 +306,14 @@ __global__ __launch_bounds__(block_threads<TPR>()) void rmsnorm_grad_kernel(Norm
     group hr[NV], gr[NV], dr[NV];
     float sums[2] = {0.0f, 0.0f};  // h^2, g w h
 #pragma unroll
-    for (int i = 0; i < NV; ++i) hr[i] = h1[i], gr[i] = g1[i], dr[i] = d1[i];
+    for (int i = 0; i < NV; ++i) {
+      hr[i] = h1[i], gr[i] = g1[i];
+      if constexpr (D_AHEAD) dr[i] = d1[i];
+      bury(at[i], hr[i]);
+      bury(at[i], gr[i]);
+    }
     // (dH may be an input itself: only rows not yet written are read)
+    if constexpr (!D_AHEAD) fetch_in(row, dr);
     if (row + step < p.rows) fetch(row + step);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -287,7 +338,7 @@ __global__ __launch_bounds__(block_threads<TPR>()) void rmsnorm_grad_kernel(Norm
         dw[i][k] = __builtin_fmaf(g[k] * s, h[k], dw[i][k]);
         d[k] += __builtin_fmaf(g[k] * w[k], s, -(h[k] * f));
       }
-      store8<T>(op, (int64_t)(i * TPR + t) * 8, p.cols, d);
+      store8<T>(op, at[i], d);
     }
   }
   if (!p.partial) return;
@@ -296,7 +347,8 @@ __global__ __launch_bounds__(block_threads<TPR>()) void rmsnorm_grad_kernel(Norm
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) joined[(sub * NV * TPR + i * TPR + t) * 8 + k] = dw[i][k];
+      for (int k = 0; k < 8; ++k)
+        if (k >= at[i].dead && k < at[i].live) joined[sub * NV * TPR * 8 + (int)at[i].at + k] = dw[i][k];
     __syncthreads();
     for (int c = threadIdx.x; c < p.cols; c += block_threads<TPR>()) {
       float v = joined[c];
@@ -306,7 +358,7 @@ __global__ __launch_bounds__(block_threads<TPR>()) void rmsnorm_grad_kernel(Norm
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) store8<T_F32>(out, (int64_t)(i * TPR + t) * 8, p.cols, dw[i]);
+    for (int i = 0; i < NV; ++i) store8<T_F32>(out, at[i], dw[i]);
   }
 }
 
