@@ -27,7 +27,7 @@ GEMM_EPI_PARTS = 16
 LINEAR_PART_SOURCE = os.path.join(CSRC, "gemm_linear_part.hip")
 GEMM_LINEAR_PARTS = 8
 LINEAR_GRAD_MM_SOURCE = os.path.join(CSRC, "gemm_linear_grad_mm.hip")
-GEMM_LINEAR_GRAD_PARTS = 6
+GEMM_LINEAR_GRAD_PARTS = 8
 LINEAR_SOURCES = [os.path.join(CSRC, f) for f in ("gemm_linear.hip", "gemm_linear_rows.hip", "gemm_linear_grad.hip",
                                                   "gemm_norm.hip", "gemm_norm_kernels.hip")]
 SOURCES = [MAIN_SOURCE, PART_SOURCE, SPLITK_SOURCE, PREP_SOURCE, LINEAR_PART_SOURCE, LINEAR_GRAD_MM_SOURCE] + LINEAR_SOURCES

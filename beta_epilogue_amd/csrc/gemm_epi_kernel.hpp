@@ -466,7 +466,7 @@ struct KMajorOperand {
 // Out-of-range rows read as zero: the buffer's extent ends at the end of K,
 // and a chunk past M (N) gets an out-of-range offset.
 // ---------------------------------------------------------------------------
-template <class CF>
+template <class CF, int CPR>  // CPR: chunks per k-row
 struct MNSwizzle {
   // XOR applied to the chunk index of k-row k, chosen so that the chunks
   // read by one half-wave (32 lanes, one LDS cycle of 8-byte reads) hit 16
@@ -475,15 +475,20 @@ struct MNSwizzle {
   //   2-byte, 32x32 blocks: k-rows {0..3} (+4), 4 chunks each;
   //   1-byte, 16x16 blocks, 16 B per lane: k-rows {0..7, 16..23} (+8), 1 chunk;
   //   1-byte, 32x32 blocks: k-rows {0..7} (+8), 2 chunks each.
+  // k-rows of 8 chunks (64 2-byte elements, 32x32 blocks) lie two to a pass of
+  // the banks, so only every second pair has to move.
+  static_assert(CPR >= 16 || (CPR == 8 && CF::MM::ESIZE == 2 && CF::BLK == 32), "layouts that are worked out");
   static constexpr __host__ __device__ int of(int k) {
-    if constexpr (CF::MM::ESIZE == 2)
+    if constexpr (CPR == 8)
+      return 4 * ((k >> 1) & 1);
+    else if constexpr (CF::MM::ESIZE == 2)
       return CF::BLK == 16 ? 2 * ((k & 3) | ((k >> 1) & 4)) : 4 * (k & 3);
     else if constexpr (CF::BLK == 32)
       return 2 * (k & 7);
     else
       return (k & 7) | ((k >> 1) & 8);
   }
-  static constexpr int MAX = 15;
+  static constexpr int MAX = CPR == 8 ? 7 : 15;
   // of(k) == of(k + step) for every k
   static constexpr bool periodic(int step) {
     for (int k = 0; k < 256; ++k)
@@ -501,7 +506,7 @@ struct MNMajorOperand {
   static constexpr int RPI = 1024 / RB;   // k-rows per wave instruction
   static constexpr int NQ = BK / (RPI * CF::NW);
   static_assert(RPI * RB == 1024 && NQ * RPI * CF::NW == BK, "k-rows must split evenly over the waves");
-  static_assert(CPR > MNSwizzle<CF>::MAX, "the swizzle stays inside a k-row");
+  static_assert(CPR > MNSwizzle<CF, CPR>::MAX, "the swizzle stays inside a k-row");
   static constexpr int E = 8 / ES;              // k per lane and transposing read
   static constexpr int KPL = CF::BPL / ES;      // k per lane and step
   static constexpr int NR = KPL / E;            // transposing reads per fragment
@@ -511,7 +516,7 @@ struct MNMajorOperand {
   // i & 1 (instructions are NW*RPI k-rows apart, a multiple of 8), so two
   // per-lane offsets serve them all; the rest of the step is a scalar.
   static constexpr int NV = NQ < 2 ? NQ : 2;
-  static_assert(MNSwizzle<CF>::periodic(2 * CF::NW * RPI), "two offset patterns cover every instruction");
+  static_assert(MNSwizzle<CF, CPR>::periodic(2 * CF::NW * RPI), "two offset patterns cover every instruction");
   v4i rsrc;
   uint32_t voff[NV];
   uint32_t kstride;  // bytes of one K tile in global memory
@@ -529,7 +534,7 @@ struct MNMajorOperand {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int krow = (i * CF::NW + wave) * RPI + lane / CPR;
-      const int lc = (lane % CPR) ^ MNSwizzle<CF>::of(krow);
+      const int lc = (lane % CPR) ^ MNSwizzle<CF, CPR>::of(krow);
       voff[i] = (int64_t)r0 + lc * (16 / ES) < extent ? (uint32_t)(krow * ldb + lc * 16) : 0x80000000u;
     }
   }
@@ -545,7 +550,7 @@ struct MNMajorOperand {
     const int roff = CF::BLK == 16 ? 0 : (b & 1) * 16;  // rows of the block's half
     const int krow = q * KPL + i16 / LPR;               // + s*KK + h*E at read time
     const int rbyte = (rbase + roff + (i16 % LPR) * E) * ES;
-    raddr = krow * RB + (((rbyte >> 4) ^ MNSwizzle<CF>::of(krow)) << 4) + (rbyte & 15);
+    raddr = krow * RB + (((rbyte >> 4) ^ MNSwizzle<CF, CPR>::of(krow)) << 4) + (rbyte & 15);
   }
   template <int Q, bool GUARD>
   __device__ __forceinline__ void issue_one(uint32_t sbase, int k_tile, int) {

@@ -381,22 +381,24 @@ void cut(GradProduct* p, int tile, int64_t splits) {
   p->splits = (int)((p->K + p->kslice - 1) / p->kslice);
 }
 
-// Modelled time (us) of the launch and the join, from forced runs of seven
-// shapes (M 64 to 6385): an item takes 1.1 us per K tile with 256x256 tiles and
-// 0.45 with 128x128 ones, or 0.85 for two that share a compute unit, and 8 or 4
-// us besides.
+// Modelled time (us) of the launch and the join, from forced runs of 40 shapes
+// (M 1 to 6385, N and K 256 to 4096): an item takes 1.1 us per K tile with 256x256
+// tiles, 0.45 with 128x128 and 0.16 with 64x64 ones, or 0.85 and 0.36 for two
+// that share a compute unit, and 8, 4 or 2 us besides.  The plans that it
+// chooses take up to 7 % longer than the best forced ones, 12 % at worst.
 double grad_time(const GradProduct& a, const GradProduct& b, int tile, int cus) {
   const double items = (double)(a.items() + b.items());
-  const bool pairs = tile == 128 && items > cus;
+  const bool pairs = tile != 256 && items > cus;
   const double slots = pairs ? 2.0 * cus : cus;
-  const double tk = tile == 256 ? 1.1 : pairs ? 0.85 : 0.45, fixed = tile == 256 ? 8.0 : 4.0;
+  const double tk = tile == 256 ? 1.1 : tile == 128 ? (pairs ? 0.85 : 0.45) : (pairs ? 0.36 : 0.16);
+  const double fixed = tile == 256 ? 8.0 : tile == 128 ? 4.0 : 2.0;
   double longest = 0.0, total = 0.0, join = 0.0;
   for (const GradProduct* p : {&a, &b}) {
     if (!p->on) continue;
     const double item = fixed + tk * (double)((std::min(p->kslice, p->K) + kGradKTile - 1) / kGradKTile);
     longest = std::max(longest, item);
     total += item * (double)p->items();
-    if (p->splits > 1) join = std::max(join, 4.0) + 2.0 * (double)p->slots(tile) / 5.0e6;
+    if (p->splits > 1) join = std::max(join, 5.0) + 2.0 * (double)p->slots(tile) / 5.0e6;
   }
   return (items <= slots ? longest : total / slots + 0.5 * longest) + join;
 }
@@ -431,8 +433,8 @@ extern "C" int gemm_epi_linear_grad_create(const gemm_epi_linear_grad_desc* desc
       return fail(GEMM_EPI_ERR_INVALID_ARG, "a gradient's type must be NONE, F16, BF16 or F32");
   if (d.da_dtype == GEMM_EPI_NONE && d.db_dtype == GEMM_EPI_NONE && d.dbias_dtype == GEMM_EPI_NONE)
     return fail(GEMM_EPI_ERR_INVALID_ARG, "no gradient is wanted");
-  if (d.tile != 0 && d.tile != 128 && d.tile != 256)
-    return fail(GEMM_EPI_ERR_INVALID_ARG, "tile must be 0, 128 or 256 (got %d)", d.tile);
+  if (d.tile != 0 && d.tile != 64 && d.tile != 128 && d.tile != 256)
+    return fail(GEMM_EPI_ERR_INVALID_ARG, "tile must be 0, 64, 128 or 256 (got %d)", d.tile);
   if (d.splits < 0) return fail(GEMM_EPI_ERR_INVALID_ARG, "splits must be >= 0 (got %d)", d.splits);
   const bool da = d.da_dtype != GEMM_EPI_NONE, db = d.db_dtype != GEMM_EPI_NONE;
   // every extent below 2^31 - 512 first, so that no product below overflows
@@ -471,7 +473,7 @@ extern "C" int gemm_epi_linear_grad_create(const gemm_epi_linear_grad_desc* desc
   h->b.on = db;
   h->b.M = d.N, h->b.N = d.K, h->b.K = d.M;
   double best = 0.0;
-  for (const int tile : {256, 128}) {
+  for (const int tile : {256, 128, 64}) {
     if (d.tile != 0 && d.tile != tile) continue;
     for (int64_t sa = 1; sa <= (da && !d.splits ? 16 : 1); ++sa)
       for (int64_t sb = 1; sb <= (db && !d.splits ? 16 : 1); ++sb) {
@@ -581,10 +583,12 @@ extern "C" int gemm_epi_linear_grad_run(const gemm_epi_linear_grad_handle* h, co
   p.C = d.N;
   p.dbias = dbias;
   p.dbias_dtype = d.dbias_dtype;
-  const int kind = h->tile == 256 ? GRAD_256 : p.ga + p.gb > h->cus ? GRAD_128 : GRAD_128_DEEP;
+  const int kind = h->tile == 256 ? GRAD_256 : h->tile == 64 ? GRAD_64 : p.ga + p.gb > h->cus ? GRAD_128 : GRAD_128_DEEP;
   static void (*const kLaunch[2][kGradKinds])(const GradParams&, hipStream_t) = {
-      {launch_linear_grad_mm<T_F16, 0>, launch_linear_grad_mm<T_F16, 1>, launch_linear_grad_mm<T_F16, 2>},
-      {launch_linear_grad_mm<T_BF16, 0>, launch_linear_grad_mm<T_BF16, 1>, launch_linear_grad_mm<T_BF16, 2>}};
+      {launch_linear_grad_mm<T_F16, 0>, launch_linear_grad_mm<T_F16, 1>, launch_linear_grad_mm<T_F16, 2>,
+       launch_linear_grad_mm<T_F16, 3>},
+      {launch_linear_grad_mm<T_BF16, 0>, launch_linear_grad_mm<T_BF16, 1>, launch_linear_grad_mm<T_BF16, 2>,
+       launch_linear_grad_mm<T_BF16, 3>}};
   kLaunch[d.ab_dtype == GEMM_EPI_BF16][kind](p, s);
   rc = launched();
   if (rc || (p.a.tail_tiles == 0 && p.b.tail_tiles == 0)) return rc;

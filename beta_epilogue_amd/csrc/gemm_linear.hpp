@@ -67,17 +67,23 @@ void launch_linear_part(int variant, const LinParams& p, int grid, hipStream_t s
 // Workgroups 0 .. ga-1 run a, the next gb run b, the rest make dbias: of the
 // chunks' column sums in partial, or without an activation of dZ = dD itself.
 // A problem that is not wanted has 0.
-// Three kernels per type: 256x256 tiles; 128x128 tiles with two workgroups per
+// Four kernels per type: 256x256 tiles; 128x128 tiles with two workgroups per
 // compute unit; 128x128 tiles with a ring of three stages, for grids of at most
 // one workgroup per compute unit, whose transposing reads have nobody else's
 // MFMAs to hide behind (dA of 64 x 4096 x 4096 37.7 -> 25.5 us; with 512 tiles,
-// 2048^3, the pair takes 35 us and the deep ring 39).
-enum : int { GRAD_256 = 0, GRAD_128 = 1, GRAD_128_DEEP = 2, kGradKinds = 3 };
-constexpr int grad_tile(int kind) { return kind == GRAD_256 ? 256 : 128; }
-constexpr int grad_occ(int kind) { return kind == GRAD_128 ? 2 : 1; }  // workgroups per compute unit
+// 2048^3, the pair takes 35 us and the deep ring 39); 64x64 tiles, two per
+// compute unit with rings of four stages, for small problems, whose larger tiles
+// would leave compute units idle or need K slices and a join (134 x 1272 x 1336
+// 19.1 us with 128x128 tiles and 15.3 with these, 449 x 1952 x 1288 23.5 and
+// 21.9; 2048^3 44 and 65).
+enum : int { GRAD_256 = 0, GRAD_128 = 1, GRAD_128_DEEP = 2, GRAD_64 = 3, kGradKinds = 4 };
+constexpr int grad_tile(int kind) { return kind == GRAD_256 ? 256 : kind == GRAD_64 ? 64 : 128; }
+// Workgroups per compute unit.
+constexpr int grad_occ(int kind) { return kind == GRAD_128 || kind == GRAD_64 ? 2 : 1; }
+constexpr int grad_stages(int kind) { return kind == GRAD_128_DEEP ? 3 : kind == GRAD_64 ? 4 : 2; }
 template <int AB, bool A_KMAJOR, int KIND>
-using GradCfg = Cfg<AB, A_KMAJOR, false, true, grad_tile(KIND), grad_tile(KIND), 128, 2, 2,
-                    KIND == GRAD_128_DEEP ? 3 : 2, KIND == GRAD_256 ? 2 : 0, 32, 2, grad_occ(KIND)>;
+using GradCfg = Cfg<AB, A_KMAJOR, false, true, grad_tile(KIND), grad_tile(KIND), 128, 2, 2, grad_stages(KIND),
+                    KIND == GRAD_256 ? 2 : 0, 32, 2, grad_occ(KIND)>;
 struct GradParams {
   LinParams a, b;
   int32_t ga, gb;

@@ -1,6 +1,6 @@
 // gemm_linear_grad_mm.hip -- the two matrix products of the linear layer's
 // backward in one launch, compiled once per type and kernel
-// (GEMM_LINEAR_GRAD_PART 0 .. 5).
+// (GEMM_LINEAR_GRAD_PART 0 .. 7).
 //
 // dA = dZ . B and dB = dB_in + dZ^T . A read what the elementwise pass left
 // and do not depend on one another, so their tiles (and K slices) share a
@@ -14,7 +14,7 @@
 #include "gemm_linear.hpp"
 
 #ifndef GEMM_LINEAR_GRAD_PART
-#error "GEMM_LINEAR_GRAD_PART must be defined (0 .. 5)"
+#error "GEMM_LINEAR_GRAD_PART must be defined (0 .. 7)"
 #endif
 
 namespace gemm_epi {

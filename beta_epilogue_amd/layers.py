@@ -245,7 +245,7 @@ class FusedLinearGrad(_Plan):
     sums of dZ.  All tensors are packed; dD, Z, dZ, A and B have type ab (f16
     or bf16).  da, db, dbias: the gradients' types, None for one not wanted.
     Without an activation dD takes dZ's place and Z and dZ are not given.  The
-    residual's gradient is dD.  tile (128 or 256) and splits force the products'
+    residual's gradient is dD.  tile (64, 128 or 256) and splits force the products'
     tile and K split.
     """
 

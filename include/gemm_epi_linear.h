@@ -113,7 +113,7 @@ typedef struct gemm_epi_linear_grad_desc {
   int32_t da_dtype;    /* NONE (no dA), F16, BF16 or F32 */
   int32_t db_dtype;    /* NONE (no dB), F16, BF16 or F32: dB and dB_in */
   int32_t dbias_dtype; /* NONE (no dbias), F16, BF16 or F32 */
-  int32_t tile;        /* 0: the plan's choice; 128 or 256: that tile */
+  int32_t tile;        /* 0: the plan's choice; 64, 128 or 256: that tile */
   int32_t splits;      /* 0: the plan's choice; n: every tile of both products
                           in n K slices (fewer if K has fewer K tiles) */
 } gemm_epi_linear_grad_desc;

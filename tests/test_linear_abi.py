@@ -76,7 +76,7 @@ GRAD_BAD = [
     (dict(act=9), INVALID), (dict(da_dtype=T["i32"]), INVALID), (dict(dbias_dtype=T["e4m3"]), INVALID),
     (dict(da_dtype=0, db_dtype=0, dbias_dtype=0), INVALID), (dict(N=250), ALIGN), (dict(K=500, N=256), ALIGN),
     (dict(M=1 << 62), UNSUPPORTED), (dict(N=1 << 40, da_dtype=0, db_dtype=0), UNSUPPORTED),
-    (dict(tile=64), INVALID), (dict(splits=-2), INVALID), (dict(K=1 << 22), UNSUPPORTED),
+    (dict(tile=32), INVALID), (dict(splits=-2), INVALID), (dict(K=1 << 22), UNSUPPORTED),
     (dict(M=1 << 20, N=1 << 12), UNSUPPORTED),  # an operand of 2 GiB or more
 ]
 

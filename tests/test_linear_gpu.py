@@ -363,7 +363,7 @@ def test_grad_sizes(M, N, K):
 
 
 @pytest.mark.parametrize("splits", [0, 1, 2, 5])
-@pytest.mark.parametrize("tile", [128, 256])
+@pytest.mark.parametrize("tile", [64, 128, 256])
 @pytest.mark.parametrize("ab", ["bf16", "f16"])
 def test_grad_tiles(ab, tile, splits):
     """Each tile, whole and in K slices, more tiles than fit at once."""
