@@ -30,9 +30,10 @@ constexpr int kTiles = (int)(sizeof kLinear / sizeof kLinear[0]);
 constexpr int kRowsVariant = kTiles;  // the few-row kernels, one entry
 constexpr int kThreads = 256;
 
-// The plan's cost model (us), fitted per type to 663 forced plans (11 shapes, M
-// 90 to 4096, N 1024 to 6528, K 512 to 8192; every tile, 1 to 6 slices): 6 to 9 %
-// rms from the measured times, and the plans that it chooses take 0 to 2 % longer
+// The plan's cost model (us), fitted per type to 1054 forced plans (24 shapes, M
+// 90 to 8192, N 704 to 8192, K 512 to 8192; every tile, 1 to 6 slices), weighted
+// towards each shape's best ones: 3 to 6 % rms from the measured times there, and
+// the plans that it chooses of them take under 1 % longer on the mean, 17 % at worst,
 // than the best measured ones.  An item (a tile or a K slice of one) takes its
 // K tiles times tk plus an epilogue of e0 + e1 * area (in 256x256 tiles); rounds
 // of items fill the compute units.  Smaller tiles of which two or three share a
@@ -42,10 +43,10 @@ struct LinearCost {
   double start, join, bw, e0, e1;
   double tk256, tk192, tk128x256, tk128, tk64, pair128, pair64, three64;
 };
-constexpr LinearCost kCost16 = {3.465, 2.297, 10.97, 2.054, 6.275, 1.029, 0.828, 0.743, 0.517, 0.182, 0.78, 0.31, 0.0};
-constexpr LinearCost kCostE4m3 = {4.475, 2.042, 9.057, 1.92, 5.632, 1.138, 0.774, 0.586, 0.386, 0.146, 0.0, 0.277, 0.0};
-constexpr LinearCost kCostI8 = {4.458, 2.078, 9.178, 1.796, 5.074, 1.11, 0.866, 0.781, 0.556, 0.195, 0.858, 0.323, 0.454};
-constexpr LinearCost kCostWide = {4.276, 2.849, 8.637, 1.004, 7.77, 0.0, 0.0, 0.0, 0.812, 0.334, 1.401, 0.526, 0.0};
+constexpr LinearCost kCost16 = {0.98, 3.65, 21.9, 3.11, 10.4, 1.296, 1.032, 0.844, 0.592, 0.231, 0.821, 0.344, 0.0};
+constexpr LinearCost kCostE4m3 = {1.89, 4.93, 32.2, 2.6, 11.4, 1.373, 1.007, 0.685, 0.407, 0.218, 0.0, 0.329, 0.0};
+constexpr LinearCost kCostI8 = {1.1, 4.2, 21.8, 3.36, 10.8, 1.287, 1.027, 0.841, 0.61, 0.259, 0.856, 0.361, 0.509};
+constexpr LinearCost kCostWide = {2.41, 3.49, 14.5, 2.14, 14.3, 0.0, 0.0, 0.0, 0.796, 0.349, 1.43, 0.53, 0.0};
 
 // Tiles of variant v: the first whole, the last `tail` in K slices of `kslice`.
 struct LinearCut {
@@ -91,7 +92,11 @@ double linear_time(const LinearVariant& v, const LinearCut& c, const gemm_epi_li
     if (v.occ >= 3 && items > 2 * cus) tk = w.three64, slots = 3 * cus;
     return (double)((items + slots - 1) / slots) * (tk * (double)((k + v.bk - 1) / v.bk) + epi);
   };
-  double t = w.start + rounds(c.tiles - c.tail, d.K) + rounds(c.tail * c.splits, std::min(c.kslice, d.K));
+  const double products = rounds(c.tiles - c.tail, d.K) + rounds(c.tail * c.splits, std::min(c.kslice, d.K));
+  // A and B once from memory, at the 4.5 TB/s that tiles of few rows reach (24
+  // bf16 rows, N = K = 8192: 39 us, 20 by the items alone)
+  const double stream = (double)(d.M + d.N) * (double)(d.K * elem_bytes(d.ab_dtype)) / 4.5e6 + epi;
+  double t = w.start + std::max(products, stream);
   if (c.tail) t += w.join + (double)c.tail * v.bm * v.bn * 4.0 * (2 * c.splits + 1) / (w.bw * 1e6);
   return t;
 }
