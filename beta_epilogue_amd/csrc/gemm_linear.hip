@@ -29,6 +29,10 @@ const LinearVariant kLinear[] = {
 constexpr int kTiles = (int)(sizeof kLinear / sizeof kLinear[0]);
 constexpr int kRowsVariant = kTiles;  // the few-row kernels, one entry
 constexpr int kThreads = 256;
+// A launch has less than 2^32 threads: 16 columns for a workgroup of up to 512 ...
+constexpr int64_t kRowsMaxN = int64_t(1) << 26;
+// ... and 32 for one of 1024 in the column sums; 256 threads for an item.
+constexpr int64_t kGradMaxN = int64_t(1) << 26, kGradMaxBlocks = int64_t(1) << 24;
 
 // The plan's cost model (us), fitted per type to 1054 forced plans (24 shapes, M
 // 90 to 8192, N 704 to 8192, K 512 to 8192; every tile, 1 to 6 slices), weighted
@@ -166,6 +170,9 @@ static int validate_linear(gemm_epi_linear_desc* d) {
   // partial sums are fp32 rows of a tile; row and column numbers are 32-bit
   if (d->M >= (int64_t(1) << 31) - 512 || d->N >= (int64_t(1) << 31) - 512)
     return fail(GEMM_EPI_ERR_UNSUPPORTED, "M and N must be below 2^31 - 512");
+  // 2^17 products of -128 by -128 reach 2^31
+  if (d->ab_dtype == GEMM_EPI_I8 && d->K >= int64_t(1) << 17)
+    return fail(GEMM_EPI_ERR_UNSUPPORTED, "int8 with K of 2^17 or more: the int32 sums could overflow");
   return GEMM_EPI_OK;
 }
 
@@ -183,7 +190,8 @@ extern "C" int gemm_epi_linear_create_variant(const gemm_epi_linear_desc* desc, 
   // (the fp8 MFMA sums a group of products with fewer bits than fp32 keeps)
   const bool widened = d.ab_dtype == GEMM_EPI_E4M3 && d.d_dtype == GEMM_EPI_F32;
   const int kernel_ab = widened ? (int)T_E4M3_WIDE : d.ab_dtype;
-  if (variant == kRowsVariant ? d.M > kRowsMax : variant >= 0 && kLinear[variant].ab != kernel_ab)
+  const bool rows_fit = d.M <= kRowsMax && d.N <= kRowsMaxN;
+  if (variant == kRowsVariant ? !rows_fit : variant >= 0 && kLinear[variant].ab != kernel_ab)
     return fail(GEMM_EPI_ERR_UNSUPPORTED, "variant %s cannot run this problem", gemm_epi_linear_variant_name(variant));
   int device = 0, cus = 0;
   rc = device_query(&device, &cus);
@@ -203,9 +211,9 @@ extern "C" int gemm_epi_linear_create_variant(const gemm_epi_linear_desc* desc, 
       }
     }
     // few rows: up to 16 always (the tiles would be mostly empty), up to 64
-    // where the model says so (32 bf16 rows: N = K = 4096 11 us against 17 as
-    // tiles, 8192 38 against 29)
-    if (forced == -1 && d.splits == 0 && (d.M <= 16 || (d.M <= kRowsMax && rows_time(d, cus) < best_us)))
+    // where the model says so (32 bf16 rows: N = K = 4096 10.8 us against
+    // 12.7 as tiles, N = 512 and K = 8192 14.2 against 11.6)
+    if (forced == -1 && d.splits == 0 && rows_fit && (d.M <= 16 || rows_time(d, cus) < best_us))
       variant = kRowsVariant;
   }
 
@@ -446,6 +454,7 @@ extern "C" int gemm_epi_linear_grad_create(const gemm_epi_linear_grad_desc* desc
   const int64_t most = (int64_t(1) << 31) - 512;
   if (d.M >= most || d.N >= most || d.K >= most)
     return fail(GEMM_EPI_ERR_UNSUPPORTED, "M, N and K must be below 2^31 - 512");
+  if (d.N > kGradMaxN) return fail(GEMM_EPI_ERR_UNSUPPORTED, "more than 2^26 columns");
   if (d.N % 8 || ((da || db) && d.K % 8))
     return fail(GEMM_EPI_ERR_ALIGNMENT, "rows of dD (%lld elements) and of A and B (%lld) must be multiples of 16 bytes",
                 (long long)d.N, (long long)d.K);
@@ -489,9 +498,9 @@ extern "C" int gemm_epi_linear_grad_create(const gemm_epi_linear_grad_desc* desc
         if (h->tile == 0 || t < best) best = t, h->tile = tile, h->a = a, h->b = b;
       }
   }
-  if (h->a.items() + h->b.items() + d.N / 32 >= most) {
+  if (h->a.items() + h->b.items() + (d.N + 31) / 32 >= kGradMaxBlocks) {
     delete h;
-    return fail(GEMM_EPI_ERR_UNSUPPORTED, "2^31 or more work items (tiles and K slices)");
+    return fail(GEMM_EPI_ERR_UNSUPPORTED, "2^24 or more work items (tiles and K slices)");
   }
   const int64_t chunks = (d.M + h->chunk - 1) / h->chunk;
   const bool sum_rows = d.act == GEMM_EPI_ACT_NONE && (da || db);

@@ -178,7 +178,7 @@ __global__ __launch_bounds__(block_threads<TPR>()) void rmsnorm_kernel(NormParam
   __shared__ float red[TPR / 64];
   __shared__ uint32_t redm[TPR / 64];
   const int t = threadIdx.x % TPR;
-  const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+  const int64_t row = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * RPB + threadIdx.x / TPR;
   if (row >= p.rows) return;  // whole waves, and whole workgroups where rows share barriers
   constexpr int XS = sizeof(typename Elem<TX>::type);
   const char* x = (const char*)p.x + row * p.ldx * XS;
@@ -365,7 +365,9 @@ __global__ __launch_bounds__(block_threads<TPR>()) void rmsnorm_grad_kernel(Norm
 template <int TX, int TY, int TPR, int NV>
 void norm(const NormParams& p, hipStream_t s) {
   constexpr int RPB = block_threads<TPR>() / TPR;
-  hipLaunchKernelGGL((rmsnorm_kernel<TX, TY, TPR, NV>), dim3((unsigned)((p.rows + RPB - 1) / RPB)),
+  // (a launch has less than 2^32 threads in each direction)
+  const int64_t blocks = (p.rows + RPB - 1) / RPB, x = blocks < 1 << 20 ? blocks : 1 << 20;
+  hipLaunchKernelGGL((rmsnorm_kernel<TX, TY, TPR, NV>), dim3((unsigned)x, (unsigned)((blocks + x - 1) / x)),
                      dim3(block_threads<TPR>()), 0, s, p);
 }
 

@@ -12,8 +12,9 @@
 // to Q / (E t) on [0, 14] by iteratively reweighted least squares of the
 // relative error (largest 8.8e-7; fp32 evaluation adds 3e-7), so the
 // far negative side keeps its relative precision.  The slopes clamp their
-// argument to |z| <= 20, where E is 0 in fp32, so an infinity times 0 does not
-// arise; a NaN passes the clamps (they compare).  z = -infinity gives NaN, as
+// argument to |z| <= 20, where E is 0 in fp32 (silu: 200, where the sigmoid is 0
+// or 1), so an infinity times 0 does not arise; a NaN passes the clamps (they
+// compare).  z = -infinity gives NaN, as
 // -infinity * 0 in the formula, with gelu, gelu_tanh and silu.
 #pragma once
 
@@ -88,8 +89,9 @@ __device__ __forceinline__ float act_slope(float z) {
     // p + z p (1 - p) u2'
     return __builtin_fmaf(zc * p * (1.0f - p), 2.0f * kTanhC * __builtin_fmaf(3.0f * kTanhK, z2, 1.0f), p);
   } else if constexpr (ACT == ACT_SILU) {
-    const float p = sigmoid(z);
-    return p * __builtin_fmaf(z, 1.0f - p, 1.0f);
+    const float zc = z > 200.0f ? 200.0f : (z < -200.0f ? -200.0f : z);
+    const float p = sigmoid(zc);
+    return p * __builtin_fmaf(zc, 1.0f - p, 1.0f);
   } else {
     return 1.0f;
   }

@@ -152,7 +152,7 @@ class _Plan:
             if stream.device.index != self.device:
                 raise ValueError("the stream is on %s, the plan on cuda:%d" % (stream.device, self.device))
             return stream.cuda_stream, stream
-        return stream, torch.cuda.ExternalStream(stream or 0)
+        return stream, torch.cuda.ExternalStream(stream or 0, device=self._device)
 
     def _workspace(self, nbytes, workspace, stream):
         """Pointer, size and owner of a call's workspace."""

@@ -14,7 +14,9 @@
  *
  * Activations (fp32): none; relu max(z, 0); gelu z Phi(z); gelu_tanh
  * z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2; silu z / (1 + exp(-z)).  A
- * NaN z gives a NaN D.  relu's slope is 1 for z > 0, else 0.
+ * NaN z gives a NaN D, and so does z = -infinity with gelu, gelu_tanh and silu
+ * (-infinity times 0, as in the formulas).  The slopes of infinite z are their
+ * limits; relu's is 1 for z > 0, else 0.
  *
  * Types: A and B fp16, bf16, e4m3 or int8 (one type); D, R and Z one type of
  * fp16, bf16, fp32.  Products are summed in fp32 (int8: int32), the epilogue
@@ -74,13 +76,14 @@ typedef struct gemm_epi_linear_handle gemm_epi_linear_handle;
  * flags other than 0 and 1, strides below the extent, a stride of a tensor
  * that is not used.  ALIGNMENT: the 16-byte rule.  UNSUPPORTED: e5m2 and uint8;
  * rows or row strides too long for the kernels' 31-bit tile offsets; 2^31 or
- * more rows, columns or work items.  DEVICE: no gfx950.
+ * more rows, columns or work items; int8 with K of 2^17 or more, whose int32
+ * sums could overflow.  DEVICE: no gfx950.
  */
 int gemm_epi_linear_create(const gemm_epi_linear_desc* desc, gemm_epi_linear_handle** out);
 
 /* As gemm_epi_linear_create with kernel `variant` (-1: its choice); one that
  * cannot run the problem is UNSUPPORTED (the last variant, "linear_rows",
- * takes M of at most 64). */
+ * takes M of at most 64 and N of at most 2^26). */
 int gemm_epi_linear_create_variant(const gemm_epi_linear_desc* desc, int variant, gemm_epi_linear_handle** out);
 
 /*
@@ -127,7 +130,7 @@ typedef struct gemm_epi_linear_grad_handle gemm_epi_linear_grad_handle;
  * dbias is summed in fp32 before that rounding, in a fixed order.  Errors as
  * above; at least one gradient must be wanted.  UNSUPPORTED as well: an
  * operand that a product reads across its rows (dA: B; dB: A and dZ) of 2 GiB
- * or more.
+ * or more; N above 2^26; 2^24 or more work items.
  */
 int gemm_epi_linear_grad_create(const gemm_epi_linear_grad_desc* desc, gemm_epi_linear_grad_handle** out);
 

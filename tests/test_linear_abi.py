@@ -62,6 +62,7 @@ LINEAR_BAD = [
     (dict(ldr=256), INVALID), (dict(ldz=256), INVALID), (dict(residual=1, ldr=255), INVALID),
     (dict(lda=1 << 40), UNSUPPORTED), (dict(K=1 << 40), UNSUPPORTED), (dict(N=1 << 40), UNSUPPORTED),
     (dict(M=1 << 40), UNSUPPORTED), (dict(ldd=1 << 62), UNSUPPORTED), (dict(M=(1 << 63) - 1), UNSUPPORTED),
+    (dict(ab_dtype=T["i8"], K=1 << 17), UNSUPPORTED),  # 2^17 products of up to 2^14 in an int32
 ]
 
 
@@ -78,6 +79,7 @@ GRAD_BAD = [
     (dict(M=1 << 62), UNSUPPORTED), (dict(N=1 << 40, da_dtype=0, db_dtype=0), UNSUPPORTED),
     (dict(tile=32), INVALID), (dict(splits=-2), INVALID), (dict(K=1 << 22), UNSUPPORTED),
     (dict(M=1 << 20, N=1 << 12), UNSUPPORTED),  # an operand of 2 GiB or more
+    (dict(N=(1 << 26) + 8, da_dtype=0, db_dtype=0), UNSUPPORTED),  # more threads than a launch has
 ]
 
 

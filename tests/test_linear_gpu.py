@@ -440,6 +440,24 @@ def test_grad_refusals():
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("ab", ["f16", "bf16"])
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+def test_grad_infinite_z(act, ab):
+    """The slope of an infinite pre-activation (an fp16 overflow) is its limit,
+    1 or 0, and a NaN stays in its place."""
+    T = ref.TORCH[ab]
+    Z = torch.zeros(4, 64, dtype=T)
+    Z[0], Z[1], Z[2, 3] = float("inf"), float("-inf"), float("nan")
+    dD = torch.full((4, 64), 2.0, dtype=T, device="cuda")
+    dZ, db = torch.empty_like(dD), torch.empty(64, device="cuda")
+    _say("case", act, ab)
+    ge.FusedLinearGrad(4, 64, 64, ab=ab, act=act, dbias="f32")(dD, Z=Z.cuda(), dZ=dZ, dbias=db)
+    torch.cuda.synchronize()
+    assert (dZ[0] == 2).all() and (dZ[1] == 0).all()
+    nan = torch.isnan(dZ[2]).cpu()
+    assert nan.sum() <= 1 and bool(nan[3]) == (act != "relu") and torch.isfinite(dZ[3]).all()
+
+
 def test_grad_graph():
     M, N, K = 260, 264, 520
     g = torch.Generator().manual_seed(4)

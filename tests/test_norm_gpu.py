@@ -302,3 +302,18 @@ def test_training_step_together():
     for name, got, want in (("D", D, out.detach()), ("dH", dH, x.grad), ("dweight", dw, w6.grad), ("dW", dW, W6.grad),
                             ("dbias", db, b6.grad)):
         assert float((ref.f64(got) - want).abs().max()) <= 0.03 * float(want.abs().max()), name
+
+
+def test_norm_more_rows_than_one_grid_direction():
+    """2^26 rows and a few: four to a workgroup of 256 threads, which would be
+    2^32 threads in one direction of the grid."""
+    rows, n = (1 << 26) + 64, 64
+    g = torch.Generator().manual_seed(5)
+    X, w = torch.randn(n, 8, generator=g).to(torch.bfloat16).cuda(), torch.ones(8, dtype=torch.bfloat16, device="cuda")
+    want = torch.empty_like(X)
+    _say("case", rows, 8)
+    ge.RmsNorm(n, 8)(X, w, Y=want)
+    many = X.repeat(rows // n, 1)
+    Y = torch.zeros_like(many)
+    ge.RmsNorm(rows, 8)(many, w, Y=Y)
+    assert (Y.view(-1, n, 8) == want).all()
