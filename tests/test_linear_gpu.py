@@ -485,3 +485,63 @@ def test_grad_graph():
         again = new()
         op(dD, A, B, Z=Z, **again)
         assert all(torch.equal(again[k], want[k]) for k in want)
+
+
+# --- tensors of more than 4 GiB --------------------------------------------
+REP = 2100  # of 256 rows; 537600 rows of 8 KiB are 4.4 GB
+
+
+def _repeats(big, base):
+    """Whether `big` is `base` REP times over."""
+    n = base.shape[0]
+    return all((big[i * n:(i + 1) * n] == base).all() for i in (0, 1, REP // 2 - 1, REP // 2, REP - 2, REP - 1)) and \
+        bool((big.view(REP, n, -1) == base).all())
+
+
+@pytest.mark.parametrize("N,K", [(64, 4096), (4096, 64)])
+def test_offsets_beyond_32_bits(N, K):
+    """A of 4.4 GB, or D, Z and the residual of 4.4 GB each: every 256 rows
+    give what they give alone, bit for bit."""
+    variant = ge.linear_variant_names().index("linear_bf16_256x256")
+    g = torch.Generator().manual_seed(N)
+    A, B, R = (_draw(g, r, c, torch.bfloat16).cuda() for r, c in ((256, K), (N, K), (256, N)))
+    out = []
+    for rep in (1, REP):
+        a, r = A.repeat(rep, 1), R.repeat(rep, 1)
+        D, Z = torch.zeros_like(r), torch.zeros_like(r)
+        _say("case", rep, N, K)
+        ge.FusedLinear(256 * rep, N, K, act="silu", residual=True, z=True, splits=1, variant=variant)(
+            a, B, D=D, Z=Z, residual=r)
+        out.append((D, Z))
+    assert _repeats(out[1][0], out[0][0]) and _repeats(out[1][1], out[0][1])
+
+
+def test_rows_offsets_beyond_32_bits():
+    """One token and a weight of 4.4 GB."""
+    g = torch.Generator().manual_seed(8)
+    A, B = (_draw(g, r, 4096, torch.bfloat16).cuda() for r in (1, 256))
+    want, D = (torch.zeros(1, n, dtype=torch.bfloat16, device="cuda") for n in (256, 256 * REP))
+    names = ge.linear_variant_names()
+    ge.FusedLinear(1, 256, 4096, variant=names.index("linear_rows"))(A, B, D=want)
+    _say("case", 1, 256 * REP, 4096)
+    ge.FusedLinear(1, 256 * REP, 4096)(A, B.repeat(REP, 1), D=D)
+    assert (D.view(REP, 256) == want).all()
+
+
+def test_grad_offsets_beyond_32_bits():
+    """dD, Z and dZ of 4.4 GB each."""
+    g = torch.Generator().manual_seed(9)
+    N, K = 4096, 64
+    dD, Z, B = torch.ones(256, N, dtype=torch.bfloat16).cuda(), _draw(g, 256, N, torch.bfloat16).cuda(), \
+        _draw(g, N, K, torch.bfloat16).cuda()
+    out = []
+    for rep in (1, REP):
+        d, z = dD.repeat(rep, 1), Z.repeat(rep, 1)
+        dZ, dA, db = torch.zeros_like(d), torch.zeros(256 * rep, K, dtype=torch.bfloat16, device="cuda"), \
+            torch.zeros(N, device="cuda")
+        _say("case", rep, N, K)
+        ge.FusedLinearGrad(256 * rep, N, K, act="relu", da="bf16", dbias="f32", tile=256, splits=1)(
+            d, B=B, Z=z, dZ=dZ, dA=dA, dbias=db)
+        out.append((dZ, dA, db))
+    assert _repeats(out[1][0], out[0][0]) and _repeats(out[1][1], out[0][1])
+    assert (out[1][2] == out[0][2] * REP).all()  # counts below 2^24

@@ -317,3 +317,28 @@ def test_norm_more_rows_than_one_grid_direction():
     Y = torch.zeros_like(many)
     ge.RmsNorm(rows, 8)(many, w, Y=Y)
     assert (Y.view(-1, n, 8) == want).all()
+
+
+def test_offsets_beyond_32_bits():
+    """Tensors of 4.4 GB: every 256 rows give what they give alone, bit for
+    bit; dweight sums 2 x 10^3 terms in a workgroup and 10^3 workgroups."""
+    rep, cols = 2100, 4096
+    g = torch.Generator().manual_seed(6)
+    x, r, dy, i = (torch.randn(256, cols, generator=g).to(torch.bfloat16).cuda() for _ in range(4))
+    w = torch.ones(cols, dtype=torch.bfloat16, device="cuda")
+    out = []
+    for n in (1, rep):
+        X, R = x.repeat(n, 1), r.repeat(n, 1)
+        Y = torch.zeros(256 * n, cols, dtype=torch.int8, device="cuda")
+        scale = torch.zeros(256 * n, device="cuda")
+        _say("case", 256 * n, cols)
+        ge.RmsNorm(256 * n, cols, y="i8", residual=True)(X, w, Y=Y, residual=R, H=X, scale=scale)
+        dW = torch.zeros(cols, device="cuda")
+        ge.RmsNormGrad(256 * n, cols)(dy.repeat(n, 1), X, w, dH=R, dH_in=i.repeat(n, 1), dweight=dW)
+        out.append((Y, scale, X, R, dW))
+    for big, base in zip(out[1][:4], out[0][:4]):
+        assert (big.view((rep,) + base.shape) == base).all()
+    h = out[0][2].double()
+    terms = dy.double() * h / torch.sqrt((h * h).mean(1, keepdim=True) + 1e-6)
+    bound = rep * terms.abs().sum(0) * 3100 * 2.0 ** -24
+    assert ((out[1][4].double() - rep * terms.sum(0)).abs() <= bound).all()
