@@ -998,7 +998,10 @@ __device__ __forceinline__ void gemm_epi_body(const typename CF::params_t& p, ch
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave % CF::WAVES_M, wn = wave / CF::WAVES_M;
 
-  const int g = p.xcd_remap ? (bid & 7) * (G >> 3) + (bid >> 3) : bid;
+  // (the linear kernels' grids need not be multiples of 8: the first G % 8
+  // XCDs take one more)
+  const int over = CF::LIN ? min(bid & 7, G & 7) : 0;
+  const int g = p.xcd_remap ? (bid & 7) * (G >> 3) + over + (bid >> 3) : bid;
 
   using OpA = Operand<CF, BM, CF::WM, CF::A_KMAJOR>;
   using OpB = Operand<CF, BN, CF::WN, CF::B_KMAJOR>;

@@ -312,7 +312,7 @@ extern "C" int gemm_epi_linear_run(const gemm_epi_linear_handle* h, const void* 
   p.tiles_m = (int32_t)h->tiles_m;
   p.tiles_n = (int32_t)h->tiles_n;
   p.group_m = h->group_m;
-  p.xcd_remap = h->grid % 8 == 0 ? 1 : 0;
+  p.xcd_remap = 1;
   p.dp_tiles = (int32_t)(h->tiles - h->tail);
   p.tail_tiles = (int32_t)h->tail;
   p.splits = h->splits;
@@ -396,14 +396,14 @@ void cut(GradProduct* p, int tile, int64_t splits) {
 
 // Modelled time (us) of the launch and the join, from forced runs of 40 shapes
 // (M 1 to 6385, N and K 256 to 4096): an item takes 1.1 us per K tile with 256x256
-// tiles, 0.45 with 128x128 and 0.16 with 64x64 ones, or 0.85 and 0.36 for two
+// tiles, 0.45 with 128x128 and 0.16 with 64x64 ones, or 0.85 and 0.38 for two
 // that share a compute unit, and 8, 4 or 2 us besides.  The plans that it
 // chooses take up to 7 % longer than the best forced ones, 12 % at worst.
 double grad_time(const GradProduct& a, const GradProduct& b, int tile, int cus) {
   const double items = (double)(a.items() + b.items());
   const bool pairs = tile != 256 && items > cus;
   const double slots = pairs ? 2.0 * cus : cus;
-  const double tk = tile == 256 ? 1.1 : tile == 128 ? (pairs ? 0.85 : 0.45) : (pairs ? 0.36 : 0.16);
+  const double tk = tile == 256 ? 1.1 : tile == 128 ? (pairs ? 0.85 : 0.45) : (pairs ? 0.38 : 0.16);
   const double fixed = tile == 256 ? 8.0 : tile == 128 ? 4.0 : 2.0;
   double longest = 0.0, total = 0.0, join = 0.0;
   for (const GradProduct* p : {&a, &b}) {
@@ -580,7 +580,7 @@ extern "C" int gemm_epi_linear_grad_run(const gemm_epi_linear_grad_handle* h, co
     q->tiles_m = (int32_t)w.tiles_m;
     q->tiles_n = (int32_t)w.tiles_n;
     q->group_m = w.tiles_n > 32 ? 8 : 4;
-    q->xcd_remap = w.items() % 8 == 0 ? 1 : 0;
+    q->xcd_remap = 1;
     q->splits = w.splits;
     q->kslice = w.kslice;
     q->tail_tiles = w.splits > 1 ? (int32_t)w.tiles : 0;
