@@ -591,6 +591,7 @@ extern "C" int gemm_epi_linear_grad_run(const gemm_epi_linear_grad_handle* h, co
   if (dB) product(&p.b, h->b, g, A, dB_in, dB, d.db_dtype, h->ws_b);
   p.ga = p.a.tiles_total;
   p.gb = p.b.tiles_total;
+  p.b_first = dB && (!dA || std::min(h->b.kslice, h->b.K) > std::min(h->a.kslice, h->a.K)) ? 1 : 0;
   p.partial = partial;
   p.rows = sum_rows ? dD : nullptr;
   p.P = sum_rows ? d.M : chunks;

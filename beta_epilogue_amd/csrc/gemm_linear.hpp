@@ -64,9 +64,9 @@ void launch_linear_part(int variant, const LinParams& p, int grid, hipStream_t s
 // The backward's products, one launch for both:
 //   a: dA = dZ . B  (M x K over N: A = dZ K-major, B = B N-major)
 //   b: dB = dB_in + dZ^T . A  (N x K over M: A = dZ M-major, B = A N-major)
-// Workgroups 0 .. ga-1 run a, the next gb run b, the rest make dbias: of the
-// chunks' column sums in partial, or without an activation of dZ = dD itself.
-// A problem that is not wanted has 0.
+// ga workgroups run a and gb run b (b's come first with b_first), the rest make
+// dbias: of the chunks' column sums in partial, or without an activation of
+// dZ = dD itself.  A problem that is not wanted has 0.
 // Four kernels per type: 256x256 tiles; 128x128 tiles with two workgroups per
 // compute unit; 128x128 tiles with a ring of three stages, for grids of at most
 // one workgroup per compute unit, whose transposing reads have nobody else's
@@ -86,7 +86,7 @@ using GradCfg = Cfg<AB, A_KMAJOR, false, true, grad_tile(KIND), grad_tile(KIND),
                     KIND == GRAD_256 ? 2 : 0, 32, 2, grad_occ(KIND)>;
 struct GradParams {
   LinParams a, b;
-  int32_t ga, gb;
+  int32_t ga, gb, b_first;
   const float* partial;  // [P][C], or NULL
   const void* rows;      // [P][C] of type AB to be summed (NULL: none)
   int64_t P, C;

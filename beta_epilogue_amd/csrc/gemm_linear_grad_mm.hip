@@ -6,7 +6,9 @@
 // and do not depend on one another, so their tiles (and K slices) share a
 // grid: the second product's workgroups start as soon as compute units are
 // free instead of behind the first one's last round, and small problems fill
-// the chip together.  The column sums of dZ (of the elementwise pass's chunks,
+// the chip together; the one with the longer items goes first (1812 x 560 x
+// 3824 bf16: 34.7 us with dA's 450 tiles of 9 K tiles first, 27.2 with dB's 150
+// of 29).  The column sums of dZ (of the elementwise pass's chunks,
 // or without an activation of dD's rows) are made by further workgroups of
 // the same launch.  Both products read the weights and
 // activations as they lie: dA has B's columns contiguous (N-major), dB both
@@ -54,9 +56,9 @@ __global__ __launch_bounds__(256, grad_occ(KIND)) void linear_grad_mm_kernel(Gra
   using CA = GradCfg<AB, true, KIND>;
   using CB = GradCfg<AB, false, KIND>;
   __shared__ __attribute__((aligned(1024))) char lds[CA::LDS_BYTES > CB::LDS_BYTES ? CA::LDS_BYTES : CB::LDS_BYTES];
-  const int bid = blockIdx.x;
-  if (bid < p.ga) gemm_epi_body<CA>(p.a, lds, bid, p.ga);
-  else if (bid < p.ga + p.gb) gemm_epi_body<CB>(p.b, lds, bid - p.ga, p.gb);
+  const int bid = blockIdx.x, a0 = p.b_first ? p.gb : 0, b0 = p.b_first ? 0 : p.ga;
+  if (bid >= a0 && bid < a0 + p.ga) gemm_epi_body<CA>(p.a, lds, bid - a0, p.ga);
+  else if (bid < p.ga + p.gb) gemm_epi_body<CB>(p.b, lds, bid - b0, p.gb);
   else if (p.partial) colsum_block<8>(p.partial, p.P, p.C, p.dbias, p.dbias_dtype, bid - p.ga - p.gb, (float*)lds);
   else colsum_rows_block<AB>((const uint16_t*)p.rows, p.P, p.C, p.dbias, p.dbias_dtype, bid - p.ga - p.gb, (float*)lds);
 }
