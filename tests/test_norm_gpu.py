@@ -166,7 +166,8 @@ def run_grad(rows, cols, x="bf16", weight=None, dweight="f32", dh_in=False, pad=
     op.close()
 
 
-@pytest.mark.parametrize("rows,cols", SHAPES + [(1300, 520), (600, 3000), (300, 9001)])
+@pytest.mark.parametrize("rows,cols", SHAPES + [(1300, 520), (600, 3000), (300, 9001), (700, 6143), (3, 6145),
+                                            (300, 12288), (2, 12289)])
 @pytest.mark.parametrize("x", ["bf16", "f16", "f32"])
 def test_grad(rows, cols, x):
     run_grad(rows, cols, x, dh_in=cols % 2 == 0, seed=cols)
