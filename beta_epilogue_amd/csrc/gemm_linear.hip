@@ -47,9 +47,9 @@ struct LinearCost {
   double start, join, bw, e0, e1;
   double tk256, tk192, tk128x256, tk128, tk64, pair128, pair64, three64;
 };
-constexpr LinearCost kCost16 = {0.98, 3.65, 21.9, 3.11, 10.4, 1.296, 1.032, 0.844, 0.592, 0.231, 0.821, 0.344, 0.0};
+constexpr LinearCost kCost16 = {0.98, 3.65, 21.9, 3.11, 10.4, 1.296, 1.032, 0.0, 0.592, 0.231, 0.821, 0.344, 0.0};
 constexpr LinearCost kCostE4m3 = {1.89, 4.93, 32.2, 2.6, 11.4, 1.373, 1.007, 0.685, 0.407, 0.218, 0.0, 0.329, 0.0};
-constexpr LinearCost kCostI8 = {1.1, 4.2, 21.8, 3.36, 10.8, 1.287, 1.027, 0.841, 0.61, 0.259, 0.856, 0.361, 0.509};
+constexpr LinearCost kCostI8 = {1.1, 4.2, 21.8, 3.36, 10.8, 1.287, 1.027, 0.0, 0.61, 0.259, 0.856, 0.361, 0.509};
 constexpr LinearCost kCostWide = {2.41, 3.49, 14.5, 2.14, 14.3, 0.0, 0.0, 0.0, 0.796, 0.349, 1.43, 0.53, 0.0};
 
 // Tiles of variant v: the first whole, the last `tail` in K slices of `kslice`.

@@ -141,7 +141,7 @@ def test_null_arguments():
     assert L.gemm_epi_linear_grad_workspace(None) == -1 and L.gemm_epi_rmsnorm_grad_workspace(None) == -1
 
 
-NAMES = 23
+NAMES = 20
 
 
 def test_variant_table():
