@@ -25,6 +25,11 @@ int check_sizes(int64_t rows, int64_t cols, float eps) {
   return GEMM_EPI_OK;
 }
 
+// What a run adds to a row's mean square: without an eps 2^-149, which changes no
+// normal number and keeps 1 / sqrt finite, so that a row of zeros is 0 times a
+// number rather than 0 times infinity.
+float run_eps(float eps) { return eps > 0x1p-149f ? eps : 0x1p-149f; }
+
 int check_stride(const char* name, int64_t* ld, int64_t rows, int64_t cols, bool used) {
   if (!used) {
     if (*ld != 0) return fail(GEMM_EPI_ERR_INVALID_ARG, "ld%s is given but the tensor is not used", name);
@@ -124,7 +129,7 @@ extern "C" int gemm_epi_rmsnorm_run(const gemm_epi_rmsnorm_handle* h, const void
   p.ldh = d.ldh;
   p.ldy = d.ldy;
   p.w_f32 = d.weight_dtype == GEMM_EPI_F32 ? 1 : 0;
-  p.eps = d.eps;
+  p.eps = run_eps(d.eps);
   (void)hipGetLastError();  // clear a stale error so the check below is ours
   launch_rmsnorm(d.x_dtype, d.y_dtype, p, (hipStream_t)stream);
   return launched();
@@ -208,7 +213,7 @@ extern "C" int gemm_epi_rmsnorm_grad_run(const gemm_epi_rmsnorm_grad_handle* h, 
   p.ldi = d.ldi;
   p.ldo = d.ldo;
   p.w_f32 = d.weight_dtype == GEMM_EPI_F32 ? 1 : 0;
-  p.eps = d.eps;
+  p.eps = run_eps(d.eps);
   (void)hipGetLastError();  // clear a stale error so the checks below are ours
   launch_rmsnorm_grad(d.x_dtype, p, h->grid, (hipStream_t)stream);
   rc = launched();

@@ -12,10 +12,12 @@
  *
  * dh is the gradient of x and of r alike.  Everything is computed in fp32 and
  * rounded once; h is also rounded into x's type as an output, while y comes
- * from the unrounded h.  (Squares that overflow fp32 make s 0.)  A row that
- * holds a NaN or an infinity gets a NaN or infinite scale in 8 bits; its
- * values are NaN or 0 (e4m3), or 0 where they would be NaN (int8).  An
- * all-zero row gives zeros.
+ * from the unrounded h.  The squares are fp32 numbers too: where their sum
+ * overflows (a root mean square of 1.8e19 / sqrt(columns)) s is 0.  eps 0 stands
+ * for 2^-149, the least positive fp32 number, so an all-zero row gives zeros
+ * with any eps.  A row that holds a NaN or an infinity gets a NaN or infinite
+ * scale in 8 bits; its values are NaN or 0 (e4m3), or 0 where they would be NaN
+ * (int8).
  *
  * Tensors are row-major with a stride between rows; any number of columns up
  * to 16384, any stride, element alignment (16 bytes are faster).  Status
@@ -37,7 +39,7 @@ typedef struct gemm_epi_rmsnorm_desc {
   int32_t y_dtype;             /* x_dtype, E4M3 or I8 */
   int32_t weight_dtype;        /* x_dtype or F32 */
   int32_t residual;            /* 1: r is added (and h may be written) */
-  float eps;                   /* finite, >= 0 */
+  float eps;                   /* finite, >= 0 (0: 2^-149) */
 } gemm_epi_rmsnorm_desc;
 
 typedef struct gemm_epi_rmsnorm_handle gemm_epi_rmsnorm_handle;

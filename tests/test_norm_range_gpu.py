@@ -70,3 +70,47 @@ def test_grad_zero_rows(cols, eps):
 def test_norm_magnitudes(cols, x, y, rms, eps):
     X = _draw(torch.Generator().manual_seed(cols), 5, cols, ref.TORCH[x], rms)
     run_norm(5, cols, x, y, X=X, eps=eps)
+
+
+@pytest.mark.parametrize("cols", COLS)
+@pytest.mark.parametrize("y", ["bf16", "e4m3", "i8"])
+def test_zero_rows_without_eps(cols, y):
+    """eps 0: a row of zeros gives zeros (with the least scale), and its
+    neighbours what they give alone."""
+    g = torch.Generator().manual_seed(cols)
+    X = _draw(g, 4, cols, torch.bfloat16)
+    X[1], X[3] = 0, 0
+    w = torch.ones(cols, dtype=torch.bfloat16, device="cuda")
+
+    def run(x):
+        n = x.shape[0]
+        Y = torch.full((n, cols), 5.0).to(ref.TORCH[y]).cuda()
+        scale = torch.full((n,), 5.0, device="cuda") if y != "bf16" else None
+        ge.RmsNorm(n, cols, y=y, eps=0.0)(x.cuda(), w, Y=Y, scale=scale)
+        torch.cuda.synchronize()
+        return Y.float(), scale
+
+    _say("case", cols, y)
+    Y, scale = run(X)
+    alone, s = run(X[[0, 2]])
+    assert (Y[[1, 3]] == 0).all() and torch.equal(Y[[0, 2]], alone)
+    if scale is not None:
+        assert (scale[[1, 3]] == 2.0 ** -126).all() and torch.equal(scale[[0, 2]], s)
+
+
+@pytest.mark.parametrize("cols", COLS)
+def test_grad_zero_rows_without_eps(cols):
+    """eps 0 stands for 2^-149: a row of zeros whose dY is 0 (padding) has dH =
+    dH_in, and another g 2^74.5, the formula's value; neither adds to dweight."""
+    g = torch.Generator().manual_seed(cols)
+    H, dY, I = (_draw(g, 5, cols, torch.float32) for _ in range(3))
+    H[1], H[3] = 0, 0
+    dY[1] = 0
+    w = 1 + 0.3 * torch.randn(cols, generator=g)
+    _say("case", cols)
+    dH, dw = _grad(H, dY, w, 0.0, I, "f32")
+    dh, dwr, bound, sw = ref.rmsnorm_grad(dY, H, w, 2.0 ** -149, I)
+    assert torch.equal(dH[1].cpu(), I[1])
+    ref.check("dH", dH, dh, bound + ref.half_step(dh.abs() + bound, torch.float32))
+    e = (ref.norm_rel(cols) + 13 * ref.U) * sw
+    ref.check("dweight", dw, dwr, e + ref.half_step(dwr.abs() + e, torch.float32))
