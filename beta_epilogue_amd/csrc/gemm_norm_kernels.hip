@@ -102,11 +102,9 @@ __device__ __forceinline__ v8f load_weight8(const void* w, bool f32, const Span&
 }
 
 // Rounds to nearest-even into 8 bits and stores: values of at most QMAX (1 + 2^-21),
-// which round to QMAX, or NaN, which stays NaN in e4m3 and becomes 0 in int8
-// (the row's scale is NaN then).  int8: adding 1.5 * 2^23 leaves the rounded
-// integer in the low byte of the sum.  TX is the inputs' type: a NaN that comes
-// from 16-bit values has zeros there already.
-template <int T, int TX>
+// which round to QMAX, or in e4m3 NaN, which stays.  int8: adding 1.5 * 2^23 leaves
+// the rounded integer in the low byte of the sum.
+template <int T>
 __device__ __forceinline__ void store8_q(void* row, const Span& g, v8f v) {
   uint32_t w[2];
 #pragma unroll
@@ -117,10 +115,7 @@ __device__ __forceinline__ void store8_q(void* row, const Span& g, v8f v) {
     } else {
       uint32_t b[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float x = v[4 * j + k];
-        b[k] = __float_as_uint((TX == T_F32 && x != x ? 0.0f : x) + 12582912.0f);
-      }
+      for (int k = 0; k < 4; ++k) b[k] = __float_as_uint(v[4 * j + k] + 12582912.0f);
       // byte 0 of each sum
       const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u), hi = __builtin_amdgcn_perm(b[3], b[2], 0x0c0c0400u);
       w[j] = __builtin_amdgcn_perm(hi, lo, 0x05040100u);
@@ -236,8 +231,15 @@ __global__ __launch_bounds__(block_threads<TPR>()) void rmsnorm_kernel(NormParam
       f = inv;
     }
     uint8_t* y = (uint8_t*)p.y + row * p.ldy;
+    if (TY == T_I8 && !(scale <= 0x1.fffffep127f)) {
+      // finite values over an infinite scale are 0, and what is NaN becomes 0 (the
+      // low byte of a NaN may be anything)
 #pragma unroll
-    for (int i = 0; i < NV; ++i) store8_q<TY, TX>(y, at[i], h[i] * f);
+      for (int i = 0; i < NV; ++i) store8_q<TY>(y, at[i], v8f{});
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) store8_q<TY>(y, at[i], h[i] * f);
+    }
     if (t == 0) p.scale[row] = scale;
   } else {
     char* y = (char*)p.y + row * p.ldy * XS;

@@ -1,5 +1,6 @@
 """The root-mean-square norm and its backward far from 1: rows whose statistics
-lie near the ends of fp32's range, rows of zeros, a small or no eps.  The forms and bounds are those of tests/linear_ref.py: no
+lie near the ends of fp32's range, rows of zeros, a small or no eps, NaN with a
+payload.  The forms and bounds are those of tests/linear_ref.py: no
 intermediate of either kernel leaves fp32's normal range at these magnitudes,
 so the relative bounds hold as they stand."""
 import pytest
@@ -114,3 +115,26 @@ def test_grad_zero_rows_without_eps(cols):
     ref.check("dH", dH, dh, bound + ref.half_step(dh.abs() + bound, torch.float32))
     e = (ref.norm_rel(cols) + 13 * ref.U) * sw
     ref.check("dweight", dw, dwr, e + ref.half_step(dwr.abs() + e, torch.float32))
+
+
+@pytest.mark.parametrize("x", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("cols", COLS)
+def test_int8_of_nan_with_payload(cols, x):
+    """int8 values that would be NaN are 0, whatever bits the NaN has: in an
+    fp32 weight, and in an fp32 x."""
+    nan = torch.tensor([0x7fc01234, 0x7f800055], dtype=torch.int32).view(torch.float32)  # quiet, signalling
+    w = torch.ones(cols)
+    X = torch.ones(3, cols, dtype=ref.TORCH[x])
+    Y, scale = torch.full((3, cols), 9, dtype=torch.int8, device="cuda"), torch.zeros(3, device="cuda")
+    op = ge.RmsNorm(3, cols, x=x, y="i8", weight="f32")
+    _say("case", cols, x)
+    for v in nan:
+        bad = w.clone()
+        bad[cols // 2] = v
+        op(X.cuda(), bad.cuda(), Y=Y.fill_(9), scale=scale)
+        assert (Y == 0).all() and torch.isnan(scale).all()
+        if x == "f32":
+            Z = X.clone()
+            Z[1, cols // 2] = v
+            op(Z.cuda(), w.cuda(), Y=Y.fill_(9), scale=scale)
+            assert (Y[1] == 0).all() and torch.isnan(scale[1]) and (Y[[0, 2]] == 127).all()
