@@ -14,7 +14,7 @@ from __future__ import annotations
 import ctypes
 import torch
 
-from . import DTYPES, _check, gemm_epi_plan
+from . import DTYPES, GEMM_EPI_ERR_ALIGNMENT, GEMM_EPI_ERR_INVALID_ARG, GemmEpiError, _check, gemm_epi_plan
 from . import lib as _load
 
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
@@ -238,6 +238,29 @@ class FusedLinear(_Plan):
         return D
 
 
+    def _refuse_before(self, **tensors):
+        """Raises what a call with these tensors would raise."""
+        d, seen = self.desc, {}
+        wanted = {"B": True, "D": True, "bias": d.bias_dtype, "scale_b": d.scale_b, "residual": d.residual}
+
+        def refuse(code, text, *a):
+            raise GemmEpiError(code, "gemm_epi_linear_run", text % a)
+
+        for spec in self._specs:
+            name = spec[0]
+            if name not in tensors:
+                continue
+            seen[name] = self._ptr(tensors[name], spec)
+            if (seen[name] is not None) != bool(wanted[name]):
+                refuse(GEMM_EPI_ERR_INVALID_ARG, "%s must be given exactly as the plan says", name)
+            if (seen[name] or 0) % 16:
+                refuse(GEMM_EPI_ERR_ALIGNMENT, "%s is not 16-byte aligned", name)
+        if seen["D"] in (seen["B"], seen["bias"], seen["scale_b"]):
+            refuse(GEMM_EPI_ERR_INVALID_ARG, "D may not be an operand")
+        if seen["D"] == seen["residual"] and d.ldd != d.ldr:
+            refuse(GEMM_EPI_ERR_INVALID_ARG, "D may be the residual only with the same row stride")
+
+
 class FusedLinearGrad(_Plan):
     """The gradients of a linear layer.
 
@@ -364,6 +387,8 @@ class FusedNormLinear:
 
     def __call__(self, x, weight, B, scale_b, *, D, residual=None, H=None, bias=None, add=None, stream=None):
         M, K = self._mk
+        # what the second call would refuse, before the first one writes H
+        self.linear._refuse_before(B=B, bias=bias, scale_b=scale_b, residual=add, D=D)
         _, s = self.norm._stream(stream)
         _, _, q = self.norm._scratch(M * K, torch.uint8, s)
         _, _, scale = self.norm._scratch(M, torch.float32, s)
