@@ -519,6 +519,14 @@ extern "C" int gemm_epi_linear_grad_create(const gemm_epi_linear_grad_desc* desc
 extern "C" int gemm_epi_linear_grad_run(const gemm_epi_linear_grad_handle* h, const void* dD, const void* A,
                                         const void* B, const void* Z, const void* dB_in, void* dZ, void* dA, void* dB,
                                         void* dbias, void* workspace, int64_t workspace_bytes, void* stream) {
+  return gemm_epi_linear_grad_run_alpha(h, dD, A, B, Z, dB_in, dZ, dA, dB, dbias, 1.0f, workspace, workspace_bytes,
+                                        stream);
+}
+
+extern "C" int gemm_epi_linear_grad_run_alpha(const gemm_epi_linear_grad_handle* h, const void* dD, const void* A,
+                                              const void* B, const void* Z, const void* dB_in, void* dZ, void* dA,
+                                              void* dB, void* dbias, float alpha, void* workspace,
+                                              int64_t workspace_bytes, void* stream) {
   clear_error();
   if (!h) return fail(GEMM_EPI_ERR_INVALID_ARG, "handle is NULL");
   const gemm_epi_linear_grad_desc& d = h->d;
@@ -578,7 +586,7 @@ extern "C" int gemm_epi_linear_grad_run(const gemm_epi_linear_grad_handle* h, co
     q->K = w.K;
     q->lda = w.K;  // (of a K-major A; the other operands are packed)
     q->ldd = q->ldr = q->ldz = w.N;
-    q->alpha = 1.0f;
+    q->alpha = alpha;
     q->d_dtype = type;
     q->tiles_total = (int32_t)w.items();
     q->L = 1;

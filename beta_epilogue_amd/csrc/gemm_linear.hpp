@@ -62,8 +62,8 @@ template <int PART>
 void launch_linear_part(int variant, const LinParams& p, int grid, hipStream_t s);
 
 // The backward's products, one launch for both:
-//   a: dA = dZ . B  (M x K over N: A = dZ K-major, B = B N-major)
-//   b: dB = dB_in + dZ^T . A  (N x K over M: A = dZ M-major, B = A N-major)
+//   a: dA = alpha dZ . B  (M x K over N: A = dZ K-major, B = B N-major)
+//   b: dB = dB_in + alpha dZ^T . A  (N x K over M: A = dZ M-major, B = A N-major)
 // ga workgroups run a and gb run b (b's come first with b_first), the rest make
 // dbias: of the chunks' column sums in partial, or without an activation of
 // dZ = dD itself.  A problem that is not wanted has 0.

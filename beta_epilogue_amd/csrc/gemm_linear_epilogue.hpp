@@ -2,7 +2,7 @@
 // accumulator tile (included by gemm_linear.hpp):
 //   z = alpha * scale_a[m] * scale_b[n] * acc + bias[n]
 //   Z = z (if kept),  D = act(z) + R
-// (LIN 2: D = acc + R)
+// (LIN 2: D = alpha * acc + R)
 // in fp32 on the unrounded accumulator (int32 sums are converted first),
 // rounded to nearest-even into the type T that D, R and Z share.
 //
@@ -124,6 +124,11 @@ __device__ __forceinline__ void epilogue_linear(const LinParams& p, const ACC (&
 #pragma unroll
         for (int i = 0; i < VEC; ++i) v[i] = act_value<decltype(act_c)::value>(v[i]);
       });
+      // (a branch: multiplying by 1 adds 0.9 us to the backward of 4096^3, 235.5)
+      if (!CF::LIN_ACT && p.alpha != 1.0f) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] *= p.alpha;
+      }
       if (p.R) {
 #pragma unroll
         for (int i = 0; i < VEC; i += 4) {

@@ -71,6 +71,8 @@ def _bind(L):
     L.gemm_epi_linear_create_variant.restype = I
     L.gemm_epi_linear_run.argtypes = [P] * 9 + [_f32, P, N, P]
     L.gemm_epi_linear_grad_run.argtypes = [P] * 11 + [N, P]
+    L.gemm_epi_linear_grad_run_alpha.argtypes = [P] * 10 + [_f32, P, N, P]
+    L.gemm_epi_linear_grad_run_alpha.restype = I
     L.gemm_epi_rmsnorm_run.argtypes = [P] * 8
     L.gemm_epi_rmsnorm_grad_run.argtypes = [P] * 8 + [N, P]
     for op in ("linear", "linear_grad", "rmsnorm", "rmsnorm_grad"):
@@ -264,12 +266,12 @@ class FusedLinear(_Plan):
 class FusedLinearGrad(_Plan):
     """The gradients of a linear layer.
 
-    dZ = dD * act'(Z), dA = dZ . B, dB = dB_in + dZ^T . A, dbias = the column
-    sums of dZ.  All tensors are packed; dD, Z, dZ, A and B have type ab (f16
-    or bf16).  da, db, dbias: the gradients' types, None for one not wanted.
-    Without an activation dD takes dZ's place and Z and dZ are not given.  The
-    residual's gradient is dD.  tile (64, 128 or 256) and splits force the products'
-    tile and K split.
+    dZ = dD * act'(Z), dA = alpha dZ . B, dB = dB_in + alpha dZ^T . A, dbias =
+    the column sums of dZ, for a forward of this alpha without scales.  All
+    tensors are packed; dD, Z, dZ, A and B have type ab (f16 or bf16).  da, db,
+    dbias: the gradients' types, None for one not wanted.  Without an activation
+    dD takes dZ's place and Z and dZ are not given.  The residual's gradient is
+    dD.  tile (64, 128 or 256) and splits force the products' tile and K split.
     """
 
     _op = "linear_grad"
@@ -285,10 +287,11 @@ class FusedLinearGrad(_Plan):
                        m("dB_in", db, N, K, K), m("dZ", ab, M, N, N), m("dA", da, M, K, K), m("dB", db, N, K, K),
                        v("dbias", dbias, N))
         self._wants = (da is not None, db is not None)
+        self._run = lib().gemm_epi_linear_grad_run_alpha
         self.workspace_bytes = lib().gemm_epi_linear_grad_workspace(self.handle)
 
     def __call__(self, dD, A=None, B=None, *, Z=None, dB_in=None, dZ=None, dA=None, dB=None, dbias=None,
-                 stream=None, workspace=None):
+                 alpha=1.0, stream=None, workspace=None):
         ptr = self._ptr
         g, a, b, z, c, gz, ga, gb, gbias = self._specs
         wants_a, wants_b = self._wants
@@ -296,10 +299,10 @@ class FusedLinearGrad(_Plan):
         ws, nbytes, keep = self._workspace(self.workspace_bytes, workspace, s)
         # (an operand that the wanted gradients do not need is not passed on)
         code = self._run(self.handle, ptr(dD, g), ptr(A if wants_b else None, a), ptr(B if wants_a else None, b),
-                         ptr(Z, z), ptr(dB_in, c), ptr(dZ, gz), ptr(dA, ga), ptr(dB, gb), ptr(dbias, gbias), ws,
-                         nbytes, raw)
+                         ptr(Z, z), ptr(dB_in, c), ptr(dZ, gz), ptr(dA, ga), ptr(dB, gb), ptr(dbias, gbias), alpha,
+                         ws, nbytes, raw)
         if code:
-            _check(code, "gemm_epi_linear_grad_run")
+            _check(code, "gemm_epi_linear_grad_run_alpha")
 
 
 class RmsNorm(_Plan):

@@ -7,10 +7,11 @@
  *     D = act(z) + R            Z = z (kept for the backward, if asked for)
  *
  *     dZ = dD * act'(Z)         dbias[n] = sum_m dZ[m][n]
- *     dA = dZ . B               dB = dB_in + dZ^T . A
+ *     dA = alpha dZ . B         dB = dB_in + alpha dZ^T . A
  *
  * A is M x K (M tokens), B is N x K (the weight, one row per output), D, R, Z
- * and dD are M x N; all are row-major.  The gradient of R is dD itself.
+ * and dD are M x N; all are row-major.  The gradient of R is dD itself.  The
+ * backward is that of a forward without scale_a and scale_b.
  *
  * Activations (fp32): none; relu max(z, 0); gelu z Phi(z); gelu_tanh
  * z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2; silu z / (1 + exp(-z)).  A
@@ -145,6 +146,11 @@ int gemm_epi_linear_grad_create(const gemm_epi_linear_grad_desc* desc, gemm_epi_
 int gemm_epi_linear_grad_run(const gemm_epi_linear_grad_handle* h, const void* dD, const void* A, const void* B,
                              const void* Z, const void* dB_in, void* dZ, void* dA, void* dB, void* dbias,
                              void* workspace, int64_t workspace_bytes, void* stream);
+
+/* The same for a forward of this alpha (gemm_epi_linear_grad_run: 1). */
+int gemm_epi_linear_grad_run_alpha(const gemm_epi_linear_grad_handle* h, const void* dD, const void* A, const void* B,
+                                   const void* Z, const void* dB_in, void* dZ, void* dA, void* dB, void* dbias,
+                                   float alpha, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Free a handle (NULL is fine). */
 int gemm_epi_linear_grad_destroy(gemm_epi_linear_grad_handle* h);
