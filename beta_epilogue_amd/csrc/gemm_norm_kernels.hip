@@ -328,8 +328,8 @@ __global__ __launch_bounds__(block_threads<TPR>()) void rmsnorm_grad_kernel(Norm
     }
     row_join<Sum, TPR>(sums, red[flip]);
     flip ^= 1;  // the next row's words are others: one barrier separates reuse
-    // with xhat = h s: dh = dh_in + s g - xhat f, f = s mean(g xhat).  (s^3 itself
-    // leaves fp32's range for rows of 1e13 or 1e-13, whose dh is of ordinary size.)
+    // dh = dh_in + s (g w - h f), f = s^2 mean(g w h).  (s^3 itself leaves fp32's
+    // range for rows of 1e13 or 1e-13, whose dh is of ordinary size.)
     const float s = 1.0f / __builtin_sqrtf(sums[0] * inv_cols + p.eps);
     const float f = s * (s * (sums[1] * inv_cols));
     char* op = (char*)p.dh + row * p.ldo * XS;
@@ -339,9 +339,8 @@ __global__ __launch_bounds__(block_threads<TPR>()) void rmsnorm_grad_kernel(Norm
       v8f d = value8(dr[i]);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float xhat = h[k] * s;
-        dw[i][k] = __builtin_fmaf(g[k], xhat, dw[i][k]);
-        d[k] += __builtin_fmaf(g[k] * w[k], s, -(xhat * f));
+        dw[i][k] = __builtin_fmaf(g[k] * s, h[k], dw[i][k]);
+        d[k] = __builtin_fmaf(s, __builtin_fmaf(-h[k], f, g[k] * w[k]), d[k]);
       }
       store8<T>(op, at[i], d);
     }
