@@ -47,7 +47,7 @@ __device__ __forceinline__ v8f value8(G g) {
 // threads: they are loaded with the rest, count as 0 and are not stored.  So a
 // load is one access without a branch, and the loads of all tensors are in
 // flight together (backward of 14545 rows of 2461 fp16: 134 us with the cut groups
-// loaded element by element, 70 so).  Rows of less than 8 elements are one group
+// loaded element by element, 66 so).  Rows of less than 8 elements are one group
 // with `live` of them.
 struct Span {
   int64_t at;
@@ -251,9 +251,11 @@ __global__ __launch_bounds__(block_threads<TPR>()) void rmsnorm_kernel(NormParam
 // The backward: a workgroup walks rows blockIdx, blockIdx + grid, ... (RPB at
 // a time), keeps its weights and its part of dweight in registers, and leaves
 // one partial sum per column; colsum adds the workgroups in a fixed order.  The
-// next row is loaded before the sums of this one are joined (8192 x 4096 bf16:
-// 68 us without, 41.5 with).  1024 threads have 128 registers each: their
-// weights stay in LDS, and an fp32 dh_in is loaded with its own row.
+// next row is loaded before the sums of this one are joined (loaded at the row's
+// start, 8192 x 4096 bf16 takes 44.2 us instead of 42.5, with dh_in 56.9 instead of
+// 54.8, 4096 x 8448 54.1 instead of 48.6).  1024 threads have 128 registers each:
+// their weights stay in LDS, and an fp32 dh_in is loaded with its own row; fp32 still
+// spills 10 registers there (4096 x 9001 fp32: 109 us).
 template <int T, int TPR, int NV>
 __global__ __launch_bounds__(block_threads<TPR>()) void rmsnorm_grad_kernel(NormGradParams p) {
   constexpr int RPB = block_threads<TPR>() / TPR;

@@ -84,7 +84,8 @@ int gemm_epi_linear_create(const gemm_epi_linear_desc* desc, gemm_epi_linear_han
 
 /* As gemm_epi_linear_create with kernel `variant` (-1: its choice); one that
  * cannot run the problem is UNSUPPORTED (the last variant, "linear_rows",
- * takes M of at most 64 and N of at most 2^26). */
+ * takes M of at most 64 and N of at most 2^26, and has no K slices: splits is
+ * ignored). */
 int gemm_epi_linear_create_variant(const gemm_epi_linear_desc* desc, int variant, gemm_epi_linear_handle** out);
 
 /*
