@@ -240,29 +240,6 @@ class FusedLinear(_Plan):
         return D
 
 
-    def _refuse_before(self, **tensors):
-        """Raises what a call with these tensors would raise."""
-        d, seen = self.desc, {}
-        wanted = {"B": True, "D": True, "bias": d.bias_dtype, "scale_b": d.scale_b, "residual": d.residual}
-
-        def refuse(code, text, *a):
-            raise GemmEpiError(code, "gemm_epi_linear_run", text % a)
-
-        for spec in self._specs:
-            name = spec[0]
-            if name not in tensors:
-                continue
-            seen[name] = self._ptr(tensors[name], spec)
-            if (seen[name] is not None) != bool(wanted[name]):
-                refuse(GEMM_EPI_ERR_INVALID_ARG, "%s must be given exactly as the plan says", name)
-            if (seen[name] or 0) % 16:
-                refuse(GEMM_EPI_ERR_ALIGNMENT, "%s is not 16-byte aligned", name)
-        if seen["D"] in (seen["B"], seen["bias"], seen["scale_b"]):
-            refuse(GEMM_EPI_ERR_INVALID_ARG, "D may not be an operand")
-        if seen["D"] == seen["residual"] and d.ldd != d.ldr:
-            refuse(GEMM_EPI_ERR_INVALID_ARG, "D may be the residual only with the same row stride")
-
-
 class FusedLinearGrad(_Plan):
     """The gradients of a linear layer.
 
@@ -386,18 +363,38 @@ class FusedNormLinear:
             raise ValueError("q must be e4m3 or i8")
         self.norm = RmsNorm(M, K, x=x, y=q, weight=weight, residual=residual, eps=eps)
         self.linear = FusedLinear(M, N, K, ab=q, d=d, act=act, bias=bias, residual=add, scale_a=True, scale_b=True)
-        self._mk, self._q = (M, K), TORCH_DTYPES[q]
+        self._bias, self._add = bias is not None, bool(add)
+        self._scale_at = (M * K + 255) // 256 * 256
+        self._scratch_bytes = self._scale_at + 4 * M
 
     def __call__(self, x, weight, B, scale_b, *, D, residual=None, H=None, bias=None, add=None, stream=None):
-        M, K = self._mk
-        # what the second call would refuse, before the first one writes H
-        self.linear._refuse_before(B=B, bias=bias, scale_b=scale_b, residual=add, D=D)
-        _, s = self.norm._stream(stream)
-        _, _, q = self.norm._scratch(M * K, torch.uint8, s)
-        _, _, scale = self.norm._scratch(M, torch.float32, s)
-        q = q.view(self._q).view(M, K)
-        self.norm(x, weight, Y=q, residual=residual, H=H, scale=scale, stream=stream)
-        return self.linear(q, B, D=D, bias=bias, scale_a=scale, scale_b=scale_b, residual=add, stream=stream)
+        norm, linear = self.norm, self.linear
+        # what the projection would refuse, before the norm writes H
+        ptr = linear._ptr
+        _, sb, sbias, _, sscale, sadd, sd, _ = linear._specs
+        b, bs, sc, r, d = ptr(B, sb), ptr(bias, sbias), ptr(scale_b, sscale), ptr(add, sadd), ptr(D, sd)
+        if b is None or d is None or sc is None or (bs is None) == self._bias or (r is None) == self._add:
+            self._refuse(GEMM_EPI_ERR_INVALID_ARG, "B, D and scale_b are required; bias and add as the plan says")
+        if (b | d | sc | (bs or 0) | (r or 0)) & 15:
+            self._refuse(GEMM_EPI_ERR_ALIGNMENT, "a tensor is not 16-byte aligned")
+        if d in (b, bs, sc):
+            self._refuse(GEMM_EPI_ERR_INVALID_ARG, "D may not be an operand")
+        raw, s = norm._stream(stream)
+        q, _, keep = norm._scratch(self._scratch_bytes, torch.uint8, s)  # the operand, then its row scales
+        scale = q + self._scale_at
+        sx, sr, sw, _, sh, _ = norm._specs
+        code = norm._run(norm.handle, ptr(x, sx), ptr(residual, sr), ptr(weight, sw), q, ptr(H, sh), scale, raw)
+        if code:
+            _check(code, "gemm_epi_rmsnorm_run")
+        ws, nbytes, keep_ws = linear._workspace(linear._ws, None, s)
+        code = linear._run(linear.handle, q, b, bs, scale, sc, r, d, None, 1.0, ws, nbytes, raw)
+        if code:
+            _check(code, "gemm_epi_linear_run")
+        return D
+
+    @staticmethod
+    def _refuse(code, text):
+        raise GemmEpiError(code, "gemm_epi_linear_run", text)
 
     def close(self):
         self.norm.close()
