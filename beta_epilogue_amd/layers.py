@@ -202,7 +202,8 @@ class FusedLinear(_Plan):
     i8; d (of D, residual and Z): f16, bf16 or f32.  bias: its type, or None;
     residual, z, scale_a, scale_b: whether the call has them.  Z receives the
     pre-activation, which ``FusedLinearGrad`` takes (with the same alpha; it has
-    no scales).  Few rows (decoding) run a kernel of their own.  variant and splits force a kernel and a K split.
+    no scales).  Few rows (decoding) run a kernel of their own.  variant and
+    splits force a kernel and a K split.
     """
 
     _op = "linear"
