@@ -5,7 +5,8 @@ kernels of the shared library.  The C entry points keep their names
 (``gemm_epi_create``, ``gemm_epi_run``, ...); ``FusedGemm`` adds the
 torch-tensor convenience layer (pointers and the current HIP stream).  The
 linear layer and the norm (``FusedLinear``, ``FusedLinearGrad``, ``RmsNorm``,
-``RmsNormGrad``, ``FusedNormLinear``) are in ``layers``.
+``RmsNormGrad``, ``FusedNormLinear``) are in ``layers``, a mixture of experts'
+operators (``ExpertSort``, ``ExpertCombine``, ``ExpertCombineGrad``) in ``experts``.
 
 The library must have been built (``python -m beta_epilogue_amd.build`` or
 ``__graft_entry__.build()``); importing the binding without it raises.
@@ -236,14 +237,18 @@ class FusedGemm:
             pass
 
 
-# The linear layer and the norm (module layers, which imports torch) are
-# loaded when first asked for.
+# The linear layer and the norm (module layers, which imports torch) and what
+# stands on them are loaded when first asked for.
 _LAYERS = ("ACTIVATIONS", "FusedLinear", "FusedLinearGrad", "FusedNormLinear", "RmsNorm", "RmsNormGrad",
            "linear_variant_names")
+_EXPERTS = ("ExpertSort", "ExpertCombine", "ExpertCombineGrad")
 
 
 def __getattr__(name):
     if name in _LAYERS:
         from . import layers
         return getattr(layers, name)
+    if name in _EXPERTS:
+        from . import experts
+        return getattr(experts, name)
     raise AttributeError("module %r has no attribute %r" % (__name__, name))

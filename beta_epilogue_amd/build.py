@@ -4,7 +4,8 @@ libgemm_epi.so is linked from gemm_epi.hip (C ABI, variant table) and
 GEMM_EPI_PARTS objects of gemm_epi_part.hip, each compiling the kernel
 variants of gemm_epi_variants.inc assigned to it; the parts compile in
 parallel.  The linear layer (gemm_linear*.hip, its tile kernels in
-GEMM_LINEAR_PARTS parts) and the norm (gemm_norm*.hip) are linked in.
+GEMM_LINEAR_PARTS parts), the norm (gemm_norm*.hip) and the experts' operators
+(gemm_experts*.hip) are linked in.
 libmfma_ceiling.so is a measurement tool for bench.py.
 """
 from __future__ import annotations
@@ -29,7 +30,8 @@ GEMM_LINEAR_PARTS = 8
 LINEAR_GRAD_MM_SOURCE = os.path.join(CSRC, "gemm_linear_grad_mm.hip")
 GEMM_LINEAR_GRAD_PARTS = 8
 LINEAR_SOURCES = [os.path.join(CSRC, f) for f in ("gemm_linear.hip", "gemm_linear_rows.hip", "gemm_linear_grad.hip",
-                                                  "gemm_norm.hip", "gemm_norm_kernels.hip")]
+                                                  "gemm_norm.hip", "gemm_norm_kernels.hip", "gemm_experts.hip",
+                                                  "gemm_experts_kernels.hip")]
 SOURCES = [MAIN_SOURCE, PART_SOURCE, SPLITK_SOURCE, PREP_SOURCE, LINEAR_PART_SOURCE, LINEAR_GRAD_MM_SOURCE] + LINEAR_SOURCES
 HEADERS = [os.path.join(CSRC, "gemm_epi_kernel.hpp"), os.path.join(CSRC, "gemm_epi_launch.hpp"),
            os.path.join(CSRC, "gemm_epi_splitk.hpp"), os.path.join(CSRC, "gemm_epi_prep.hpp"),
@@ -37,9 +39,9 @@ HEADERS = [os.path.join(CSRC, "gemm_epi_kernel.hpp"), os.path.join(CSRC, "gemm_e
            os.path.join(CSRC, "gemm_epi_host.hpp"),
            os.path.join(CSRC, "linear_act.hpp"), os.path.join(CSRC, "gemm_linear_epilogue.hpp"),
            os.path.join(CSRC, "gemm_linear.hpp"), os.path.join(CSRC, "gemm_linear_variants.inc"),
-           os.path.join(CSRC, "gemm_norm.hpp"),
+           os.path.join(CSRC, "gemm_norm.hpp"), os.path.join(CSRC, "gemm_experts.hpp"),
            os.path.join(ROOT, "include", "gemm_epi.h"), os.path.join(ROOT, "include", "gemm_epi_linear.h"),
-           os.path.join(ROOT, "include", "gemm_epi_norm.h")]
+           os.path.join(ROOT, "include", "gemm_epi_norm.h"), os.path.join(ROOT, "include", "gemm_epi_experts.h")]
 # measurement tool used by bench.py --mfma-ceiling (not part of the GEMM path)
 CEILING_LIB = os.path.join(HERE, "libmfma_ceiling.so")
 CEILING_SOURCE = os.path.join(CSRC, "mfma_ceiling.hip")

@@ -1,0 +1,47 @@
+// gemm_experts.hpp -- the device code around the experts' products as its host
+// code (gemm_experts.hip) sees it: the sort of tokens by expert, the way back
+// and its gradient (gemm_experts_kernels.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace gemm_epi {
+
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxTopK = 64;
+// Choices (of a token and an expert) that one workgroup ranks.
+constexpr int kSortChunk = 4096;
+
+struct SortParams {
+  const void* ids;       // choices x int32 or int64
+  const void* X;         // rows to move, or NULL
+  const float* scale;    // of the rows of X, or NULL
+  int32_t* offsets;      // experts + 1
+  int32_t* rows;         // choices
+  void* Y;
+  float* scale_out;
+  int32_t* counts;       // workspace: chunks x experts (one chunk: NULL)
+  int64_t tokens;
+  int64_t row_bytes, ldx, ldy;  // bytes; a multiple of 16
+  int32_t top_k, experts, chunks, ids64;
+};
+void launch_expert_sort(const SortParams& p, hipStream_t s);
+
+struct CombineParams {
+  const void* Y;
+  const int32_t* rows;
+  const float* weights;  // NULL: 1
+  const void* R;         // NULL: 0
+  void* D;
+  const void* dD;        // backward
+  void* dY;
+  float* dweights;
+  int64_t tokens, cols, ldy, ldd, ldr, ldg;  // elements
+  int32_t top_k;
+};
+// t: T_F16, T_BF16 or T_F32.
+void launch_expert_combine(int t, const CombineParams& p, hipStream_t s);
+void launch_expert_combine_grad(int t, const CombineParams& p, int cus, hipStream_t s);
+
+}  // namespace gemm_epi

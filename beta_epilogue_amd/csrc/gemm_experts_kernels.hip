@@ -1,0 +1,319 @@
+// gemm_experts_kernels.hip -- tokens sorted by expert, their results brought
+// back with the router's weights, and the gradient of that.
+//
+// The sort is a stable counting sort of the T * top_k choices: row = offsets[e]
+// + the number of earlier choices of e.  Counts are integers, so LDS atomics on
+// them leave nothing to the order in which they run; ranks come from ballots,
+// never from atomics.  Moving the rows is bound by memory: a token's row is read
+// once and stored top_k times.
+#include "gemm_experts.hpp"
+#include "gemm_linear.hpp"
+
+namespace gemm_epi {
+
+namespace {
+
+constexpr int kSortThreads = 1024, kSortWaves = 16;
+constexpr int kPerWave = kSortChunk / kSortWaves;  // consecutive choices of a wave
+
+// Choice i's expert; -1: none.
+__device__ __forceinline__ int choice(const SortParams& p, int64_t i, int64_t n) {
+  if (i >= n) return -1;
+  const int64_t e = p.ids64 ? ((const int64_t*)p.ids)[i] : (int64_t)((const int32_t*)p.ids)[i];
+  return e >= 0 && e < p.experts ? (int)e : -1;
+}
+
+struct SortLds {
+  int cnt[kSortWaves][kMaxExperts];  // a wave's choices of an expert, then its next row
+  int base[kMaxExperts];             // rows before this chunk's: of earlier experts and chunks
+  int wave_sum[kSortWaves];
+};
+
+// Counts of the chunk's choices, per wave.
+__device__ __forceinline__ void count_chunk(const SortParams& p, int chunk, SortLds& s, int (&e)[kPerWave / 64]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t n = p.tokens * p.top_k, i0 = (int64_t)chunk * kSortChunk + wave * kPerWave;
+#pragma unroll
+  for (int k = 0; k < kPerWave / 64; ++k) e[k] = choice(p, i0 + k * 64 + lane, n);
+  for (int i = threadIdx.x; i < kSortWaves * p.experts; i += kSortThreads) s.cnt[i / p.experts][i % p.experts] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kPerWave / 64; ++k)
+    if (e[k] >= 0) atomicAdd(&s.cnt[wave][e[k]], 1);
+  __syncthreads();
+}
+
+__global__ __launch_bounds__(kSortThreads) void expert_count_kernel(SortParams p) {
+  __shared__ SortLds s;
+  int e[kPerWave / 64];
+  count_chunk(p, blockIdx.x, s, e);
+  for (int x = threadIdx.x; x < p.experts; x += kSortThreads) {
+    int n = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) n += s.cnt[w][x];
+    p.counts[(int64_t)blockIdx.x * p.experts + x] = n;
+  }
+}
+
+// Ranks the choices of one chunk: their rows into row[] (-1: none); offsets by
+// the workgroup that has `write`.
+__device__ __forceinline__ void rank_chunk(const SortParams& p, int chunk, bool write, SortLds& s,
+                                           int (&row)[kPerWave / 64]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, t = threadIdx.x;
+  int e[kPerWave / 64];
+  count_chunk(p, chunk, s, e);
+  // expert t's choices in all, and in the chunks before this one
+  int all = 0, before = 0;
+  if (t < p.experts) {
+    if (p.chunks == 1) {
+#pragma unroll
+      for (int w = 0; w < kSortWaves; ++w) all += s.cnt[w][t];
+    } else {
+#pragma unroll 8
+      for (int c = 0; c < p.chunks; ++c) {
+        const int n = p.counts[(int64_t)c * p.experts + t];
+        all += n;
+        before += c < chunk ? n : 0;
+      }
+    }
+  }
+  // an exclusive sum over the experts
+  int sum = all;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(sum, d);
+    sum += lane >= d ? o : 0;
+  }
+  if (lane == 63) s.wave_sum[wave] = sum;
+  __syncthreads();
+  int first = sum - all;
+  for (int w = 0; w < wave; ++w) first += s.wave_sum[w];
+  if (t < p.experts) {
+    if (write) {
+      p.offsets[t] = first;
+      if (t == p.experts - 1) p.offsets[t + 1] = first + all;
+    }
+    int at = first + before;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
+      const int n = s.cnt[w][t];
+      s.cnt[w][t] = at;
+      at += n;
+    }
+  }
+  __syncthreads();
+  // a wave's choices in order, 64 at a time: those of the same expert among
+  // them by one ballot per bit of the expert's number
+  const int bits = 32 - __clz(p.experts);
+#pragma unroll
+  for (int k = 0; k < kPerWave / 64; ++k) {
+    uint64_t same = __ballot(e[k] >= 0);
+    for (int b = 0; b < bits; ++b) {
+      const uint64_t one = __ballot((e[k] >> b) & 1);
+      same &= (e[k] >> b) & 1 ? one : ~one;
+    }
+    const int earlier = __popcll(same & ((uint64_t(1) << lane) - 1));
+    row[k] = -1;
+    if (e[k] >= 0) row[k] = s.cnt[wave][e[k]] + earlier;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (e[k] >= 0 && earlier == 0) s.cnt[wave][e[k]] += __popcll(same);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+}
+
+__global__ __launch_bounds__(kSortThreads) void expert_rank_kernel(SortParams p) {
+  __shared__ SortLds s;
+  int row[kPerWave / 64];
+  rank_chunk(p, blockIdx.x, blockIdx.x == 0, s, row);
+  const int64_t n = p.tokens * p.top_k;
+  const int64_t i0 = (int64_t)blockIdx.x * kSortChunk + (threadIdx.x >> 6) * kPerWave + (threadIdx.x & 63);
+#pragma unroll
+  for (int k = 0; k < kPerWave / 64; ++k)
+    if (i0 + k * 64 < n) p.rows[i0 + k * 64] = row[k];
+}
+
+// A thread moves 16 bytes of a token's row; `chunks` of them per row.
+__global__ __launch_bounds__(256) void expert_gather_kernel(SortParams p) {
+  const uint32_t per = (uint32_t)(p.row_bytes / 16);
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t t = i / per;
+  if (t >= p.tokens) return;
+  const uint32_t c = (uint32_t)(i - t * per);
+  const v4u v = __builtin_nontemporal_load((const v4u*)((const char*)p.X + t * p.ldx + (int64_t)c * 16));
+  const float sc = p.scale && c == 0 ? p.scale[t] : 0.0f;
+  const int32_t* rows = p.rows + t * p.top_k;
+#pragma unroll 4
+  for (int j = 0; j < p.top_k; ++j) {
+    const int r = rows[j];
+    if (r < 0) continue;
+    __builtin_nontemporal_store(v, (v4u*)((char*)p.Y + r * p.ldy + (int64_t)c * 16));
+    if (p.scale && c == 0) p.scale_out[r] = sc;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The way back
+// ---------------------------------------------------------------------------
+template <int T> struct Vec {
+  static constexpr int N = T == T_F32 ? 4 : 8;  // elements of a 16-byte access
+  float v[N];
+  __device__ __forceinline__ void decode(v4u r) {
+    const v4f lo = epi_dec<T>(r, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = lo[i];
+    if constexpr (N == 8) {
+      const v4f hi = epi_dec<T>(r, 1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[4 + i] = hi[i];
+    }
+  }
+  __device__ __forceinline__ v4u pack() const {
+    return epi_pack<T>(v4f{v[0], v[1], v[2], v[3]}, N == 8 ? v4f{v[N - 4], v[N - 3], v[N - 2], v[N - 1]} : v4f{});
+  }
+};
+
+// A thread makes 16 bytes of a token's row, summed in fp32 in the order of the
+// token's choices; G choices' rows are in flight at a time.
+template <int T>
+__global__ __launch_bounds__(256) void expert_combine_kernel(CombineParams p) {
+  using V = Vec<T>;
+  constexpr int ES = EpiElem<T>::SIZE, G = 4;
+  const uint32_t per = (uint32_t)(p.cols / V::N);
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t t = i / per;
+  if (t >= p.tokens) return;
+  const int64_t c = (i - t * per) * V::N;
+  const uint32_t total = (uint32_t)(p.tokens * p.top_k);
+  V sum;
+#pragma unroll
+  for (int k = 0; k < V::N; ++k) sum.v[k] = 0.0f;
+  if (p.R) sum.decode(*(const v4u*)((const char*)p.R + (t * p.ldr + c) * ES));
+  const int32_t* rows = p.rows + t * p.top_k;
+  const float* w = p.weights ? p.weights + t * p.top_k : nullptr;
+  for (int j0 = 0; j0 < p.top_k; j0 += G) {
+    v4u y[G];
+    float f[G];
+    bool live[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int j = j0 + g;
+      const uint32_t r = j < p.top_k ? (uint32_t)rows[j] : ~0u;
+      live[g] = r < total;
+      f[g] = w && j < p.top_k ? w[j] : 1.0f;
+      if (live[g]) y[g] = __builtin_nontemporal_load((const v4u*)((const char*)p.Y + ((int64_t)r * p.ldy + c) * ES));
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      if (!live[g]) continue;
+      V x;
+      x.decode(y[g]);
+#pragma unroll
+      for (int k = 0; k < V::N; ++k) sum.v[k] = __builtin_fmaf(f[g], x.v[k], sum.v[k]);
+    }
+  }
+  __builtin_nontemporal_store(sum.pack(), (v4u*)((char*)p.D + (t * p.ldd + c) * ES));
+}
+
+// The gradient: W waves take a token (W == 4: a workgroup, W == 1: four tokens
+// per workgroup) and G of its choices at a time, so that dD is read once for
+// them; the products with the rows are summed over lanes, then waves, in a
+// fixed order.
+template <int T, int W>
+__global__ __launch_bounds__(256) void expert_combine_grad_kernel(CombineParams p) {
+  using V = Vec<T>;
+  constexpr int ES = EpiElem<T>::SIZE, G = 4;
+  __shared__ float red[4][G];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t = W == 4 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + wave;
+  if (W == 1 && t >= p.tokens) return;
+  const uint32_t total = (uint32_t)(p.tokens * p.top_k);
+  const char* dd = (const char*)p.dD + t * p.ldd * ES;
+  for (int j0 = 0; j0 < p.top_k; j0 += G) {
+    uint32_t r[G];
+    float w[G], sum[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const bool there = j0 + g < p.top_k;
+      r[g] = there ? (uint32_t)p.rows[t * p.top_k + j0 + g] : ~0u;
+      w[g] = there ? p.weights[t * p.top_k + j0 + g] : 0.0f;
+      sum[g] = 0.0f;
+    }
+    for (int64_t c = (int64_t)((W == 4 ? wave * 64 : 0) + lane) * V::N; c < p.cols; c += W * 64 * V::N) {
+      V d;
+      d.decode(*(const v4u*)(dd + c * ES));
+      v4u y[G];
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        if (r[g] < total) y[g] = __builtin_nontemporal_load((const v4u*)((const char*)p.Y + ((int64_t)r[g] * p.ldy + c) * ES));
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        if (r[g] >= total) continue;
+        V x, o;
+        x.decode(y[g]);
+#pragma unroll
+        for (int k = 0; k < V::N; ++k) {
+          sum[g] = __builtin_fmaf(d.v[k], x.v[k], sum[g]);
+          o.v[k] = w[g] * d.v[k];
+        }
+        __builtin_nontemporal_store(o.pack(), (v4u*)((char*)p.dY + ((int64_t)r[g] * p.ldg + c) * ES));
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+      for (int d = 32; d >= 1; d >>= 1) sum[g] += __shfl_xor(sum[g], d);
+    if constexpr (W == 4) {
+      if (lane == 0) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) red[wave][g] = sum[g];
+      }
+      __syncthreads();
+      if (threadIdx.x < G && j0 + (int)threadIdx.x < p.top_k)
+        p.dweights[t * p.top_k + j0 + threadIdx.x] =
+            (red[0][threadIdx.x] + red[1][threadIdx.x]) + (red[2][threadIdx.x] + red[3][threadIdx.x]);
+      __syncthreads();
+    } else if (lane == 0) {
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        if (j0 + g < p.top_k) p.dweights[t * p.top_k + j0 + g] = sum[g];
+    }
+  }
+}
+
+template <int T>
+void combine(const CombineParams& p, hipStream_t s) {
+  const int64_t n = p.tokens * (p.cols / Vec<T>::N);
+  hipLaunchKernelGGL(expert_combine_kernel<T>, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, p);
+}
+
+template <int T>
+void combine_grad(const CombineParams& p, int cus, hipStream_t s) {
+  if (p.tokens < 8 * cus)
+    hipLaunchKernelGGL((expert_combine_grad_kernel<T, 4>), dim3((unsigned)p.tokens), dim3(256), 0, s, p);
+  else
+    hipLaunchKernelGGL((expert_combine_grad_kernel<T, 1>), dim3((unsigned)((p.tokens + 3) / 4)), dim3(256), 0, s, p);
+}
+
+}  // namespace
+
+void launch_expert_sort(const SortParams& p, hipStream_t s) {
+  if (p.chunks > 1) hipLaunchKernelGGL(expert_count_kernel, dim3(p.chunks), dim3(kSortThreads), 0, s, p);
+  hipLaunchKernelGGL(expert_rank_kernel, dim3(p.chunks), dim3(kSortThreads), 0, s, p);
+  if (!p.X) return;
+  const int64_t n = p.tokens * (p.row_bytes / 16);
+  hipLaunchKernelGGL(expert_gather_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, p);
+}
+
+void launch_expert_combine(int t, const CombineParams& p, hipStream_t s) {
+  if (t == T_F16) combine<T_F16>(p, s);
+  else if (t == T_BF16) combine<T_BF16>(p, s);
+  else combine<T_F32>(p, s);
+}
+
+void launch_expert_combine_grad(int t, const CombineParams& p, int cus, hipStream_t s) {
+  if (t == T_F16) combine_grad<T_F16>(p, cus, s);
+  else if (t == T_BF16) combine_grad<T_BF16>(p, cus, s);
+  else combine_grad<T_F32>(p, cus, s);
+}
+
+}  // namespace gemm_epi
