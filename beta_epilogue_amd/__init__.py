@@ -6,7 +6,8 @@ kernels of the shared library.  The C entry points keep their names
 torch-tensor convenience layer (pointers and the current HIP stream).  The
 linear layer and the norm (``FusedLinear``, ``FusedLinearGrad``, ``RmsNorm``,
 ``RmsNormGrad``, ``FusedNormLinear``) are in ``layers``, a mixture of experts'
-operators (``ExpertSort``, ``ExpertCombine``, ``ExpertCombineGrad``) in ``experts``.
+operators (``ExpertSort``, ``ExpertLinear``, ``ExpertCombine`` and their
+gradients) in ``experts``.
 
 The library must have been built (``python -m beta_epilogue_amd.build`` or
 ``__graft_entry__.build()``); importing the binding without it raises.
@@ -241,7 +242,8 @@ class FusedGemm:
 # stands on them are loaded when first asked for.
 _LAYERS = ("ACTIVATIONS", "FusedLinear", "FusedLinearGrad", "FusedNormLinear", "RmsNorm", "RmsNormGrad",
            "linear_variant_names")
-_EXPERTS = ("ExpertSort", "ExpertCombine", "ExpertCombineGrad")
+_EXPERTS = ("ExpertSort", "ExpertCombine", "ExpertCombineGrad", "ExpertLinear", "ExpertLinearGrad",
+            "expert_linear_variant_names")
 
 
 def __getattr__(name):

@@ -116,8 +116,14 @@ struct Params {
   int32_t int_unit;
 };
 
-// Arguments of the linear layer's kernels (gemm_linear.hpp).
+// Arguments of the linear layer's kernels (gemm_linear.hpp) and of the experts'
+// (gemm_grouped.hpp).
 struct LinParams;
+struct GroupParams;
+
+// Row groups with a B each (GroupParams): of the output's rows, or of the
+// contraction (a sum over each group's rows, one output per group).
+enum : int { GROUP_NONE = 0, GROUP_ROWS = 1, GROUP_K = 2 };
 
 // ---------------------------------------------------------------------------
 // MFMA traits per A/B element type and block size BLK (32: 32x32 output
@@ -248,7 +254,9 @@ template <> struct Mma<T_U8, 32> : Mma<T_I8, 32> {};
 //   BLK         MFMA output block: 32 (32x32) or 16 (16x16)
 //   LIN         1: the linear layer's arguments, row strides (of K-major
 //               operands) and epilogue (N-major D); 2: the same without bias,
-//               scales, activation and Z (its backward's products)
+//               scales, activation and Z (its backward's products); 3: 1 over
+//               groups of rows, with a factor in R's place; 4 and 5: 2 over
+//               groups of rows, and of the contraction
 //   OCC         workgroups meant to share a compute unit (bounds the registers)
 template <int AB_, bool A_KMAJOR_, bool B_KMAJOR_, bool CD_NMAJOR_, int BM_ = 256, int BN_ = 256,
           int ROWB_ = 128, int WAVES_M_ = 2, int WAVES_N_ = 2, int STAGES_ = 2, int DQ_ = 0,
@@ -256,9 +264,12 @@ template <int AB_, bool A_KMAJOR_, bool B_KMAJOR_, bool CD_NMAJOR_, int BM_ = 25
 struct Cfg {
   static constexpr int OCC = OCC_;
   static constexpr bool LIN = LIN_ != 0;
-  static constexpr bool LIN_ACT = LIN_ == 1;
+  static constexpr bool LIN_ACT = LIN_ == 1 || LIN_ == 3;
+  static constexpr bool LIN_MUL = LIN_ == 3;  // R multiplies
+  static constexpr int GROUP = LIN_ == 3 || LIN_ == 4 ? GROUP_ROWS : LIN_ == 5 ? GROUP_K : GROUP_NONE;
   static_assert(!LIN || (CD_NMAJOR_ && AB_ != T_U8), "what the linear kernels have");
-  using params_t = typename std::conditional<LIN_ != 0, LinParams, Params>::type;
+  using params_t = typename std::conditional<
+      GROUP != GROUP_NONE, GroupParams, typename std::conditional<LIN_ != 0, LinParams, Params>::type>::type;
   static constexpr int BLK = BLK_;
   using MM = Mma<AB_, BLK_>;
   static constexpr int DQ = DQ_;
@@ -979,11 +990,22 @@ template <class CF, int T, class ACC>
 __device__ void epilogue_linear(const LinParams& p, const ACC (&acc)[CF::FM][CF::FN], char* lds, int wave, int lane,
                                 int mw, int nw);
 
+// Row groups (gemm_grouped.hpp; GROUP kernels only).
+struct GroupTile {
+  int group, begin, end;  // the group and its rows
+  int first, tiles;       // its first row tile among all groups', and their number
+};
+template <class CF>
+__device__ int group_table(const GroupParams& p, int* first);
+__device__ GroupTile group_of_tile(const GroupParams& p, const int* first, int row_tile);
+__device__ GroupTile group_rows(const GroupParams& p, int group);
+
 // ---------------------------------------------------------------------------
 // The kernel
 // ---------------------------------------------------------------------------
 // The work of workgroup `bid` of `G` that share a problem, with the LDS array
-// `lds` of CF::LDS_BYTES (1 KiB aligned).
+// `lds` of CF::LDS_BYTES (1 KiB aligned; GROUP_ROWS: and the table of groups
+// behind them).
 template <class CF>
 __device__ __forceinline__ void gemm_epi_body(const typename CF::params_t& p, char* lds, int bid, int G) {
   using MM = typename CF::MM;
@@ -997,6 +1019,15 @@ __device__ __forceinline__ void gemm_epi_body(const typename CF::params_t& p, ch
   const int lane = __lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave % CF::WAVES_M, wn = wave / CF::WAVES_M;
+
+  int tiles_total = p.tiles_total;
+  [[maybe_unused]] const int* group_first = (const int*)(lds + CF::LDS_BYTES);
+  if constexpr (CF::GROUP == GROUP_ROWS) {
+    // row tiles of all groups; the workgroups that have one share the runs below
+    tiles_total = group_table<CF>(p, (int*)(lds + CF::LDS_BYTES)) * p.tiles_n;
+    G = min(G, tiles_total);
+    if (bid >= G) return;
+  }
 
   // (the linear kernels' grids need not be multiples of 8: the first G % 8
   // XCDs take one more)
@@ -1018,24 +1049,45 @@ __device__ __forceinline__ void gemm_epi_body(const typename CF::params_t& p, ch
   opb.setup_reader(wn * CF::WN, lane);
   using raw_t = typename CF::RAW;
 
-  for (int t = g; t < p.tiles_total; t += G) {
+  for (int t = g; t < tiles_total; t += G) {
     // ---- work item: a whole tile, or K slice `split` of tile ts ----------
     int split = -1;  // whole K range, epilogue here
     int ts = t;
-    if (t >= p.dp_tiles) {
+    [[maybe_unused]] GroupTile gt = {};
+    int tiles_m = p.tiles_m;
+    if constexpr (CF::GROUP == GROUP_ROWS) {
+      gt = group_of_tile(p, group_first, (int)((unsigned)t / (unsigned)p.tiles_n));
+      ts = t - gt.first * p.tiles_n;
+      tiles_m = gt.tiles;
+    }
+    if (CF::GROUP == GROUP_NONE && t >= p.dp_tiles) {
       const int u = t - p.dp_tiles;  // the item's workspace slot
       split = (int)((unsigned)u / (unsigned)p.tail_tiles);
       ts = p.dp_tiles + (u - split * p.tail_tiles);
     }
-    const TileRC tc = raster_tile(ts, p.tiles_m, p.tiles_n, p.group_m);
+    const TileRC tc = raster_tile(ts, tiles_m, p.tiles_n, p.group_m);
     const int l = tc.l;
+    if constexpr (CF::GROUP == GROUP_K) {
+      gt = group_rows(p, l);
+      gt.begin = __builtin_amdgcn_readfirstlane(gt.begin);
+      gt.end = __builtin_amdgcn_readfirstlane(gt.end);
+    }
     const int64_t kbeg = split > 0 ? (int64_t)split * p.kslice : 0;
-    const int64_t kbytes = (split < 0 ? p.K : min(p.K - kbeg, p.kslice)) * ES;  // this item's K, in bytes
-    const int KT = (int)((kbytes + CF::ROWB - 1) / CF::ROWB);
-    const int m0 = tc.tm * BM, n0 = tc.tn * BN;
+    const int64_t K = CF::GROUP == GROUP_K ? (int64_t)(gt.end - gt.begin) : p.K;
+    const int64_t kbytes = (split < 0 ? K : min(K - kbeg, p.kslice)) * ES;  // this item's K, in bytes
+    int KT = (int)((kbytes + CF::ROWB - 1) / CF::ROWB);
+    if constexpr (CF::GROUP == GROUP_K) KT = max(KT, 1);  // (a group without rows: one K tile of zeros)
+    const int m0 = (CF::GROUP == GROUP_ROWS ? gt.begin : 0) + tc.tm * BM, n0 = tc.tn * BN;
 
     // ---- staging set-up --------------------------------------------------
-    if constexpr (CF::LIN) {
+    if constexpr (CF::GROUP == GROUP_ROWS) {
+      opa.setup((const char*)p.A, gt.end, p.lda, 0, m0, wave, lane);
+      opb.setup((const char*)p.B + (int64_t)gt.group * p.N * p.K * ES, p.N, p.K, 0, n0, wave, lane);
+    } else if constexpr (CF::GROUP == GROUP_K) {
+      opa.setup((const char*)p.A + gt.begin * p.M * ES, p.M, K, 0, m0, wave, lane);
+      opb.setup((const char*)p.B + gt.begin * p.N * ES, p.N, K, 0, n0, wave, lane);
+      if (K == 0) opa.rsrc[2] = opb.rsrc[2] = 0;
+    } else if constexpr (CF::LIN) {
       // a K-major operand's row stride stands for its row length: chunks past
       // K are masked by the K tile's guard, not by the extent
       opa.setup((const char*)p.A, p.M, CF::A_KMAJOR ? p.lda : p.K, kbeg, m0, wave, lane);
@@ -1252,7 +1304,21 @@ __device__ __forceinline__ void gemm_epi_body(const typename CF::params_t& p, ch
     // otherwise (bf16 included) the mixed-type one (4 elements per lane).
     constexpr bool NM = CF::CD_NMAJOR;
     const int emw = m0 + wm * CF::WM, enw = n0 + wn * CF::WN;
-    if (t >= p.dp_tiles) {
+    if constexpr (CF::GROUP != GROUP_NONE) {
+      typename CF::params_t q = p;
+      if constexpr (CF::GROUP == GROUP_ROWS) {
+        q.M = gt.end;
+        if (q.bias) q.bias = (const char*)q.bias + ((int64_t)gt.group * p.N << epi_shift(p.bias_dtype));
+        if (q.scale_b) q.scale_b += (int64_t)gt.group * p.N;
+      } else {
+        const int64_t at = (int64_t)l * p.M * p.N << epi_shift(p.d_dtype);
+        q.D = (char*)q.D + at;
+        if (q.R) q.R = (const char*)q.R + at;
+      }
+      if (p.d_dtype == T_F16) epilogue_linear<CF, T_F16>(q, acc, lds, wave, lane, emw, enw);
+      else if (p.d_dtype == T_BF16) epilogue_linear<CF, T_BF16>(q, acc, lds, wave, lane, emw, enw);
+      else if constexpr (CF::AB != T_E4M3) epilogue_linear<CF, T_F32>(q, acc, lds, wave, lane, emw, enw);
+    } else if (t >= p.dp_tiles) {
       // a K slice: its partial sums, unscaled, into its workspace slot, as a
       // rows x cols matrix of its own (the tile's part inside the matrix)
       Params q = p;

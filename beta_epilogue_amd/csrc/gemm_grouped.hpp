@@ -1,0 +1,165 @@
+// gemm_grouped.hpp -- the experts' linear layers' device code as its host code
+// (gemm_experts_linear.hip) sees it: the tile kernels over groups of rows
+// (gemm_grouped_part.hip), the few-row kernels (gemm_grouped_rows.hip) and the
+// backward (gemm_grouped_grad.hip, gemm_grouped_act.hip).
+//
+// Rows offsets[e] .. offsets[e + 1] - 1 of A, D, ... are group e's, whose B, bias
+// and column scales are the e-th.  Only the device knows the offsets, so a
+// launch has as many workgroups as the worst distribution needs, or persistent
+// ones, and each finds its group from the offsets by itself: nothing is copied to
+// the host and no table is made by another launch.
+#pragma once
+
+#include "gemm_experts.hpp"
+#include "gemm_linear.hpp"
+
+namespace gemm_epi {
+
+// Arguments of the grouped kernels: the linear layer's, with M the batch's rows or
+// (LIN 5) a group's output's; R is the factor of the forward (LIN 3) or dB_in (LIN
+// 5).  B, bias, scale_b, and the backward's dB and dB_in hold one packed part
+// per group.
+struct GroupParams : LinParams {
+  const int32_t* offsets;  // groups + 1
+  int32_t groups;
+  int32_t rows;            // the batch's capacity
+};
+
+// Offsets that do not ascend within 0 .. rows are moved into that range, so no access
+// leaves the tensors whatever they hold.
+__device__ __forceinline__ GroupTile group_rows(const GroupParams& p, int group) {
+  GroupTile t = {};
+  t.group = group;
+  t.begin = min(max(p.offsets[group], 0), p.rows);
+  t.end = min(max(p.offsets[group + 1], t.begin), p.rows);
+  return t;
+}
+
+__device__ __forceinline__ int wave_scan(int v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(v, d);
+    v += lane >= d ? o : 0;
+  }
+  return v;
+}
+
+// The table of groups in LDS: first[g] = tiles of `rows` rows in the groups
+// before g (first[groups]: in all, returned).  All threads of the workgroup.
+constexpr int kGroupTableBytes = (kMaxExperts + 1) * 4 + 12;
+__device__ __forceinline__ int group_table_rows(const GroupParams& p, int* first, int rows) {
+  const int lane = __lane_id();
+  if (threadIdx.x < 64) {
+    int before = 0;
+    for (int base = 0; base < p.groups; base += 64) {
+      const int g = base + lane;
+      int n = 0;
+      if (g < p.groups) {
+        const GroupTile t = group_rows(p, g);
+        n = (t.end - t.begin + rows - 1) / rows;
+      }
+      const int sum = wave_scan(n, lane);
+      if (g < p.groups) first[g] = before + sum - n;
+      before += __shfl(sum, 63);
+    }
+    if (lane == 0) first[p.groups] = before;
+  }
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(first[p.groups]);
+}
+template <class CF>
+__device__ __forceinline__ int group_table(const GroupParams& p, int* first) {
+  return group_table_rows(p, first, CF::BM);
+}
+
+// The group of row tile number `row_tile` (below first[groups]).
+__device__ __forceinline__ GroupTile group_of_tile(const GroupParams& p, const int* first, int row_tile) {
+  const int lane = __lane_id();
+  int g = 0;
+  for (int base = 0; base < p.groups; base += 64) {
+    const int n = __popcll(__ballot(base + lane < p.groups && first[base + lane + 1] <= row_tile));
+    g += n;
+    if (n < 64) break;
+  }
+  g = __builtin_amdgcn_readfirstlane(g);
+  GroupTile t = group_rows(p, g);
+  t.begin = __builtin_amdgcn_readfirstlane(t.begin);
+  t.end = __builtin_amdgcn_readfirstlane(t.end);
+  t.first = __builtin_amdgcn_readfirstlane(first[g]);
+  t.tiles = __builtin_amdgcn_readfirstlane(first[g + 1]) - t.first;
+  return t;
+}
+
+// Chunk number `slot` of `rows` rows, without a table (one chunk per workgroup):
+// begin .. end - 1 are the chunk's rows; group -1: there is no such chunk.
+__device__ __forceinline__ GroupTile group_chunk(const GroupParams& p, int slot, int rows) {
+  const int lane = __lane_id();
+  int before = 0;
+  for (int base = 0; base < p.groups; base += 64) {
+    const int g = base + lane;
+    GroupTile t = {};
+    if (g < p.groups) t = group_rows(p, g);
+    const int n = (t.end - t.begin + rows - 1) / rows;
+    const int sum = before + wave_scan(n, lane);  // chunks of this group and those before
+    const uint64_t behind = __ballot(sum > slot);
+    if (behind) {
+      const int l = __ffsll((unsigned long long)behind) - 1;
+      GroupTile r = {};
+      r.group = base + l;
+      const int begin = __builtin_amdgcn_readfirstlane(__shfl(t.begin, l)), end = __builtin_amdgcn_readfirstlane(__shfl(t.end, l));
+      const int c = slot - __builtin_amdgcn_readfirstlane(__shfl(sum - n, l));
+      r.begin = begin + c * rows;
+      r.end = min(end, r.begin + rows);
+      return r;
+    }
+    before = __builtin_amdgcn_readfirstlane(__shfl(sum, 63));
+  }
+  GroupTile none = {};
+  none.group = -1;
+  return none;
+}
+
+// Tile kernels of the forward.
+template <int AB, int BM, int BN, int S, int OCC, int BLK>
+using GroupedCfg = Cfg<AB, true, true, true, BM, BN, 128, 2, 2, S, 0, BLK, 3, OCC>;
+
+constexpr int kGroupedParts = 7;
+template <int PART>
+void launch_grouped_part(int variant, const GroupParams& p, int grid, hipStream_t s);
+
+// Few rows per group: chunks of up to 4 * mb rows (mb 1, 2, 4 or 8), 16 weight
+// rows per workgroup; slots: chunks that the worst distribution has.
+void launch_grouped_rows(int ab, int mb, const GroupParams& p, int slots, hipStream_t s);
+
+// The backward's products, one launch for both (GRAD_* as for the linear layer):
+//   a: dA = dZ . B[e] over groups of rows; ga workgroups, a tile each at most
+//   b: dB[e] = dB_in[e] + dZ^T . A over each group's rows; gb workgroups
+// b's come first; the rest add up the chunks' column sums: dbias.
+template <int AB, bool ROWS, int KIND>
+using GroupedGradCfg = Cfg<AB, ROWS, false, true, grad_tile(KIND), grad_tile(KIND), 128, 2, 2, grad_stages(KIND),
+                           KIND == GRAD_256 ? 2 : 0, 32, ROWS ? 4 : 5, grad_occ(KIND)>;
+struct GroupGradParams {
+  GroupParams a, b;
+  int32_t ga, gb, sums;   // workgroups
+  const float* partial;   // [chunk][N]
+  int32_t chunk, slots;   // rows of a chunk, chunks that partial holds
+  void* dbias;            // groups x N
+  int32_t dbias_dtype;
+  int64_t N;
+};
+template <int AB, int KIND>
+void launch_grouped_grad(const GroupGradParams& p, hipStream_t s);
+
+// The elementwise pass over the rows of all groups, in chunks of `chunk` rows:
+//   g = dD * U,  dZ = g * act'(Z),  dU = dD * act(Z)
+// (without Z: dZ is dD and only summed) and the column sums of dZ, unrounded, of
+// each chunk into partial[slot][N] (NULL: not wanted).  Packed tensors of type t.
+struct GroupActParams : GroupParams {
+  const void *dD, *U, *dZin;  // dZin: Z
+  void *dZ, *dU;
+  float* partial;
+  int32_t chunk;
+};
+void launch_grouped_act(int t, const GroupActParams& p, int slots, hipStream_t s);
+
+}  // namespace gemm_epi

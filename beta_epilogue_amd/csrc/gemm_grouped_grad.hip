@@ -1,0 +1,53 @@
+// gemm_grouped_grad.hip -- the two matrix products of the experts' backward in
+// one launch, compiled once per type and kernel (GEMM_GROUPED_GRAD_PART 0 .. 7).
+//
+// dA = dZ . B[e] has tiles of each expert's rows; dB[e] = dB_in[e] + dZ^T . A sums
+// over the expert's rows, one set of tiles per expert.  dB's tiles go first: an
+// expert with many rows makes long ones.  dbias is made by further workgroups
+// from the elementwise pass's column sums, in the order of the chunks.
+#include "gemm_grouped.hpp"
+
+#ifndef GEMM_GROUPED_GRAD_PART
+#error "GEMM_GROUPED_GRAD_PART must be defined (0 .. 7)"
+#endif
+
+namespace gemm_epi {
+
+namespace {
+
+// 256 columns of group g's dbias.
+__device__ __forceinline__ void group_sums(const GroupGradParams& p, int block, int* first) {
+  const GroupParams& q = p.a;
+  group_table_rows(q, first, p.chunk);
+  const int per = (int)((p.N + 255) / 256), g = block / per;
+  const int64_t n = (int64_t)(block - g * per) * 256 + threadIdx.x;
+  if (n >= p.N) return;
+  float s = 0.0f;
+  const int last = min(first[g + 1], p.slots);  // (offsets that do not ascend could have more)
+#pragma unroll 8
+  for (int c = first[g]; c < last; ++c) s += p.partial[c * p.N + n];
+  store_as(p.dbias, g * p.N + n, p.dbias_dtype, s);
+}
+
+template <int AB, int KIND>
+__global__ __launch_bounds__(256, grad_occ(KIND)) void grouped_grad_kernel(GroupGradParams p) {
+  using CA = GroupedGradCfg<AB, true, KIND>;
+  using CB = GroupedGradCfg<AB, false, KIND>;
+  constexpr int A_BYTES = CA::LDS_BYTES + kGroupTableBytes;
+  __shared__ __attribute__((aligned(1024))) char lds[A_BYTES > CB::LDS_BYTES ? A_BYTES : CB::LDS_BYTES];
+  const int bid = blockIdx.x;
+  if (bid < p.gb) gemm_epi_body<CB>(p.b, lds, bid, p.gb);
+  else if (bid < p.gb + p.ga) gemm_epi_body<CA>(p.a, lds, bid - p.gb, p.ga);
+  else group_sums(p, bid - p.gb - p.ga, (int*)lds);
+}
+
+}  // namespace
+
+constexpr int kAb = GEMM_GROUPED_GRAD_PART % 2 ? T_BF16 : T_F16, kKind = GEMM_GROUPED_GRAD_PART / 2;
+
+template <>
+void launch_grouped_grad<kAb, kKind>(const GroupGradParams& p, hipStream_t s) {
+  hipLaunchKernelGGL((grouped_grad_kernel<kAb, kKind>), dim3((unsigned)(p.ga + p.gb + p.sums)), dim3(256), 0, s, p);
+}
+
+}  // namespace gemm_epi

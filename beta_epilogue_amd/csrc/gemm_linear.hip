@@ -11,6 +11,7 @@
 #include "gemm_epi_host.hpp"
 #include "gemm_epi_linear.h"
 #include "gemm_linear.hpp"
+#include "gemm_linear_cost.hpp"
 
 using namespace gemm_epi;
 
@@ -33,24 +34,6 @@ constexpr int kThreads = 256;
 constexpr int64_t kRowsMaxN = int64_t(1) << 26;
 // ... and 32 for one of 1024 in the column sums; 256 threads for an item.
 constexpr int64_t kGradMaxN = int64_t(1) << 26, kGradMaxBlocks = int64_t(1) << 24;
-
-// The plan's cost model (us), fitted per type to 1054 forced plans (24 shapes, M
-// 90 to 8192, N 704 to 8192, K 512 to 8192; every tile, 1 to 6 slices), weighted
-// towards each shape's best ones: 3 to 6 % rms from the measured times there, and
-// the plans that it chooses of them take under 1 % longer on the mean, 17 % at worst,
-// than the best measured ones.  An item (a tile or a K slice of one) takes its
-// K tiles times tk plus an epilogue of e0 + e1 * area (in 256x256 tiles); rounds
-// of items fill the compute units.  Smaller tiles of which two or three share a
-// compute unit take pair or three together.  Slices add a second launch, `join`
-// us and their partial sums at bw TB/s.
-struct LinearCost {
-  double start, join, bw, e0, e1;
-  double tk256, tk192, tk128x256, tk128, tk64, pair128, pair64, three64;
-};
-constexpr LinearCost kCost16 = {0.98, 3.65, 21.9, 3.11, 10.4, 1.296, 1.032, 0.0, 0.592, 0.231, 0.821, 0.344, 0.0};
-constexpr LinearCost kCostE4m3 = {1.89, 4.93, 32.2, 2.6, 11.4, 1.373, 1.007, 0.685, 0.407, 0.218, 0.0, 0.329, 0.0};
-constexpr LinearCost kCostI8 = {1.1, 4.2, 21.8, 3.36, 10.8, 1.287, 1.027, 0.0, 0.61, 0.259, 0.856, 0.361, 0.509};
-constexpr LinearCost kCostWide = {2.41, 3.49, 14.5, 2.14, 14.3, 0.0, 0.0, 0.0, 0.796, 0.349, 1.43, 0.53, 0.0};
 
 // Tiles of variant v: the first whole, the last `tail` in K slices of `kslice`.
 struct LinearCut {
@@ -86,15 +69,10 @@ double rows_time(const gemm_epi_linear_desc& d, int64_t cus) {
 }
 
 double linear_time(const LinearVariant& v, const LinearCut& c, const gemm_epi_linear_desc& d, int64_t cus) {
-  const LinearCost& w = v.ab == T_E4M3 ? kCostE4m3 : v.ab == T_I8 ? kCostI8 : v.ab == T_E4M3_WIDE ? kCostWide : kCost16;
-  const double area = (double)v.bm * v.bn / 65536.0, epi = w.e0 + w.e1 * area;
+  const LinearCost& w = linear_cost(v.ab);
+  const double epi = linear_epilogue_time(w, v.bm, v.bn);
   auto rounds = [&](int64_t items, int64_t k) {
-    if (items == 0) return 0.0;
-    double tk = v.bm == 256 ? w.tk256 : v.bm == 192 ? w.tk192 : v.bn == 256 ? w.tk128x256 : v.bm == 128 ? w.tk128 : w.tk64;
-    int64_t slots = cus;
-    if (v.occ >= 2 && items > cus) tk = v.bm == 128 ? w.pair128 : w.pair64, slots = 2 * cus;
-    if (v.occ >= 3 && items > 2 * cus) tk = w.three64, slots = 3 * cus;
-    return (double)((items + slots - 1) / slots) * (tk * (double)((k + v.bk - 1) / v.bk) + epi);
+    return linear_rounds(w, v.bm, v.bn, v.occ, items, (k + v.bk - 1) / v.bk, cus);
   };
   const double products = rounds(c.tiles - c.tail, d.K) + rounds(c.tail * c.splits, std::min(c.kslice, d.K));
   // A and B once from memory, at the 4.5 TB/s that tiles of few rows reach (24

@@ -2,7 +2,7 @@
 // accumulator tile (included by gemm_linear.hpp):
 //   z = alpha * scale_a[m] * scale_b[n] * acc + bias[n]
 //   Z = z (if kept),  D = act(z) + R
-// (LIN 2: D = alpha * acc + R)
+// (LIN 2, 4 and 5: D = alpha * acc + R; LIN 3: D = act(z) * R)
 // in fp32 on the unrounded accumulator (int32 sums are converted first),
 // rounded to nearest-even into the type T that D, R and Z share.
 //
@@ -134,7 +134,7 @@ __device__ __forceinline__ void epilogue_linear(const LinParams& p, const ACC (&
         for (int i = 0; i < VEC; i += 4) {
           const v4f d = epi_dec<T>(r, i / 4);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) v[i + j] += d[j];
+          for (int j = 0; j < 4; ++j) v[i + j] = CF::LIN_MUL ? v[i + j] * d[j] : v[i + j] + d[j];
         }
       }
       epi_st<T>(rd, od + (uint32_t)pass * sd, pack(v));

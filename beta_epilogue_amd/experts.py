@@ -1,6 +1,6 @@
 """Thin Python binding of a mixture of experts' operators
-(include/gemm_epi_experts.h): tokens sorted by expert and their results brought
-back.
+(include/gemm_epi_experts.h): tokens sorted by expert, the experts' linear
+layers and the results brought back.
 
 Plan objects as in ``layers``: a handle for one problem shape, torch tensors
 checked against it, nothing computed in Python.  T tokens choose top_k experts
@@ -14,9 +14,9 @@ import ctypes
 
 import torch
 
-from . import DTYPES, _check
+from . import DTYPES, _check, gemm_epi_plan
 from . import layers
-from .layers import TORCH_DTYPES, _code, _f32, _i32, _i64, _Plan
+from .layers import ACTIVATIONS, TORCH_DTYPES, _code, _i32, _i64, _Plan
 
 IDS_DTYPES = {"i32": torch.int32, "i64": torch.int64}
 
@@ -36,6 +36,21 @@ class gemm_epi_expert_combine_grad_desc(ctypes.Structure):
                 ("x_dtype", _i32)]
 
 
+class gemm_epi_expert_linear_desc(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("N", _i64), ("K", _i64), ("lda", _i64), ("ldd", _i64), ("ldu", _i64), ("ldz", _i64),
+                ("experts", _i32), ("ab_dtype", _i32), ("d_dtype", _i32), ("bias_dtype", _i32), ("act", _i32),
+                ("mul", _i32), ("z", _i32), ("scale_a", _i32), ("scale_b", _i32)]
+
+
+class gemm_epi_expert_linear_grad_desc(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("N", _i64), ("K", _i64), ("experts", _i32), ("ab_dtype", _i32), ("act", _i32),
+                ("mul", _i32), ("da_dtype", _i32), ("db_dtype", _i32), ("dbias_dtype", _i32), ("tile", _i32)]
+
+
+_DESCS = {"expert_sort": gemm_epi_expert_sort_desc, "expert_combine": gemm_epi_expert_combine_desc,
+          "expert_combine_grad": gemm_epi_expert_combine_grad_desc, "expert_linear": gemm_epi_expert_linear_desc,
+          "expert_linear_grad": gemm_epi_expert_linear_grad_desc}
+
 _bound = None
 
 
@@ -45,20 +60,35 @@ def lib():
     if _bound is None:
         L = layers.lib()
         P, I, N = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
-        for op, desc in (("expert_sort", gemm_epi_expert_sort_desc),
-                         ("expert_combine", gemm_epi_expert_combine_desc),
-                         ("expert_combine_grad", gemm_epi_expert_combine_grad_desc)):
+        for op, desc in _DESCS.items():
             create, destroy = getattr(L, "gemm_epi_%s_create" % op), getattr(L, "gemm_epi_%s_destroy" % op)
             create.argtypes, create.restype = [ctypes.POINTER(desc), ctypes.POINTER(P)], I
             destroy.argtypes, destroy.restype = [P], I
         L.gemm_epi_expert_sort_run.argtypes = [P] * 9 + [N, P]
         L.gemm_epi_expert_combine_run.argtypes = [P] * 7
         L.gemm_epi_expert_combine_grad_run.argtypes = [P] * 8
-        for op in ("expert_sort", "expert_combine", "expert_combine_grad"):
+        L.gemm_epi_expert_linear_run.argtypes = [P] * 11
+        L.gemm_epi_expert_linear_grad_run.argtypes = [P] * 14 + [N, P]
+        for op in _DESCS:
             getattr(L, "gemm_epi_%s_run" % op).restype = I
-        L.gemm_epi_expert_sort_workspace.argtypes, L.gemm_epi_expert_sort_workspace.restype = [P], N
+        for op in ("expert_sort", "expert_linear_grad"):
+            f = getattr(L, "gemm_epi_%s_workspace" % op)
+            f.argtypes, f.restype = [P], N
+        f = L.gemm_epi_expert_linear_create_variant
+        f.argtypes, f.restype = [ctypes.POINTER(gemm_epi_expert_linear_desc), I, ctypes.POINTER(P)], I
+        L.gemm_epi_expert_linear_get_plan.argtypes = [P, ctypes.POINTER(gemm_epi_plan)]
+        L.gemm_epi_expert_linear_get_plan.restype = I
+        L.gemm_epi_expert_linear_variant_count.argtypes, L.gemm_epi_expert_linear_variant_count.restype = [], I
+        L.gemm_epi_expert_linear_variant_name.argtypes = [I]
+        L.gemm_epi_expert_linear_variant_name.restype = ctypes.c_char_p
         _bound = L
     return _bound
+
+
+def expert_linear_variant_names() -> list:
+    """Names of the experts' linear layer's kernels, by variant number."""
+    L = lib()
+    return [L.gemm_epi_expert_linear_variant_name(i).decode() for i in range(L.gemm_epi_expert_linear_variant_count())]
 
 
 class _ExpertPlan(_Plan):
@@ -164,3 +194,91 @@ class ExpertCombineGrad(_ExpertPlan):
         if code:
             _check(code, "gemm_epi_expert_combine_grad_run")
         return dY
+
+
+class ExpertLinear(_ExpertPlan):
+    """D[r] = act(scale_a[r] * scale_b[e] * (A[r] . B[e]^T) + bias[e]) * U[r] for
+    the rows r of every expert e.
+
+    A is rows x K (``ExpertSort``'s Y), B experts x N x K (packed), bias and
+    scale_b experts x N, scale_a rows, D, U and Z rows x N; rows is the batch's
+    capacity, tokens * top_k.  ab: f16, bf16, e4m3 or i8; d (of D, U and Z):
+    f16, bf16 or f32.  bias: its type, or None; mul, z, scale_a, scale_b:
+    whether the call has U, Z and the scales.  Z receives the pre-activation,
+    which ``ExpertLinearGrad`` takes.  A gated layer is two calls: U = ExpertLinear
+    of one weight, then act and mul with the other.  variant forces a kernel.
+    """
+
+    _op = "expert_linear"
+
+    def __init__(self, rows, experts, N, K, *, ab="bf16", d=None, act="none", bias=None, mul=False, z=False,
+                 scale_a=False, scale_b=False, lda=0, ldd=0, ldu=0, ldz=0, variant=-1):
+        d = d or (ab if ab in ("f16", "bf16") else "bf16")
+        super().__init__(gemm_epi_expert_linear_desc(
+            rows, N, K, lda, ldd, ldu, ldz, experts, _code(DTYPES, ab, "type"), _code(DTYPES, d, "type"),
+            _code(DTYPES, bias, "type"), _code(ACTIVATIONS, act, "activation"), int(mul), int(z), int(scale_a),
+            int(scale_b)), variant)
+        ab, d, bias = TORCH_DTYPES[ab], TORCH_DTYPES[d], TORCH_DTYPES[bias] if bias else None
+        m, v = self._matrix, self._vector
+        self._specs = (m("A", ab, rows, K, lda or K), ("B", ab, (experts, N, K), (N * K, K, 1)),
+                       v("offsets", torch.int32, experts + 1), m("bias", bias, experts, N, N),
+                       v("scale_a", torch.float32, rows), m("scale_b", torch.float32, experts, N, N),
+                       m("U", d, rows, N, ldu or N), m("D", d, rows, N, ldd or N), m("Z", d, rows, N, ldz or N))
+
+    @property
+    def plan(self) -> dict:
+        p = gemm_epi_plan()
+        _check(lib().gemm_epi_expert_linear_get_plan(self.handle, ctypes.byref(p)), "gemm_epi_expert_linear_get_plan")
+        return {k: getattr(p, k) for k, _ in p._fields_ if k != "name"} | {"name": p.name.decode()}
+
+    def __call__(self, A, B, offsets, *, D, bias=None, scale_a=None, scale_b=None, U=None, Z=None, stream=None):
+        ptr = self._ptr
+        a, b, o, bs, sa, sb, u, d, z = self._specs
+        code = self._run(self.handle, ptr(A, a), ptr(B, b), ptr(offsets, o), ptr(bias, bs), ptr(scale_a, sa),
+                         ptr(scale_b, sb), ptr(U, u), ptr(D, d), ptr(Z, z), self._stream(stream)[0])
+        if code:
+            _check(code, "gemm_epi_expert_linear_run")
+        return D
+
+
+class ExpertLinearGrad(_ExpertPlan):
+    """The gradients of ``ExpertLinear`` without scales.
+
+    g = dD * U, dZ = g * act'(Z), dU = dD * act(Z), dA[r] = dZ[r] . B[e], and over
+    every expert's rows dB[e] = dB_in[e] + dZ^T . A, dbias[e] = the column sums of
+    dZ.  All tensors are packed; dD, Z, U, dZ, dU, A and B have type ab (f16 or
+    bf16).  da, db, dbias: the gradients' types, None for one not wanted.
+    Without an activation and mul dD takes dZ's place and Z and dZ are not given.
+    tile (64, 128 or 256) forces the products' tile.
+    """
+
+    _op = "expert_linear_grad"
+
+    def __init__(self, rows, experts, N, K, *, ab="bf16", act="none", mul=False, da=None, db=None, dbias=None, tile=0):
+        super().__init__(gemm_epi_expert_linear_grad_desc(
+            rows, N, K, experts, _code(DTYPES, ab, "type"), _code(ACTIVATIONS, act, "activation"), int(mul),
+            _code(DTYPES, da, "type"), _code(DTYPES, db, "type"), _code(DTYPES, dbias, "type"), tile))
+        ab = TORCH_DTYPES[ab]
+        da, db, dbias = (TORCH_DTYPES[t] if t else None for t in (da, db, dbias))
+        m, E = self._matrix, experts
+        w = (N * K, K, 1)
+        self._specs = (m("dD", ab, rows, N, N), m("A", ab, rows, K, K), ("B", ab, (E, N, K), w),
+                       self._vector("offsets", torch.int32, E + 1), m("Z", ab, rows, N, N), m("U", ab, rows, N, N),
+                       ("dB_in", db, (E, N, K), w), m("dZ", ab, rows, N, N), m("dU", ab, rows, N, N),
+                       m("dA", da, rows, K, K), ("dB", db, (E, N, K), w), m("dbias", dbias, E, N, N))
+        self._wants = (da is not None, db is not None)
+        self.workspace_bytes = lib().gemm_epi_expert_linear_grad_workspace(self.handle)
+
+    def __call__(self, dD, A, B, offsets, *, Z=None, U=None, dB_in=None, dZ=None, dU=None, dA=None, dB=None,
+                 dbias=None, stream=None, workspace=None):
+        ptr = self._ptr
+        sd, sa, sb, so, sz, su, sc, gz, gu, ga, gb, gs = self._specs
+        wants_a, wants_b = self._wants
+        raw, s = self._stream(stream)
+        ws, nbytes, keep = self._workspace(self.workspace_bytes, workspace, s)
+        # (an operand that the wanted gradients do not need is not passed on)
+        code = self._run(self.handle, ptr(dD, sd), ptr(A if wants_b else None, sa), ptr(B if wants_a else None, sb),
+                         ptr(offsets, so), ptr(Z, sz), ptr(U, su), ptr(dB_in, sc), ptr(dZ, gz), ptr(dU, gu),
+                         ptr(dA, ga), ptr(dB, gb), ptr(dbias, gs), ws, nbytes, raw)
+        if code:
+            _check(code, "gemm_epi_expert_linear_grad_run")

@@ -114,6 +114,95 @@ int gemm_epi_expert_combine_grad_run(const gemm_epi_expert_combine_grad_handle* 
                                      void* stream);
 int gemm_epi_expert_combine_grad_destroy(gemm_epi_expert_combine_grad_handle* h);
 
+typedef struct gemm_epi_expert_linear_desc {
+  int64_t rows;         /* the sorted batch's capacity (tokens * top_k), >= 1 */
+  int64_t N, K;         /* an expert's outputs and inputs, >= 1 */
+  int64_t lda;          /* elements between rows of A; 0: K */
+  int64_t ldd, ldu, ldz; /* of D, U and Z; 0: N */
+  int32_t experts;      /* 1 .. 1024 */
+  int32_t ab_dtype;     /* F16, BF16, E4M3 or I8 */
+  int32_t d_dtype;      /* F16, BF16 or F32: D, U and Z */
+  int32_t bias_dtype;   /* NONE, F16, BF16 or F32 */
+  int32_t act;          /* GEMM_EPI_ACT_* */
+  int32_t mul;          /* 1: D = act(z) * U */
+  int32_t z;            /* 1: Z is written */
+  int32_t scale_a;      /* 1: one fp32 scale per row */
+  int32_t scale_b;      /* 1: one fp32 scale per expert and output */
+} gemm_epi_expert_linear_desc;
+
+typedef struct gemm_epi_expert_linear_handle gemm_epi_expert_linear_handle;
+
+/* Validate and plan: a kernel for few rows per expert, which streams the weights
+ * of the experts that have rows, or a tile kernel, by a cost model that takes the
+ * rows as evenly spread (the result never depends on it).  Types and errors as for
+ * gemm_epi_linear_create; an expert's bias must be a multiple of 16 bytes long. */
+int gemm_epi_expert_linear_create(const gemm_epi_expert_linear_desc* desc, gemm_epi_expert_linear_handle** out);
+
+/* The same with kernel `variant` (-1: the plan's choice); one that cannot run the
+ * problem is UNSUPPORTED. */
+int gemm_epi_expert_linear_create_variant(const gemm_epi_expert_linear_desc* desc, int variant,
+                                          gemm_epi_expert_linear_handle** out);
+
+/*
+ * Enqueue D (and Z) for rows 0 .. offsets[experts] - 1.  A is rows x K, B experts x
+ * N x K (packed), bias experts x N, scale_a rows, scale_b experts x N, U, D and Z
+ * rows x N.  D may be U itself (with ldd == ldu); no other overlap of an output
+ * with another tensor is allowed.
+ */
+int gemm_epi_expert_linear_run(const gemm_epi_expert_linear_handle* h, const void* A, const void* B,
+                               const int32_t* offsets, const void* bias, const float* scale_a, const float* scale_b,
+                               const void* U, void* D, void* Z, void* stream);
+int gemm_epi_expert_linear_destroy(gemm_epi_expert_linear_handle* h);
+
+/* What a handle launches (tiles and grid: for the worst distribution of the rows;
+ * few rows: chunks of tile_m rows by tile_n weight rows per workgroup). */
+int gemm_epi_expert_linear_get_plan(const gemm_epi_expert_linear_handle* h, gemm_epi_plan* out);
+
+/* Number of the experts' kernels and the name of one (NULL out of range). */
+int gemm_epi_expert_linear_variant_count(void);
+const char* gemm_epi_expert_linear_variant_name(int variant);
+
+typedef struct gemm_epi_expert_linear_grad_desc {
+  int64_t rows, N, K;   /* the forward's; all tensors packed */
+  int32_t experts;
+  int32_t ab_dtype;     /* F16 or BF16: dD, Z, U, dZ, dU, A and B */
+  int32_t act;          /* the forward's activation */
+  int32_t mul;          /* the forward's */
+  int32_t da_dtype;     /* NONE (no dA), F16, BF16 or F32 */
+  int32_t db_dtype;     /* NONE (no dB), F16, BF16 or F32: dB and dB_in */
+  int32_t dbias_dtype;  /* NONE (no dbias), F16, BF16 or F32 */
+  int32_t tile;         /* 0: the plan's choice; 64, 128 or 256: that tile */
+} gemm_epi_expert_linear_grad_desc;
+
+typedef struct gemm_epi_expert_linear_grad_handle gemm_epi_expert_linear_grad_handle;
+
+/*
+ * Validate and plan a backward (of a forward without scales): an elementwise
+ * pass, then one launch for both products and dbias.  dZ is rounded to ab_dtype,
+ * the type the matrix cores read; dbias is summed before that rounding, in a
+ * fixed order.  UNSUPPORTED as well: an expert's B, or with dB the whole of A or dZ,
+ * of 2 GiB or more; 2^24 or more work items.
+ */
+int gemm_epi_expert_linear_grad_create(const gemm_epi_expert_linear_grad_desc* desc,
+                                       gemm_epi_expert_linear_grad_handle** out);
+
+/*
+ * Enqueue the gradients.  dD and offsets are required; A exactly for dB, B exactly
+ * for dA; Z and dZ exactly with an activation or mul (else dD takes dZ's place), U and dU
+ * exactly with mul; dA, dB, dbias exactly when their types are set; dB_in (or NULL:
+ * 0) only with dB.  Rows of dZ, dU and dA behind the last expert's are left as they
+ * are; an expert without rows gets dB[e] = dB_in[e] and dbias[e] = 0.  dZ may be dD
+ * or Z, dU may be U and dB may be dB_in itself; no other overlap of an output with
+ * another tensor is allowed.
+ */
+int gemm_epi_expert_linear_grad_run(const gemm_epi_expert_linear_grad_handle* h, const void* dD, const void* A,
+                                    const void* B, const int32_t* offsets, const void* Z, const void* U,
+                                    const void* dB_in, void* dZ, void* dU, void* dA, void* dB, void* dbias,
+                                    void* workspace, int64_t workspace_bytes, void* stream);
+int gemm_epi_expert_linear_grad_destroy(gemm_epi_expert_linear_grad_handle* h);
+/* Bytes of workspace a run needs (-1 for a NULL handle). */
+int64_t gemm_epi_expert_linear_grad_workspace(const gemm_epi_expert_linear_grad_handle* h);
+
 #ifdef __cplusplus
 }
 #endif

@@ -87,6 +87,57 @@ def test_combine_grad_validation(bad, code):
     assert _create("expert_combine_grad", **(good | bad)) == code, ge.last_error()
 
 
+LINEAR = dict(rows=100, experts=8, N=256, K=512, ab_dtype=T["bf16"], d_dtype=T["bf16"])
+LINEAR_BAD = [
+    (dict(rows=0), INVALID), (dict(N=-1), INVALID), (dict(K=0), INVALID), (dict(experts=0), INVALID),
+    (dict(experts=1025), INVALID), (dict(ab_dtype=0), INVALID), (dict(ab_dtype=T["f32"]), INVALID),
+    (dict(ab_dtype=T["e5m2"]), UNSUPPORTED), (dict(ab_dtype=T["u8"]), UNSUPPORTED), (dict(d_dtype=T["i32"]), INVALID),
+    (dict(d_dtype=0), INVALID), (dict(bias_dtype=T["i8"]), INVALID), (dict(act=5), INVALID), (dict(act=-1), INVALID),
+    (dict(mul=2), INVALID), (dict(z=-1), INVALID), (dict(scale_a=3), INVALID), (dict(scale_b=-1), INVALID),
+    (dict(K=516), ALIGN), (dict(N=252), ALIGN), (dict(ab_dtype=T["e4m3"], K=520), ALIGN), (dict(lda=500), INVALID),
+    (dict(lda=516), ALIGN), (dict(ldd=260), ALIGN), (dict(ldu=256), INVALID), (dict(ldz=256), INVALID),
+    (dict(N=260, d_dtype=T["f32"], bias_dtype=T["f16"]), ALIGN),
+    (dict(lda=1 << 40), UNSUPPORTED), (dict(K=1 << 40), UNSUPPORTED), (dict(N=1 << 40), UNSUPPORTED),
+    (dict(rows=1 << 40), UNSUPPORTED), (dict(rows=(1 << 63) - 1), UNSUPPORTED), (dict(ab_dtype=T["i8"], K=1 << 17), UNSUPPORTED),
+]
+
+
+@pytest.mark.parametrize("bad,code", LINEAR_BAD, ids=lambda v: str(v))
+def test_linear_validation(bad, code):
+    assert _create("expert_linear", **(LINEAR | bad)) == code, ge.last_error()
+
+
+GRAD = dict(rows=100, experts=8, N=256, K=512, ab_dtype=T["bf16"], da_dtype=T["bf16"], db_dtype=T["f32"],
+            dbias_dtype=T["f32"])
+GRAD_BAD = [
+    (dict(rows=0), INVALID), (dict(K=-5), INVALID), (dict(experts=2000), INVALID), (dict(ab_dtype=0), INVALID),
+    (dict(ab_dtype=T["e4m3"]), UNSUPPORTED), (dict(act=9), INVALID), (dict(mul=-1), INVALID),
+    (dict(da_dtype=T["i32"]), INVALID), (dict(dbias_dtype=T["e4m3"]), INVALID),
+    (dict(da_dtype=0, db_dtype=0, dbias_dtype=0), INVALID), (dict(N=250), ALIGN), (dict(K=500), ALIGN),
+    (dict(tile=32), INVALID), (dict(rows=1 << 62), UNSUPPORTED), (dict(K=1 << 22), UNSUPPORTED),
+    (dict(rows=1 << 22), UNSUPPORTED),  # A of 2 GiB or more
+]
+
+
+@pytest.mark.parametrize("bad,code", GRAD_BAD, ids=lambda v: str(v))
+def test_linear_grad_validation(bad, code):
+    assert _create("expert_linear_grad", **(GRAD | bad)) == code, ge.last_error()
+
+
+def test_linear_variants():
+    names = ge.expert_linear_variant_names()
+    assert len(set(names)) == len(names) and names[-1] == "experts_rows32"
+    L = experts.lib()
+    assert L.gemm_epi_expert_linear_variant_name(-1) is None
+    assert L.gemm_epi_expert_linear_variant_name(len(names)) is None
+    d, h = experts.gemm_epi_expert_linear_desc(**LINEAR), ctypes.c_void_p()
+    create = L.gemm_epi_expert_linear_create_variant
+    assert create(ctypes.byref(d), len(names), ctypes.byref(h)) == INVALID
+    assert create(ctypes.byref(d), names.index("experts_f16_256x256"), ctypes.byref(h)) == UNSUPPORTED
+    d.rows = 1 << 20  # more chunks of four rows than a launch's second dimension has
+    assert create(ctypes.byref(d), names.index("experts_rows4"), ctypes.byref(h)) == UNSUPPORTED
+
+
 def test_valid_problems_stop_at_the_device():
     if torch.cuda.is_available():
         pytest.skip("a GPU is present")
@@ -94,13 +145,18 @@ def test_valid_problems_stop_at_the_device():
                  dict(x_dtype=T["e4m3"], scale=1), dict(tokens=1 << 20, top_k=8, experts=1024, x_dtype=T["f32"])):
         assert _create("expert_sort", **(SORT | more)) == DEVICE, ge.last_error()
     assert _create("expert_combine", **(COMBINE | dict(residual=1, ldr=128))) == DEVICE
+    for more in ({}, dict(rows=1), dict(ab_dtype=T["e4m3"], d_dtype=T["f32"], scale_a=1, scale_b=1),
+                 dict(lda=520, ldd=264, mul=1, ldu=264, z=1, act=4, bias_dtype=T["f16"])):
+        assert _create("expert_linear", **(LINEAR | more)) == DEVICE, ge.last_error()
+    assert _create("expert_linear_grad", **GRAD) == DEVICE
+    assert _create("expert_linear_grad", **(GRAD | dict(da_dtype=0, db_dtype=0, dbias_dtype=0, mul=1))) == DEVICE
     assert _create("expert_combine_grad", **{k: v for k, v in COMBINE.items() if k != "weights"}) == DEVICE
 
 
 def test_null_arguments():
     L = experts.lib()
     h = ctypes.c_void_p()
-    for op in ("expert_sort", "expert_combine", "expert_combine_grad"):
+    for op in experts._DESCS:
         assert getattr(L, "gemm_epi_%s_create" % op)(None, ctypes.byref(h)) == INVALID
         desc = getattr(experts, "gemm_epi_%s_desc" % op)()
         assert getattr(L, "gemm_epi_%s_create" % op)(ctypes.byref(desc), None) == INVALID
@@ -108,7 +164,11 @@ def test_null_arguments():
     assert L.gemm_epi_expert_sort_run(None, 16, 16, None, 16, 16, 16, None, None, 0, None) == INVALID
     assert L.gemm_epi_expert_combine_run(None, 16, 16, None, None, 16, None) == INVALID
     assert L.gemm_epi_expert_combine_grad_run(None, 16, 16, 16, 16, 16, 16, None) == INVALID
-    assert L.gemm_epi_expert_sort_workspace(None) == -1
+    assert L.gemm_epi_expert_linear_run(None, 16, 16, 16, None, None, None, None, 16, None, None) == INVALID
+    assert L.gemm_epi_expert_linear_grad_run(None, 16, 16, 16, 16, None, None, None, None, None, 16, 16, None, None, 0,
+                                             None) == INVALID
+    assert L.gemm_epi_expert_linear_get_plan(None, ctypes.byref(ge.gemm_epi_plan())) == INVALID
+    assert L.gemm_epi_expert_sort_workspace(None) == -1 and L.gemm_epi_expert_linear_grad_workspace(None) == -1
 
 
 def test_unknown_names_are_refused():
