@@ -995,19 +995,25 @@ struct GroupTile {
   int group, begin, end;  // the group and its rows
   int first, tiles;       // its first row tile among all groups', and their number
 };
-template <class CF>
-__device__ int group_table(const GroupParams& p, int* first);
+// What a workgroup does of a GROUP_ROWS problem: items begin .. end - 1, of the
+// table of groups `first` (in LDS).  quarter: an item is a quarter of a tile of
+// twice the height and width, which the table counts.
+struct GroupWork {
+  const int* first;
+  int begin, end, quarter;
+};
 __device__ GroupTile group_of_tile(const GroupParams& p, const int* first, int row_tile);
 __device__ GroupTile group_rows(const GroupParams& p, int group);
+__device__ int group_k_item(const GroupParams& p, int bid);
 
 // ---------------------------------------------------------------------------
 // The kernel
 // ---------------------------------------------------------------------------
 // The work of workgroup `bid` of `G` that share a problem, with the LDS array
-// `lds` of CF::LDS_BYTES (1 KiB aligned; GROUP_ROWS: and the table of groups
-// behind them).
+// `lds` of CF::LDS_BYTES (1 KiB aligned).  GROUP_ROWS: its share of `work`.
 template <class CF>
-__device__ __forceinline__ void gemm_epi_body(const typename CF::params_t& p, char* lds, int bid, int G) {
+__device__ __forceinline__ void gemm_epi_body(const typename CF::params_t& p, char* lds, int bid, int G,
+                                              GroupWork work = {}) {
   using MM = typename CF::MM;
   using acc_t = typename MM::acc_t;
   using frag_t = typename MM::frag_t;
@@ -1020,19 +1026,19 @@ __device__ __forceinline__ void gemm_epi_body(const typename CF::params_t& p, ch
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave % CF::WAVES_M, wn = wave / CF::WAVES_M;
 
-  int tiles_total = p.tiles_total;
-  [[maybe_unused]] const int* group_first = (const int*)(lds + CF::LDS_BYTES);
+  // (only the workgroups that have an item share the runs below)
   if constexpr (CF::GROUP == GROUP_ROWS) {
-    // row tiles of all groups; the workgroups that have one share the runs below
-    tiles_total = group_table<CF>(p, (int*)(lds + CF::LDS_BYTES)) * p.tiles_n;
-    G = min(G, tiles_total);
+    G = min(G, work.end - work.begin);
     if (bid >= G) return;
   }
 
   // (the linear kernels' grids need not be multiples of 8: the first G % 8
   // XCDs take one more)
   const int over = CF::LIN ? min(bid & 7, G & 7) : 0;
-  const int g = p.xcd_remap ? (bid & 7) * (G >> 3) + over + (bid >> 3) : bid;
+  int g = p.xcd_remap ? (bid & 7) * (G >> 3) + over + (bid >> 3) : bid;
+  int tiles_total = p.tiles_total;
+  if constexpr (CF::GROUP == GROUP_ROWS) g += work.begin, tiles_total = work.end;
+  if constexpr (CF::GROUP == GROUP_K) g = group_k_item(p, bid);
 
   using OpA = Operand<CF, BM, CF::WM, CF::A_KMAJOR>;
   using OpB = Operand<CF, BN, CF::WN, CF::B_KMAJOR>;
@@ -1056,8 +1062,9 @@ __device__ __forceinline__ void gemm_epi_body(const typename CF::params_t& p, ch
     [[maybe_unused]] GroupTile gt = {};
     int tiles_m = p.tiles_m;
     if constexpr (CF::GROUP == GROUP_ROWS) {
-      gt = group_of_tile(p, group_first, (int)((unsigned)t / (unsigned)p.tiles_n));
-      ts = t - gt.first * p.tiles_n;
+      ts = work.quarter ? t >> 2 : t;
+      gt = group_of_tile(p, work.first, (int)((unsigned)ts / (unsigned)p.tiles_n));
+      ts -= gt.first * p.tiles_n;
       tiles_m = gt.tiles;
     }
     if (CF::GROUP == GROUP_NONE && t >= p.dp_tiles) {
@@ -1077,7 +1084,12 @@ __device__ __forceinline__ void gemm_epi_body(const typename CF::params_t& p, ch
     const int64_t kbytes = (split < 0 ? K : min(K - kbeg, p.kslice)) * ES;  // this item's K, in bytes
     int KT = (int)((kbytes + CF::ROWB - 1) / CF::ROWB);
     if constexpr (CF::GROUP == GROUP_K) KT = max(KT, 1);  // (a group without rows: one K tile of zeros)
-    const int m0 = (CF::GROUP == GROUP_ROWS ? gt.begin : 0) + tc.tm * BM, n0 = tc.tn * BN;
+    int m0 = tc.tm * BM, n0 = tc.tn * BN;
+    if constexpr (CF::GROUP == GROUP_ROWS) {
+      if (work.quarter) m0 = 2 * m0 + (t & 1) * BM, n0 = 2 * n0 + ((t >> 1) & 1) * BN;
+      m0 += gt.begin;
+      if (m0 >= gt.end || n0 >= p.N) continue;  // (a quarter outside the group)
+    }
 
     // ---- staging set-up --------------------------------------------------
     if constexpr (CF::GROUP == GROUP_ROWS) {

@@ -28,10 +28,11 @@ const GroupedVariant kGrouped[] = {
 };
 #undef X
 constexpr int kTiles = (int)(sizeof kGrouped / sizeof kGrouped[0]);
-// The few-row kernels: chunks of 4, 8, 16 and 32 rows.
-constexpr int kRowsBlocks[] = {1, 2, 4, 8};
-const char* const kRowsNames[] = {"experts_rows4", "experts_rows8", "experts_rows16", "experts_rows32"};
-constexpr int kVariants = kTiles + 4;
+// The few-row kernels: chunks of 4 and 16 rows.  (8 and 32 were never ahead of
+// both and the 64x64 tiles by more than 3 %.)
+constexpr int kRowsBlocks[] = {1, 4};
+const char* const kRowsNames[] = {"experts_rows4", "experts_rows16"};
+constexpr int kVariants = kTiles + 2;
 
 typedef void (*part_fn)(int, const GroupParams&, int, hipStream_t);
 const part_fn kParts[kGroupedParts] = {launch_grouped_part<0>, launch_grouped_part<1>, launch_grouped_part<2>,
@@ -45,30 +46,42 @@ int64_t worst_chunks(int64_t rows, int64_t experts, int64_t chunk) {
   return n + (rows - n) / chunk;
 }
 
-// ... and an even distribution.
-int64_t even_chunks(int64_t rows, int64_t experts, int64_t chunk) {
-  const int64_t n = std::min(rows, experts), per = (rows + n - 1) / n;
-  return n * ((per + chunk - 1) / chunk);
+// ... and that are to be expected of a router: an expert's last chunk is half full
+// on the mean, and there is one at least.
+double likely_chunks(int64_t rows, int64_t experts, int64_t chunk) {
+  const double n = (double)std::min(rows, experts), per = (double)rows / n;
+  return n * std::max(1.0, per / (double)chunk + (per > 1.0 ? 0.5 : 0.0));
 }
 
-// Modelled time (us) of a tile kernel with the rows spread evenly: the linear
-// layer's model, whose items are each expert's tiles, and the weights of the
-// experts that have rows once from memory.
+// Modelled time (us) of a tile kernel: the linear layer's model over the tiles
+// that are to be expected (half a round on the mean for the last one; 256x256 tiles
+// may finish it as quarters), and the weights of the experts that have rows once
+// from memory, at the 5.2 TB/s that the 64x64 tiles reach (512 rows, 64 experts,
+// bf16 1536 x 2048: 78 us).
 double tiles_time(const GroupedVariant& v, const gemm_epi_expert_linear_desc& d, int64_t cus) {
   const LinearCost& w = linear_cost(v.ab);
-  const int64_t items = even_chunks(d.rows, d.experts, v.bm) * ((d.N + v.bn - 1) / v.bn);
+  const double items = likely_chunks(d.rows, d.experts, v.bm) * (double)((d.N + v.bn - 1) / v.bn);
+  const double epi = linear_epilogue_time(w, v.bm, v.bn);
+  double tk = v.bm == 256 ? w.tk256 : v.bm == 128 ? w.tk128 : w.tk64, slots = (double)cus;
+  if (v.occ >= 2 && items > (double)cus) tk = v.bm == 128 ? w.pair128 : w.pair64, slots *= 2;
+  if (v.occ >= 3 && items > 2.0 * (double)cus) tk = w.three64, slots *= 1.5;
+  const double item = tk * (double)((d.K + v.bk - 1) / v.bk) + epi;
+  const double rounds = std::max(1.0, items / slots + (v.bm == 256 ? 0.35 : 0.5));
   const double es = elem_bytes(d.ab_dtype), n = (double)std::min<int64_t>(d.rows, d.experts);
-  const double stream = (n * (double)d.N + (double)d.rows) * (double)d.K * es / 4.5e6;
-  return w.start + std::max(linear_rounds(w, v.bm, v.bn, v.occ, items, (d.K + v.bk - 1) / v.bk, cus),
-                            stream + linear_epilogue_time(w, v.bm, v.bn));
+  const double stream = (n * (double)d.N + (double)d.rows) * (double)d.K * es / 5.2e6;
+  return w.start + std::max(rounds * item, stream);
 }
 
+// The few-row kernels: a workgroup's waves stream runs of 256 bytes of K each; a
+// run costs its latency or, with every compute unit at work, its share of the
+// bandwidth.  Within a fifth of 14 shapes of 1 to 128 rows, N 256 to 4096, K 768 to
+// 8192, bf16 and e4m3.
 double rows_time(int mb, const gemm_epi_expert_linear_desc& d, int64_t cus) {
-  const int nw = mb <= 2 ? 8 : 4;
-  const double runs = (double)((d.K * elem_bytes(d.ab_dtype) + nw * 256 - 1) / (nw * 256));
-  const double blocks = (double)even_chunks(d.rows, d.experts, 4 * mb) * (double)((d.N + 15) / 16);
-  const double busy = 1.9 * nw / 8, latency = 1.2;
-  return std::max(4.5 + runs * latency, 3.0 + runs * std::max(1.0, blocks / (double)cus) * busy);
+  const int bytes = mb == 1 ? 8 * 256 : 4 * 256;  // of K, all waves' runs
+  const double runs = (double)((d.K * elem_bytes(d.ab_dtype) + bytes - 1) / bytes);
+  const double blocks = likely_chunks(d.rows, d.experts, 4 * mb) * (double)((d.N + 15) / 16) / (double)cus;
+  const double latency = mb == 1 ? 0.55 : 0.37;
+  return std::max(4.2 + runs * latency, 3.0 + blocks * (mb == 1 ? runs * 1.3 + 1.0 : runs * 0.67 + 1.3));
 }
 
 // As the linear layer's: row stride `ld` (0: packed) of a tensor with `cols`
@@ -184,8 +197,8 @@ extern "C" int gemm_epi_expert_linear_create_variant(const gemm_epi_expert_linea
     const GroupedVariant& v = kGrouped[variant];
     h.tiles_n = (d.N + v.bn - 1) / v.bn;
     const int64_t tiles_m = worst_chunks(d.rows, d.experts, v.bm);
-    if (tiles_m >= (int64_t(1) << 31) / h.tiles_n)
-      return fail(GEMM_EPI_ERR_UNSUPPORTED, "2^31 or more tiles");
+    if (tiles_m >= (int64_t(1) << 29) / h.tiles_n)  // their quarters are counted in 32 bits
+      return fail(GEMM_EPI_ERR_UNSUPPORTED, "2^29 or more tiles");
     h.grid = std::min<int64_t>(tiles_m * h.tiles_n, (int64_t)cus * v.occ);
   } else {
     h.tiles_n = (d.N + 15) / 16;
@@ -274,7 +287,7 @@ extern "C" int gemm_epi_expert_linear_get_plan(const gemm_epi_expert_linear_hand
     const int mb = kRowsBlocks[h->variant - kTiles];
     out->tile_m = 4 * mb;
     out->tile_n = 16;
-    out->threads = (mb <= 2 ? 8 : 4) * 64;
+    out->threads = (mb == 1 ? 8 : 4) * 64;
     out->tiles = h->grid * h->tiles_n;
     out->grid = (int)std::min<int64_t>(out->tiles, INT32_MAX);
   } else {
@@ -388,14 +401,14 @@ extern "C" int gemm_epi_expert_linear_grad_create(const gemm_epi_expert_linear_g
   }
   const int64_t tn = (d.N + h.tile - 1) / h.tile, tk = (d.K + h.tile - 1) / h.tile;
   h.ga = d.da_dtype != GEMM_EPI_NONE ? worst_chunks(d.rows, d.experts, h.tile) * tk : 0;
-  h.gb = d.db_dtype != GEMM_EPI_NONE ? d.experts * tn * tk : 0;
+  h.gb = d.db_dtype != GEMM_EPI_NONE ? 8 * d.experts * ((tn * tk + 7) / 8) : 0;
   h.sums = d.dbias_dtype != GEMM_EPI_NONE ? d.experts * ((d.N + 255) / 256) : 0;
   // 256 threads for each, fewer than 2^32 in all
   if (h.ga + h.gb + h.sums >= int64_t(1) << 24) return fail(GEMM_EPI_ERR_UNSUPPORTED, "2^24 or more work items");
   // rows per workgroup of the elementwise pass: 64, fewer as long as there are under
   // four workgroups for a compute unit, more where 2^16 chunks would not do
   h.chunk = 64;
-  while (h.chunk > 8 && (d.N + 255) / 256 * even_chunks(d.rows, d.experts, h.chunk) < 4 * cus) h.chunk /= 2;
+  while (h.chunk > 8 && (d.N + 255) / 256 * worst_chunks(d.rows, d.experts, h.chunk) < 4 * cus) h.chunk /= 2;
   while (worst_chunks(d.rows, d.experts, h.chunk) > 65535) h.chunk *= 2;
   h.slots = worst_chunks(d.rows, d.experts, h.chunk);
   h.ws_bytes = d.dbias_dtype != GEMM_EPI_NONE ? up256(h.slots * d.N * 4) : 0;
@@ -494,7 +507,10 @@ extern "C" int gemm_epi_expert_linear_grad_run(const gemm_epi_expert_linear_grad
   p.b.K = d.rows;
   p.b.d_dtype = d.db_dtype;
   p.b.tiles_m = (int32_t)((d.N + h->tile - 1) / h->tile);
-  p.b.tiles_total = (int32_t)h->gb;
+  p.b.tiles_total = d.experts * p.b.tiles_m * p.b.tiles_n;
+  // the last items should be short ones: dA's are N long, dB's (the longest first)
+  // the experts' rows
+  p.b_first = d.rows > d.experts * d.N;
   p.ga = (int32_t)h->ga;
   p.gb = (int32_t)h->gb;
   p.sums = (int32_t)h->sums;

@@ -44,6 +44,30 @@ __device__ __forceinline__ int wave_scan(int v, int lane) {
   return v;
 }
 
+// GROUP_K: the item (tile of a group's output) of workgroup bid of 8 * groups *
+// ceil(tiles / 8), tiles_total for none.  Workgroups go round the 8 XCDs, and a
+// group with many rows has long items: every group's tiles are spread over all
+// XCDs, and the groups with the most rows (of up to 64) go first.
+__device__ __forceinline__ int group_k_item(const GroupParams& p, int bid) {
+  const int tiles = p.tiles_m * p.tiles_n, per = (tiles + 7) >> 3, lane = __lane_id();
+  int e = (int)((unsigned)(bid >> 3) / (unsigned)per);
+  const int j = (bid >> 3) - e * per;
+  if (p.groups <= 64) {
+    int rows = -1, before = 0;
+    if (lane < p.groups) {
+      const GroupTile t = group_rows(p, lane);
+      rows = t.end - t.begin;
+    }
+    for (int l = 0; l < p.groups; ++l) {
+      const int other = __builtin_amdgcn_readlane(rows, l);
+      before += other > rows || (other == rows && l < lane) ? 1 : 0;
+    }
+    e = __ffsll((unsigned long long)__ballot(lane < p.groups && before == e)) - 1;
+  }
+  const int tile = (((bid & 7) + e) & 7) * per + j;
+  return __builtin_amdgcn_readfirstlane(tile < tiles ? e * tiles + tile : p.tiles_total);
+}
+
 // The table of groups in LDS: first[g] = tiles of `rows` rows in the groups
 // before g (first[groups]: in all, returned).  All threads of the workgroup.
 constexpr int kGroupTableBytes = (kMaxExperts + 1) * 4 + 12;
@@ -66,10 +90,6 @@ __device__ __forceinline__ int group_table_rows(const GroupParams& p, int* first
   }
   __syncthreads();
   return __builtin_amdgcn_readfirstlane(first[p.groups]);
-}
-template <class CF>
-__device__ __forceinline__ int group_table(const GroupParams& p, int* first) {
-  return group_table_rows(p, first, CF::BM);
 }
 
 // The group of row tile number `row_tile` (below first[groups]).
@@ -122,25 +142,29 @@ __device__ __forceinline__ GroupTile group_chunk(const GroupParams& p, int slot,
 // Tile kernels of the forward.
 template <int AB, int BM, int BN, int S, int OCC, int BLK>
 using GroupedCfg = Cfg<AB, true, true, true, BM, BN, 128, 2, 2, S, 0, BLK, 3, OCC>;
+// The 128x128 kernel that finishes the last round of 256x256 tiles.
+template <int AB>
+using GroupedQuarter = GroupedCfg<AB, 128, 128, AB == T_E4M3 ? 4 : 2, 1, AB == T_E4M3 ? 32 : 16>;
 
 constexpr int kGroupedParts = 7;
 template <int PART>
 void launch_grouped_part(int variant, const GroupParams& p, int grid, hipStream_t s);
 
-// Few rows per group: chunks of up to 4 * mb rows (mb 1, 2, 4 or 8), 16 weight
+// Few rows per group: chunks of up to 4 * mb rows (mb 1 or 4), 16 weight
 // rows per workgroup; slots: chunks that the worst distribution has.
 void launch_grouped_rows(int ab, int mb, const GroupParams& p, int slots, hipStream_t s);
 
 // The backward's products, one launch for both (GRAD_* as for the linear layer):
 //   a: dA = dZ . B[e] over groups of rows; ga workgroups, a tile each at most
 //   b: dB[e] = dB_in[e] + dZ^T . A over each group's rows; gb workgroups
-// b's come first; the rest add up the chunks' column sums: dbias.
+// b's come first with b_first; the rest add up the chunks' column sums: dbias.
 template <int AB, bool ROWS, int KIND>
 using GroupedGradCfg = Cfg<AB, ROWS, false, true, grad_tile(KIND), grad_tile(KIND), 128, 2, 2, grad_stages(KIND),
                            KIND == GRAD_256 ? 2 : 0, 32, ROWS ? 4 : 5, grad_occ(KIND)>;
 struct GroupGradParams {
   GroupParams a, b;
   int32_t ga, gb, sums;   // workgroups
+  int32_t b_first;
   const float* partial;   // [chunk][N]
   int32_t chunk, slots;   // rows of a chunk, chunks that partial holds
   void* dbias;            // groups x N

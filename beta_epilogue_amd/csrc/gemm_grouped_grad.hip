@@ -2,9 +2,11 @@
 // one launch, compiled once per type and kernel (GEMM_GROUPED_GRAD_PART 0 .. 7).
 //
 // dA = dZ . B[e] has tiles of each expert's rows; dB[e] = dB_in[e] + dZ^T . A sums
-// over the expert's rows, one set of tiles per expert.  dB's tiles go first: an
-// expert with many rows makes long ones.  dbias is made by further workgroups
-// from the elementwise pass's column sums, in the order of the chunks.
+// over the expert's rows, one set of tiles per expert, those of the experts with
+// the most rows first and each expert's spread over the XCDs (16384 rows of 8
+// experts, 825 to 4282 each, N 4096, K 2048: dB 344 us with an expert per XCD).
+// dbias is made by further workgroups from the elementwise pass's column sums, in
+// the order of the chunks.
 #include "gemm_grouped.hpp"
 
 #ifndef GEMM_GROUPED_GRAD_PART
@@ -35,10 +37,16 @@ __global__ __launch_bounds__(256, grad_occ(KIND)) void grouped_grad_kernel(Group
   using CB = GroupedGradCfg<AB, false, KIND>;
   constexpr int A_BYTES = CA::LDS_BYTES + kGroupTableBytes;
   __shared__ __attribute__((aligned(1024))) char lds[A_BYTES > CB::LDS_BYTES ? A_BYTES : CB::LDS_BYTES];
-  const int bid = blockIdx.x;
-  if (bid < p.gb) gemm_epi_body<CB>(p.b, lds, bid, p.gb);
-  else if (bid < p.gb + p.ga) gemm_epi_body<CA>(p.a, lds, bid - p.gb, p.ga);
-  else group_sums(p, bid - p.gb - p.ga, (int*)lds);
+  const int bid = blockIdx.x, a0 = p.b_first ? p.gb : 0, b0 = p.b_first ? 0 : p.ga;
+  if (bid >= a0 && bid < a0 + p.ga) {
+    int* first = (int*)(lds + CA::LDS_BYTES);
+    const int total = group_table_rows(p.a, first, CA::BM) * p.a.tiles_n;
+    gemm_epi_body<CA>(p.a, lds, bid - a0, p.ga, GroupWork{first, 0, total, 0});
+  } else if (bid < p.gb + p.ga) {
+    gemm_epi_body<CB>(p.b, lds, bid - b0, p.gb);
+  } else {
+    group_sums(p, bid - p.gb - p.ga, (int*)lds);
+  }
 }
 
 }  // namespace

@@ -39,9 +39,7 @@ void rows(const GroupParams& p, int slots, hipStream_t s) {
 template <int AB>
 void rows_ab(int mb, const GroupParams& p, int slots, hipStream_t s) {
   if (mb == 1) rows<AB, 1, 8, 2>(p, slots, s);
-  else if (mb == 2) rows<AB, 2, 8, 2>(p, slots, s);
-  else if (mb == 4) rows<AB, 4, 4, 2>(p, slots, s);
-  else rows<AB, 8, 4, 1>(p, slots, s);
+  else rows<AB, 4, 4, 2>(p, slots, s);
 }
 
 }  // namespace

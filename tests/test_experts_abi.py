@@ -126,7 +126,7 @@ def test_linear_grad_validation(bad, code):
 
 def test_linear_variants():
     names = ge.expert_linear_variant_names()
-    assert len(set(names)) == len(names) and names[-1] == "experts_rows32"
+    assert len(set(names)) == len(names) and names[-1] == "experts_rows16"
     L = experts.lib()
     assert L.gemm_epi_expert_linear_variant_name(-1) is None
     assert L.gemm_epi_expert_linear_variant_name(len(names)) is None
