@@ -7,7 +7,8 @@ torch-tensor convenience layer (pointers and the current HIP stream).  The
 linear layer and the norm (``FusedLinear``, ``FusedLinearGrad``, ``RmsNorm``,
 ``RmsNormGrad``, ``FusedNormLinear``) are in ``layers``, a mixture of experts'
 operators (``ExpertSort``, ``ExpertLinear``, ``ExpertCombine`` and their
-gradients) in ``experts``.
+gradients) in ``experts``, the linear layer with adapters (``AdapterLinear``) in
+``adapters``.
 
 The library must have been built (``python -m beta_epilogue_amd.build`` or
 ``__graft_entry__.build()``); importing the binding without it raises.
@@ -253,4 +254,7 @@ def __getattr__(name):
     if name in _EXPERTS:
         from . import experts
         return getattr(experts, name)
+    if name == "AdapterLinear":
+        from . import adapters
+        return adapters.AdapterLinear
     raise AttributeError("module %r has no attribute %r" % (__name__, name))

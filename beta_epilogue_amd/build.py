@@ -6,7 +6,8 @@ variants of gemm_epi_variants.inc assigned to it; the parts compile in
 parallel.  The linear layer (gemm_linear*.hip, its tile kernels in
 GEMM_LINEAR_PARTS parts), the norm (gemm_norm*.hip) and the experts' operators
 (gemm_experts*.hip; gemm_grouped*.hip, in GEMM_GROUPED_PARTS and
-GEMM_GROUPED_GRAD_PARTS parts) are linked in.
+GEMM_GROUPED_GRAD_PARTS parts) and the adapters (gemm_adapter*.hip, tile kernels
+in GEMM_ADAPTER_PARTS parts) are linked in.
 libmfma_ceiling.so is a measurement tool for bench.py.
 """
 from __future__ import annotations
@@ -34,12 +35,15 @@ GROUPED_PART_SOURCE = os.path.join(CSRC, "gemm_grouped_part.hip")
 GEMM_GROUPED_PARTS = 7
 GROUPED_GRAD_SOURCE = os.path.join(CSRC, "gemm_grouped_grad.hip")
 GEMM_GROUPED_GRAD_PARTS = 8
+ADAPTER_PART_SOURCE = os.path.join(CSRC, "gemm_adapter_part.hip")
+GEMM_ADAPTER_PARTS = 4
 LINEAR_SOURCES = [os.path.join(CSRC, f) for f in ("gemm_linear.hip", "gemm_linear_rows.hip", "gemm_linear_grad.hip",
                                                   "gemm_norm.hip", "gemm_norm_kernels.hip", "gemm_experts.hip",
                                                   "gemm_experts_kernels.hip", "gemm_experts_linear.hip",
-                                                  "gemm_grouped_rows.hip", "gemm_grouped_act.hip")]
+                                                  "gemm_grouped_rows.hip", "gemm_grouped_act.hip", "gemm_adapters.hip",
+                                                  "gemm_adapter_rows.hip", "gemm_adapter_down.hip")]
 SOURCES = [MAIN_SOURCE, PART_SOURCE, SPLITK_SOURCE, PREP_SOURCE, LINEAR_PART_SOURCE, LINEAR_GRAD_MM_SOURCE,
-           GROUPED_PART_SOURCE, GROUPED_GRAD_SOURCE] + LINEAR_SOURCES
+           GROUPED_PART_SOURCE, GROUPED_GRAD_SOURCE, ADAPTER_PART_SOURCE] + LINEAR_SOURCES
 HEADERS = [os.path.join(CSRC, "gemm_epi_kernel.hpp"), os.path.join(CSRC, "gemm_epi_launch.hpp"),
            os.path.join(CSRC, "gemm_epi_splitk.hpp"), os.path.join(CSRC, "gemm_epi_prep.hpp"),
            os.path.join(CSRC, "gemm_epi_raster.hpp"), os.path.join(CSRC, "gemm_epi_variants.inc"),
@@ -48,9 +52,11 @@ HEADERS = [os.path.join(CSRC, "gemm_epi_kernel.hpp"), os.path.join(CSRC, "gemm_e
            os.path.join(CSRC, "gemm_linear.hpp"), os.path.join(CSRC, "gemm_linear_variants.inc"),
            os.path.join(CSRC, "gemm_linear_rows.hpp"), os.path.join(CSRC, "gemm_linear_cost.hpp"),
            os.path.join(CSRC, "gemm_norm.hpp"), os.path.join(CSRC, "gemm_experts.hpp"),
+           os.path.join(CSRC, "gemm_linear_host.hpp"), os.path.join(CSRC, "gemm_adapter.hpp"),
            os.path.join(CSRC, "gemm_grouped.hpp"), os.path.join(CSRC, "gemm_grouped_variants.inc"),
            os.path.join(ROOT, "include", "gemm_epi.h"), os.path.join(ROOT, "include", "gemm_epi_linear.h"),
-           os.path.join(ROOT, "include", "gemm_epi_norm.h"), os.path.join(ROOT, "include", "gemm_epi_experts.h")]
+           os.path.join(ROOT, "include", "gemm_epi_norm.h"), os.path.join(ROOT, "include", "gemm_epi_experts.h"),
+           os.path.join(ROOT, "include", "gemm_epi_adapters.h")]
 # measurement tool used by bench.py --mfma-ceiling (not part of the GEMM path)
 CEILING_LIB = os.path.join(HERE, "libmfma_ceiling.so")
 CEILING_SOURCE = os.path.join(CSRC, "mfma_ceiling.hip")
@@ -150,6 +156,9 @@ def build(verbose: bool = False, extra=(), only=None, cache_dir=None) -> str:
                   for k in range(GEMM_GROUPED_PARTS)]
         units += [obj("grouped_grad%d.o" % k, GROUPED_GRAD_SOURCE, grouped_deps, ["-DGEMM_GROUPED_GRAD_PART=%d" % k])
                   for k in range(GEMM_GROUPED_GRAD_PARTS)]
+        adapter_deps = linear_deps + [os.path.join(CSRC, "gemm_adapter.hpp")]
+        units += [obj("adapter%d.o" % k, ADAPTER_PART_SOURCE, adapter_deps, ["-DGEMM_ADAPTER_PART=%d" % k])
+                  for k in range(GEMM_ADAPTER_PARTS)]
         units += [obj(os.path.basename(f) + ".o", f, HEADERS) for f in LINEAR_SOURCES]
         jobs = [cmd for _, cmd in units if cmd]
         ceil_tmp = CEILING_LIB + ".tmp%d" % os.getpid()

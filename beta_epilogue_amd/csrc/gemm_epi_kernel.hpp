@@ -117,9 +117,10 @@ struct Params {
 };
 
 // Arguments of the linear layer's kernels (gemm_linear.hpp) and of the experts'
-// (gemm_grouped.hpp).
+// (gemm_grouped.hpp), and of the linear layer with adapters (gemm_adapter.hpp).
 struct LinParams;
 struct GroupParams;
+struct AdapterParams;
 
 // Row groups with a B each (GroupParams): of the output's rows, or of the
 // contraction (a sum over each group's rows, one output per group).
@@ -256,7 +257,8 @@ template <> struct Mma<T_U8, 32> : Mma<T_I8, 32> {};
 //               operands) and epilogue (N-major D); 2: the same without bias,
 //               scales, activation and Z (its backward's products); 3: 1 over
 //               groups of rows, with a factor in R's place; 4 and 5: 2 over
-//               groups of rows, and of the contraction
+//               groups of rows, and of the contraction; 6: 1 with the rows'
+//               adapters
 //   OCC         workgroups meant to share a compute unit (bounds the registers)
 template <int AB_, bool A_KMAJOR_, bool B_KMAJOR_, bool CD_NMAJOR_, int BM_ = 256, int BN_ = 256,
           int ROWB_ = 128, int WAVES_M_ = 2, int WAVES_N_ = 2, int STAGES_ = 2, int DQ_ = 0,
@@ -264,12 +266,15 @@ template <int AB_, bool A_KMAJOR_, bool B_KMAJOR_, bool CD_NMAJOR_, int BM_ = 25
 struct Cfg {
   static constexpr int OCC = OCC_;
   static constexpr bool LIN = LIN_ != 0;
-  static constexpr bool LIN_ACT = LIN_ == 1 || LIN_ == 3;
+  static constexpr bool LIN_ACT = LIN_ == 1 || LIN_ == 3 || LIN_ == 6;
+  static constexpr bool ADAPTERS = LIN_ == 6;
   static constexpr bool LIN_MUL = LIN_ == 3;  // R multiplies
   static constexpr int GROUP = LIN_ == 3 || LIN_ == 4 ? GROUP_ROWS : LIN_ == 5 ? GROUP_K : GROUP_NONE;
   static_assert(!LIN || (CD_NMAJOR_ && AB_ != T_U8), "what the linear kernels have");
   using params_t = typename std::conditional<
-      GROUP != GROUP_NONE, GroupParams, typename std::conditional<LIN_ != 0, LinParams, Params>::type>::type;
+      GROUP != GROUP_NONE, GroupParams,
+      typename std::conditional<
+          ADAPTERS, AdapterParams, typename std::conditional<LIN_ != 0, LinParams, Params>::type>::type>::type;
   static constexpr int BLK = BLK_;
   using MM = Mma<AB_, BLK_>;
   static constexpr int DQ = DQ_;
@@ -995,6 +1000,11 @@ struct GroupTile {
   int group, begin, end;  // the group and its rows
   int first, tiles;       // its first row tile among all groups', and their number
 };
+// Adds the rows' adapters to a wave's accumulators (gemm_adapter.hpp; ADAPTERS
+// kernels only).
+template <class CF, class ACC>
+__device__ void adapter_step(const AdapterParams& p, ACC (&acc)[CF::FM][CF::FN], int mw, int nw);
+
 // What a workgroup does of a GROUP_ROWS problem: items begin .. end - 1, of the
 // table of groups `first` (in LDS).  quarter: an item is a quarter of a tile of
 // twice the height and width, which the table counts.
@@ -1316,6 +1326,9 @@ __device__ __forceinline__ void gemm_epi_body(const typename CF::params_t& p, ch
     // otherwise (bf16 included) the mixed-type one (4 elements per lane).
     constexpr bool NM = CF::CD_NMAJOR;
     const int emw = m0 + wm * CF::WM, enw = n0 + wn * CF::WN;
+    if constexpr (CF::ADAPTERS) {
+      if (split <= 0) adapter_step<CF>(p, acc, emw, enw);  // (once per tile)
+    }
     if constexpr (CF::GROUP != GROUP_NONE) {
       typename CF::params_t q = p;
       if constexpr (CF::GROUP == GROUP_ROWS) {

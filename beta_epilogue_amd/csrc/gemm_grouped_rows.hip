@@ -27,7 +27,7 @@ __global__ __launch_bounds__(NW * 64) void grouped_rows_kernel(GroupParams p) {
   if (p.bias) q.bias = (const char*)p.bias + (g * p.N << epi_shift(p.bias_dtype));
   if (p.scale_a) q.scale_a = p.scale_a + r;
   if (p.scale_b) q.scale_b = p.scale_b + g * p.N;
-  linear_rows_body<AB, MB, NW, NS, true>(q, (int64_t)blockIdx.x * 16, lds);
+  linear_rows_body<AB, MB, NW, NS, true>(q, (int64_t)blockIdx.x * 16, lds, [](auto&) {});
 }
 
 template <int AB, int MB, int NW, int NS>

@@ -12,6 +12,7 @@
 #include "gemm_epi_linear.h"
 #include "gemm_linear.hpp"
 #include "gemm_linear_cost.hpp"
+#include "gemm_linear_host.hpp"
 
 using namespace gemm_epi;
 
@@ -112,15 +113,6 @@ int check_stride(const char* name, int64_t* ld, int64_t cols, int es, bool used)
 bool flag_ok(int f) { return f == 0 || f == 1; }
 
 }  // namespace
-
-struct gemm_epi_linear_handle {
-  gemm_epi_linear_desc d;  // strides filled in
-  int variant, device, cus, grid;
-  int nw;                  // few rows: waves per workgroup
-  int64_t tiles_m, tiles_n, tiles, tail, kslice, items;
-  int splits, group_m;
-  int64_t ws_bytes;
-};
 
 static int validate_linear(gemm_epi_linear_desc* d) {
   if (d->M < 1 || d->N < 1 || d->K < 1)
@@ -237,11 +229,9 @@ extern "C" int gemm_epi_linear_create(const gemm_epi_linear_desc* desc, gemm_epi
   return gemm_epi_linear_create_variant(desc, -1, out);
 }
 
-extern "C" int gemm_epi_linear_run(const gemm_epi_linear_handle* h, const void* A, const void* B, const void* bias,
-                                   const float* scale_a, const float* scale_b, const void* R, void* D, void* Z,
-                                   float alpha, void* workspace, int64_t workspace_bytes, void* stream) {
-  clear_error();
-  if (!h) return fail(GEMM_EPI_ERR_INVALID_ARG, "handle is NULL");
+int gemm_epi::linear_params(const gemm_epi_linear_handle* h, const void* A, const void* B, const void* bias,
+                            const float* scale_a, const float* scale_b, const void* R, void* D, void* Z, float alpha,
+                            void* workspace, int64_t workspace_bytes, LinParams* out) {
   const gemm_epi_linear_desc& d = h->d;
   if (!A || !B || !D) return fail(GEMM_EPI_ERR_INVALID_ARG, "A, B and D are required");
   if ((bias != nullptr) != (d.bias_dtype != GEMM_EPI_NONE) || (scale_a != nullptr) != (d.scale_a != 0) ||
@@ -257,7 +247,8 @@ extern "C" int gemm_epi_linear_run(const gemm_epi_linear_handle* h, const void* 
   if (!rc) rc = check_device(h->device);
   if (rc) return rc;
 
-  LinParams p = {};
+  LinParams& p = *out;
+  p = {};
   p.A = A;
   p.B = B;
   p.D = D;
@@ -278,13 +269,7 @@ extern "C" int gemm_epi_linear_run(const gemm_epi_linear_handle* h, const void* 
   p.ldz = d.ldz;
   p.bias_dtype = d.bias_dtype;
   p.act = d.act;
-  hipStream_t s = (hipStream_t)stream;
-  (void)hipGetLastError();  // clear a stale error so the checks below are ours
-  if (h->variant == kRowsVariant) {
-    launch_linear_rows(d.ab_dtype, h->nw, p, s);
-    return launched();
-  }
-  const LinearVariant& v = kLinear[h->variant];
+  if (h->variant == kRowsVariant) return GEMM_EPI_OK;
   p.tiles_total = (int32_t)h->items;
   p.L = 1;
   p.tiles_m = (int32_t)h->tiles_m;
@@ -296,13 +281,35 @@ extern "C" int gemm_epi_linear_run(const gemm_epi_linear_handle* h, const void* 
   p.splits = h->splits;
   p.kslice = h->kslice;
   p.ws = workspace;
-  kParts[v.part](h->variant, p, h->grid, s);
-  rc = launched();
-  if (rc || h->splits == 1) return rc;
+  return GEMM_EPI_OK;
+}
+
+int gemm_epi::linear_join(const gemm_epi_linear_handle* h, const LinParams& p, hipStream_t s) {
+  if (h->variant == kRowsVariant || h->splits == 1) return GEMM_EPI_OK;
+  const LinearVariant& v = kLinear[h->variant];
   const int64_t blocks = (h->tail * v.bm * v.bn / 4 + 255) / 256;
-  launch_linear_splitk(p, v.bm, v.bn, d.ab_dtype == GEMM_EPI_I8, (int)std::min<int64_t>(blocks, (int64_t)h->cus * 8),
+  launch_linear_splitk(p, v.bm, v.bn, h->d.ab_dtype == GEMM_EPI_I8, (int)std::min<int64_t>(blocks, (int64_t)h->cus * 8),
                        s);
   return launched();
+}
+
+extern "C" int gemm_epi_linear_run(const gemm_epi_linear_handle* h, const void* A, const void* B, const void* bias,
+                                   const float* scale_a, const float* scale_b, const void* R, void* D, void* Z,
+                                   float alpha, void* workspace, int64_t workspace_bytes, void* stream) {
+  clear_error();
+  if (!h) return fail(GEMM_EPI_ERR_INVALID_ARG, "handle is NULL");
+  LinParams p;
+  int rc = linear_params(h, A, B, bias, scale_a, scale_b, R, D, Z, alpha, workspace, workspace_bytes, &p);
+  if (rc) return rc;
+  hipStream_t s = (hipStream_t)stream;
+  (void)hipGetLastError();  // clear a stale error so the checks below are ours
+  if (h->variant == kRowsVariant) {
+    launch_linear_rows(h->d.ab_dtype, h->nw, p, s);
+    return launched();
+  }
+  kParts[kLinear[h->variant].part](h->variant, p, h->grid, s);
+  rc = launched();
+  return rc ? rc : linear_join(h, p, s);
 }
 
 extern "C" int gemm_epi_linear_destroy(gemm_epi_linear_handle* h) {

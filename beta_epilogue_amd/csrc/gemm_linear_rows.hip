@@ -26,7 +26,7 @@ namespace {
 template <int AB, int MB, int NW, int NS>
 __global__ __launch_bounds__(NW * 64) void linear_rows_kernel(LinParams p) {
   __shared__ __attribute__((aligned(1024))) char lds[RowsLds<AB, MB, NW, NS>::BYTES];
-  linear_rows_body<AB, MB, NW, NS, false>(p, (int64_t)blockIdx.x * 16, lds);
+  linear_rows_body<AB, MB, NW, NS, false>(p, (int64_t)blockIdx.x * 16, lds, [](auto&) {});
 }
 
 // ---------------------------------------------------------------------------

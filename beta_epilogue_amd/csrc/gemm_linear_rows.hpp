@@ -113,9 +113,9 @@ struct RowsLds {
 };
 
 // Columns n0 .. n0 + 15 of D for p.M <= 4 * MB tokens, with the LDS array `lds`
-// (1 KiB aligned).
-template <int AB, int MB, int NW, int NS, bool MUL>
-__device__ __forceinline__ void linear_rows_body(const LinParams& p, int64_t n0, char* lds) {
+// (1 KiB aligned).  more(acc): what a wave adds to its part of the sums.
+template <int AB, int MB, int NW, int NS, bool MUL, class F>
+__device__ __forceinline__ void linear_rows_body(const LinParams& p, int64_t n0, char* lds, F&& more) {
   using MM = RowsMma<AB>;
   constexpr int ES = AB == T_F16 || AB == T_BF16 ? 2 : 1;
   constexpr int NB = (MB + 3) / 4;               // token blocks of 16
@@ -171,6 +171,7 @@ __device__ __forceinline__ void linear_rows_body(const LinParams& p, int64_t n0,
   uint32_t k = (uint32_t)wave * kSeg;
 #pragma unroll
   for (int st = 0; st < NS; ++st) issue(st, k + (uint32_t)st * step);
+  more(acc);
   // (segments past K are issued too, without traffic, so the counts hold)
   int st = 0;
   for (; k < kbytes; k += step) {
