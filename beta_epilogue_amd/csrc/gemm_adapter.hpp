@@ -10,17 +10,19 @@
 // rounded once.
 #pragma once
 
-#include "gemm_linear.hpp"
+#include "gemm_grouped.hpp"
 
 namespace gemm_epi {
 
 struct AdapterParams : LinParams {
-  const void* U;       // M x rank
-  const void* up;      // adapters x N x rank
-  const int32_t* ids;  // M
+  const void* U;          // M x rank
+  const void* up;         // adapters x N x rank
+  const int32_t* ids;     // M
+  const int32_t* finite;  // adapters x kFiniteParts: 1 where that part of up[g] is finite
   int32_t rank, adapters;
 };
 
+constexpr int kFiniteParts = 4;
 constexpr int kMaxRank = 128;
 
 // The adapter of row m; -1: none, or no such row.
@@ -39,50 +41,135 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t adapter_up(const AdapterParams
   return __builtin_amdgcn_make_buffer_rsrc((void*)((const char*)p.up + g * bytes), (short)0, (int)bytes, 0x00020000);
 }
 
-// Adds U . up[g]^T to a wave's accumulators (16x16 blocks, rows mw .., columns
-// nw ..), one adapter of its rows after the other; fragments come straight from the
-// cache.  A block of 16 rows that are not all g's own is summed apart and only
-// g's rows are added: an infinity or a NaN in up[g] times a zero would reach the
-// others.
-template <class CF, class ACC>
-__device__ __forceinline__ void adapter_step(const AdapterParams& p, ACC (&acc)[CF::FM][CF::FN], int mw, int nw) {
+// The adapters of a tile's rows.  U . up[g]^T is a contraction like A . B^T, so the
+// adapters that the tile's rows have add K tiles to the tile's, staged and
+// multiplied by the same loop: A's rows are U's, zero for rows of other adapters,
+// B's are up[g]'s.  A K tile of 64 holds as many adapters as fit (rank 16: four).
+// Packed prompts have one or two adapters per tile; a batch of single tokens has up
+// to one per row (256 x 4096 x 4096, rank 16, 48 adapters: see the rows' own figures
+// in gemm_adapter_down.hip).
+//
+// A zero times an infinity or a NaN in up[g] would reach the other rows, so an
+// adapter whose up[g] is not finite (the first launch has looked) is left out
+// there and added by `step`, which keeps its own rows only.
+template <class CF>
+struct AdapterTiles {
   using MM = typename CF::MM;
-  static_assert(CF::BLK == 16 && MM::KSB == 64, "16-bit operands, 16x16 blocks");
-  const int lane = __lane_id(), r = lane & 15, q = lane >> 4;
-  int id[CF::FM];
-  uint32_t todo[CF::FM];  // rows (lanes 0 .. 15) whose adapter is still to come
-#pragma unroll
-  for (int i = 0; i < CF::FM; ++i) {
-    id[i] = row_adapter(p, mw + i * 16 + r);
-    todo[i] = (uint32_t)__ballot(id[i] >= 0) & 0xffffu;
+  static_assert(CF::BLK == 16 && MM::KSB == 64 && CF::ROWB == 128 && CF::BM <= CF::THREADS, "16-bit operands, 16x16 blocks");
+  // behind the ring: the rows' adapters, a list of them, a bit for each, counts
+  static constexpr int BITS = kMaxExperts / 32;
+  static constexpr int LDS_BYTES = (2 * CF::BM + BITS + 4) * 4;
+  int tiles;        // K tiles
+  bool apart;       // some row's adapter is not finite
+  int m0, n0;       // the tile's first row and column
+  int slot;         // of this lane's 16 bytes of a K tile: which of its adapters,
+  uint32_t k;       // and which byte of the rank (past it: at least 2 * rank)
+  int shift;        // adapters in a K tile: 1 << shift; -1: two K tiles for one
+  uint32_t bytes;   // of a row of U and of up
+  int cur;          // the adapter being staged
+  uint32_t at;      // its byte in up
+
+  static __device__ __forceinline__ int* ids(char* lds) { return (int*)(lds + CF::LDS_BYTES); }
+
+  // on: this item adds them at all (one K slice of a tile does); cb: the byte of K
+  // that this lane stages
+  __device__ __forceinline__ void setup(const AdapterParams& p, char* lds, int row0, int column0, bool on, uint32_t cb,
+                                        int lane) {
+    m0 = row0;
+    n0 = column0;
+    tiles = 0;
+    apart = false;
+    if (!on) return;
+    int *id = ids(lds), *list = id + CF::BM, *bits = list + CF::BM, *count = bits + BITS;
+    const int t = threadIdx.x;
+    if (t < BITS + 2) bits[t] = 0;
+    __syncthreads();
+    if (t < CF::BM) {
+      int g = row_adapter(p, (int64_t)m0 + t);
+      if (g >= 0) {
+        const v4i f = *(const v4i*)(p.finite + (int64_t)g * kFiniteParts);
+        if (f.x & f.y & f.z & f.w) atomicOr(&bits[g >> 5], 1 << (g & 31));
+        else g = -1, atomicOr(&count[1], 1);
+      }
+      id[t] = g;
+    }
+    __syncthreads();
+    if (t < 64) {
+      uint32_t word = t < BITS ? (uint32_t)bits[t] : 0u;
+      const int n = __popc(word), sum = wave_scan(n, lane);
+      for (int i = sum - n; word; ++i, word &= word - 1) list[i] = t * 32 + __ffs(word) - 1;
+      if (t == 63) count[0] = sum;
+    }
+    __syncthreads();
+    const int n = __builtin_amdgcn_readfirstlane(count[0]);
+    apart = __builtin_amdgcn_readfirstlane(count[1]) != 0;
+    bytes = (uint32_t)p.rank * 2;
+    shift = p.rank <= 8 ? 3 : p.rank <= 16 ? 2 : p.rank <= 32 ? 1 : p.rank <= 64 ? 0 : -1;
+    tiles = shift < 0 ? 2 * n : (n + (1 << shift) - 1) >> shift;
+    slot = shift < 0 ? 0 : (int)(cb >> (7 - shift));
+    k = shift < 0 ? cb : cb & (127u >> shift);
+    cur = -1;
+    at = 0;
   }
-  const int rows = (int)min(max(p.M - mw, (int64_t)0), (int64_t)CF::WM);
-  const __amdgpu_buffer_rsrc_t ru = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)((const char*)p.U + (int64_t)mw * p.rank * 2), (short)0, rows * p.rank * 2, 0x00020000);
-  const uint32_t row = (uint32_t)p.rank * 2, ub = (uint32_t)r * row + 16 * q, nb = (uint32_t)(nw + r) * row + 16 * q;
-  for (;;) {
-    int g = -1;
+
+  // The row that this lane stages by instruction Q.
+  template <int Q>
+  static __device__ __forceinline__ uint32_t stage_row() {
+    const int lane = __lane_id(), wave = threadIdx.x >> 6;
+    return (uint32_t)((Q * CF::NW + wave) * CF::ROWS_PER_DMA + lane / CF::CH);
+  }
+  // Instruction Q of K tile t (a K tile's instructions are issued in order, the rows' first).
+  template <int Q>
+  __device__ __forceinline__ void issue_rows(const AdapterParams& p, char* lds, uint32_t sbase, int t) {
+    if constexpr (Q == 0) {
+      const int a = shift < 0 ? t >> 1 : (t << shift) + slot;
+      const int n = ids(lds)[2 * CF::BM + BITS];
+      cur = a < n ? ids(lds)[CF::BM + a] : -1;
+      const uint32_t kk = k + (shift < 0 && (t & 1) ? 128u : 0u);
+      if (kk >= bytes) cur = -1;
+      at = (uint32_t)cur * (uint32_t)p.N * bytes + kk;
+    }
+    const v4i ru = make_rsrc((const char*)p.U + (int64_t)m0 * bytes, (uint32_t)min((int64_t)CF::BM, p.M - m0) * bytes);
+    const uint32_t row = stage_row<Q>(), kk = k + (shift < 0 && (t & 1) ? 128u : 0u);
+    dma16s<(uint32_t)Q * CF::NW * 1024u>(ru, sbase, cur >= 0 && ids(lds)[row] == cur ? row * bytes + kk : 0x80000000u, 0);
+  }
+  template <int Q>
+  __device__ __forceinline__ void issue_columns(const AdapterParams& p, uint32_t sbase) {
+    const int64_t first = (int64_t)n0 * bytes;
+    const v4i rp = make_rsrc((const char*)p.up + first, (uint32_t)((int64_t)p.adapters * p.N * bytes - first));
+    // (columns past the matrix get something else's weights, and are never stored)
+    dma16s<(uint32_t)Q * CF::NW * 1024u>(rp, sbase, cur >= 0 ? at + stage_row<Q>() * bytes : 0x80000000u, 0);
+  }
+
+  // Adds what was left out to a wave's accumulators (rows mw .., columns nw ..):
+  // block row by block row, fragments straight from the cache.
+  template <class ACC>
+  __device__ __forceinline__ void step(const AdapterParams& p, ACC (&acc)[CF::FM][CF::FN], int mw, int nw) const {
+    const int lane = __lane_id(), r = lane & 15, q = lane >> 4;
+    const int rows = (int)min(max(p.M - mw, (int64_t)0), (int64_t)CF::WM);
+    const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)((const char*)p.U + (int64_t)mw * p.rank * 2), (short)0, rows * p.rank * 2, 0x00020000);
+    const uint32_t row = (uint32_t)p.rank * 2, ub = (uint32_t)r * row + 16 * q, nb = (uint32_t)(nw + r) * row + 16 * q;
     static_for<0, CF::FM>([&](auto i_c) {
       constexpr int i = decltype(i_c)::value;
-      if (g < 0 && todo[i]) g = __builtin_amdgcn_readlane(id[i], __ffs(todo[i]) - 1);
-    });
-    if (g < 0) break;
-    const __amdgpu_buffer_rsrc_t rp = adapter_up(p, g);
-    for (int k = 0; k < p.rank; k += 32) {
-      const bool in = k + 8 * q < p.rank;
-      v4i fb[CF::FN];
-      // (columns past the matrix lie outside the resource)
+      int id = row_adapter(p, mw + i * 16 + r);
+      if (id >= 0) {
+        const v4i f = *(const v4i*)(p.finite + (int64_t)id * kFiniteParts);
+        if (f.x & f.y & f.z & f.w) id = -1;
+      }
+      uint32_t todo = (uint32_t)__ballot(id >= 0) & 0xffffu;  // rows whose adapter is still to come
+      while (todo) {
+        const int g = __builtin_amdgcn_readlane(id, __ffs(todo) - 1);
+        const uint32_t mine = (uint32_t)__ballot(id == g) & 0xffffu;
+        todo &= ~mine;
+        const __amdgpu_buffer_rsrc_t rp = adapter_up(p, g);
+        for (int k = 0; k < p.rank; k += 32) {
+          const bool in = k + 8 * q < p.rank;
+          const v4i fa = adapter_load(rw, in && id == g ? ub + i * 16 * row + 2 * k : 0x80000000u);
+          v4i fb[CF::FN];
+          // (columns past the matrix lie outside the resource)
 #pragma unroll
-      for (int j = 0; j < CF::FN; ++j) fb[j] = adapter_load(rp, in ? nb + j * 16 * row + 2 * k : 0x80000000u);
-      static_for<0, CF::FM>([&](auto i_c) {
-        constexpr int i = decltype(i_c)::value;
-        const uint32_t mine = (uint32_t)__ballot(id[i] == g) & 0xffffu;
-        if (mine == 0) return;
-        const v4i fa = adapter_load(ru, in && id[i] == g ? ub + i * 16 * row + 2 * k : 0x80000000u);
-        if (mine == 0xffffu) {
-#pragma unroll
-          for (int j = 0; j < CF::FN; ++j) acc[i][j] = MM::mma(fa, fb[j], acc[i][j]);
-        } else {
+          for (int j = 0; j < CF::FN; ++j) fb[j] = adapter_load(rp, in ? nb + j * 16 * row + 2 * k : 0x80000000u);
 #pragma unroll
           for (int j = 0; j < CF::FN; ++j) {
             const typename MM::acc_t t = MM::mma(fa, fb[j], typename MM::acc_t{});
@@ -90,29 +177,33 @@ __device__ __forceinline__ void adapter_step(const AdapterParams& p, ACC (&acc)[
             for (int v = 0; v < MM::ACCN; ++v) acc[i][j][v] += mine >> MM::acc_row(lane, v) & 1 ? t[v] : 0.0f;
           }
         }
-      });
-    }
-    static_for<0, CF::FM>([&](auto i_c) {
-      constexpr int i = decltype(i_c)::value;
-      todo[i] &= ~((uint32_t)__ballot(id[i] == g) & 0xffffu);
+      }
     });
   }
-}
+};
 
 // U[m] = scale[g] A[m] . down[g]^T of type ab (T_F16 or T_BF16); rows without an
-// adapter are left as they are.
+// adapter are left as they are.  finite (NULL: not wanted): whether each part of
+// up[g] is, for the adapters that some row has.
 struct AdapterDownParams {
   const void* A;
   const void* down;    // adapters x rank x K
+  const void* up;      // adapters x N x rank
   const float* scale;  // adapters
   const int32_t* ids;
   void* U;
-  int64_t M, K, lda;
+  int32_t* finite;
+  int32_t* order;      // workspace, with adapter_sorted: the rows by adapter,
+  int32_t* offsets;    // where each adapter's begin,
+  int32_t* counts;     // and the sort's
+  int64_t M, N, K, lda;
   int32_t rank, adapters;
 };
+// Whether the rows are sorted by adapter first.
+inline bool adapter_sorted(int64_t M, int rank) { return M * rank > 8192; }
 void launch_adapter_down(int ab, const AdapterDownParams& p, hipStream_t s);
 
-// The linear layer's kernels with the step above.
+// The linear layer's kernels with the rows' adapters.
 template <int AB, int BM, int BN, int S, int OCC>
 using AdapterCfg = Cfg<AB, true, true, true, BM, BN, 128, 2, 2, S, 0, 16, 6, OCC>;
 // Tile kernel bm x bn of the linear layer's plan (one of part PART).

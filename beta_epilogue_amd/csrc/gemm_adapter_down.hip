@@ -5,11 +5,15 @@
 // as many adapters cost the same, and every weight is read once per row that has
 // it, from the cache but for the first time.
 //
-// More rows: 16 or 32 rows per workgroup, K split over its 8 waves, whose partial
-// sums are joined through LDS in wave order; fragments come straight from memory,
-// 128 bytes of a row in one load of 4 lanes.  Bound by the one read of A.  Rows of
-// several adapters take one pass over K for each, and keep only their own.
+// More rows are sorted by adapter (gemm_experts_kernels.hip), so that a workgroup
+// has 16 rows of one, streamed past the adapter's weights by the few-row kernel
+// (gemm_linear_rows.hip): 4001 x 4096, rank 64, 14 us with the fragments through LDS
+// and 24 with fragments straight from memory.
+//
+// Further workgroups of the same launch look whether the up[g] that the rows meet
+// are finite (AdapterTiles).
 #include "gemm_adapter.hpp"
+#include "gemm_linear_rows.hpp"
 
 namespace gemm_epi {
 
@@ -25,13 +29,57 @@ __device__ __forceinline__ float dot8(v4u a, v4u b, float s) {
   return s;
 }
 
-// Workgroup (x, y): products 4 x .. 4 x + 3 of row y, one wave each.
+// Whether any thread of the workgroup says so; red: a word per wave.
+__device__ __forceinline__ bool any_thread(bool v, int* red) {
+  const bool any = __any(v);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = any;
+  __syncthreads();
+  bool all = false;
+  for (int w = 0; w < (int)blockDim.x / 64; ++w) all |= red[w] != 0;
+  return all;
+}
+
+// Whether part `block % kFiniteParts` of up[block / kFiniteParts] is finite; an
+// adapter that no row has is not read (and nobody asks).
 template <int AB>
-__global__ __launch_bounds__(256) void adapter_dots_kernel(AdapterDownParams p) {
-  const int64_t m = blockIdx.y;
+__device__ __forceinline__ void finite_block(const AdapterDownParams& p, int block, int* red) {
+  const int g = block / kFiniteParts, part = block % kFiniteParts, threads = blockDim.x;
+  bool met = false;
+  if (p.offsets) {
+    met = p.offsets[g + 1] > p.offsets[g];
+  } else {
+    for (int64_t m = threadIdx.x; m < p.M; m += threads) met |= p.ids[m] == g;
+    met = any_thread(met, red);
+  }
+  if (!met) return;
+  constexpr uint32_t kExp = AB == T_F16 ? 0x7c00u : 0x7f80u;
+  const int64_t n = p.N * p.rank / 8;  // 16-byte pieces
+  const v4u* w = (const v4u*)((const char*)p.up + g * n * 16);
+  bool bad = false;
+#pragma unroll 8
+  for (int64_t i = part * (int64_t)threads + threadIdx.x; i < n; i += (int64_t)kFiniteParts * threads) {
+    const v4u v = w[i];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      bad |= (v[k] & kExp) == kExp || (v[k] & (kExp << 16)) == kExp << 16;
+  }
+  bad = any_thread(bad, red);
+  if (threadIdx.x == 0) p.finite[g * kFiniteParts + part] = !bad;
+}
+
+// Products 4 x .. 4 x + 3 of a row, one wave each.
+template <int AB>
+__global__ __launch_bounds__(256) void adapter_dots_kernel(AdapterDownParams p, int blocks) {
+  __shared__ int red[4];
+  if ((int)blockIdx.x >= blocks) {
+    finite_block<AB>(p, blockIdx.x - blocks, red);
+    return;
+  }
+  const int per = p.rank / 4, m = blockIdx.x / per;
   const int g = p.ids[m];
   if (g < 0 || g >= p.adapters) return;
-  const int lane = threadIdx.x & 63, j = blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, j = (blockIdx.x - m * per) * 4 + (threadIdx.x >> 6);
   const uint16_t* a = (const uint16_t*)p.A + m * p.lda;
   const uint16_t* w = (const uint16_t*)p.down + ((int64_t)g * p.rank + j) * p.K;
   float s = 0.0f;
@@ -39,108 +87,78 @@ __global__ __launch_bounds__(256) void adapter_dots_kernel(AdapterDownParams p) 
   for (int64_t k = lane * 8; k < p.K; k += 512) s = dot8<AB>(*(const v4u*)(a + k), *(const v4u*)(w + k), s);
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) s += __shfl_xor(s, d);
-  if (lane == 0) store_as(p.U, m * p.rank + j, AB, s * p.scale[g]);
+  if (lane == 0) store_as(p.U, (int64_t)m * p.rank + j, AB, s * p.scale[g]);
 }
 
-// RB blocks of 16 rows, up to CB * 16 products of each.
-template <int AB, int RB, int CB>
-__global__ __launch_bounds__(512) void adapter_down_kernel(AdapterDownParams p) {
-  using MM = Mma<AB, 16>;
-  constexpr int NW = 8, ROWS = RB * 16;
-  __shared__ v4f part[NW][RB * CB][64];
-  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t m0 = (int64_t)blockIdx.x * ROWS;
-  const int rows = (int)min(p.M - m0, (int64_t)ROWS);
-  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)((const char*)p.A + m0 * p.lda * 2), (short)0, (int)(((rows - 1) * p.lda + p.K) * 2), 0x00020000);
-  int id[RB];
-  uint32_t oa[RB];
-#pragma unroll
-  for (int i = 0; i < RB; ++i) {
-    const int m = i * 16 + r;
-    const int g = m < rows ? p.ids[m0 + m] : -1;
-    id[i] = g >= 0 && g < p.adapters ? g : -1;
-    oa[i] = m < rows ? (uint32_t)((m * p.lda + q * 16) * 2) : 0x80000000u;
+// 16 rows of one adapter, 64 of its products (4 * MB at most): the few-row kernel with
+// the rows in the weight's place and the adapter's in the tokens'.
+template <int AB, int MB, int NW, int NS>
+__global__ __launch_bounds__(NW * 64) void adapter_down_kernel(AdapterDownParams p, int blocks, int per) {
+  __shared__ __attribute__((aligned(1024))) char lds[RowsLds<AB, MB, NW, NS>::BYTES];
+  if ((int)blockIdx.x >= blocks * per) {
+    finite_block<AB>(p, blockIdx.x - blocks * per, (int*)lds);
+    return;
   }
-  uint32_t todo[RB];
+  GroupParams gp;
+  gp.offsets = p.offsets;
+  gp.groups = p.adapters;
+  gp.rows = (int)p.M;
+  const int chunk = blockIdx.x / per, j0 = (blockIdx.x - chunk * per) * 64;
+  const GroupTile t = group_chunk(gp, chunk, 16);
+  if (t.group < 0) return;
+  const int lane = threadIdx.x & 63;
+  const int mine = t.begin + (lane & 15) < t.end ? p.order[t.begin + (lane & 15)] : -1;  // lane i: row i
+  LinParams q;
+  q.A = (const char*)p.down + ((int64_t)t.group * p.rank + j0) * p.K * 2;
+  q.M = min(p.rank - j0, 64);
+  q.K = q.lda = p.K;
+  const float f = p.scale[t.group];
+  rows_products<AB, MB, NW, NS>(
+      q, make_rsrc(p.A, (uint32_t)(((p.M - 1) * p.lda + p.K) * 2)),
+      [&](int i) {
+        const int m = __shfl(mine, i);
+        return m >= 0 ? (uint32_t)(m * p.lda * 2) : 0x80000000u;
+      },
+      lds, [](int, int) {}, [](auto&) {},
+      [&](int j, int i, v4f sum) {
 #pragma unroll
-  for (int i = 0; i < RB; ++i) todo[i] = (uint32_t)__ballot(id[i] >= 0) & 0xffffu;
-  for (;;) {
-    int g = -1;
-    static_for<0, RB>([&](auto i_c) {
-      constexpr int i = decltype(i_c)::value;
-      if (g < 0 && todo[i]) g = __builtin_amdgcn_readlane(id[i], __ffs(todo[i]) - 1);
-    });
-    if (g < 0) break;
-    const int64_t bytes = p.rank * p.K * 2;
-    const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)((const char*)p.down + g * bytes), (short)0, (int)bytes, 0x00020000);
-    v4f acc[RB][CB] = {};
-#pragma unroll 2
-    for (int64_t k = wave * 64; k < p.K; k += NW * 64) {
-      // lane (q, r): k + 16 q .. + 15 of its rows; each half is one product
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const bool in = k + q * 16 + h * 8 < p.K;
-        const uint32_t at = (uint32_t)(k + h * 8) * 2;
-        v4i fa[RB], fb[CB];
-#pragma unroll
-        for (int i = 0; i < RB; ++i)
-          fa[i] = adapter_load(ra, in && oa[i] != 0x80000000u ? oa[i] + at : 0x80000000u);
-#pragma unroll
-        for (int c = 0; c < CB; ++c)
-          fb[c] = adapter_load(rb, in && c * 16 + r < p.rank ? (uint32_t)(((c * 16 + r) * p.K + q * 16) * 2) + at
-                                                             : 0x80000000u);
-        // (products are the matrix core's rows: a lane ends with four of a token)
-#pragma unroll
-        for (int i = 0; i < RB; ++i)
-#pragma unroll
-          for (int c = 0; c < CB; ++c) acc[i][c] = MM::mma(fb[c], fa[i], acc[i][c]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < RB; ++i)
-#pragma unroll
-      for (int c = 0; c < CB; ++c) part[wave][i * CB + c][lane] = acc[i][c];
-    __syncthreads();
-    for (int b = wave; b < RB * CB; b += NW) {
-      v4f s = part[0][b][lane];
-#pragma unroll
-      for (int w = 1; w < NW; ++w) s += part[w][b][lane];
-      const int m = (b / CB) * 16 + r, j = (b % CB) * 16 + 4 * q;
-      int mine = -1;
-      static_for<0, RB>([&](auto i_c) {
-        if (b / CB == decltype(i_c)::value) mine = id[decltype(i_c)::value];
+        for (int e = 0; e < 4; ++e) {
+          if (t.begin + i + e >= t.end) continue;
+          const int64_t m = p.order[t.begin + i + e];
+          store_as(p.U, m * p.rank + j0 + j, AB, sum[e] * f);
+        }
       });
-      if (mine != g || j >= p.rank) continue;
-      const float f = p.scale[g];
-      uint16_t* out = (uint16_t*)p.U + (m0 + m) * p.rank + j;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) store_as(out, e, AB, s[e] * f);
-    }
-    __syncthreads();
-    static_for<0, RB>([&](auto i_c) {
-      constexpr int i = decltype(i_c)::value;
-      todo[i] &= ~((uint32_t)__ballot(id[i] == g) & 0xffffu);
-    });
-  }
 }
 
-template <int AB, int RB, int CB>
+template <int AB, int MB, int NW, int NS>
 void down(const AdapterDownParams& p, hipStream_t s) {
-  hipLaunchKernelGGL((adapter_down_kernel<AB, RB, CB>), dim3((unsigned)((p.M + RB * 16 - 1) / (RB * 16))), dim3(512), 0, s,
-                     p);
+  const int64_t n = p.M < p.adapters ? p.M : p.adapters;
+  const int blocks = (int)(n + (p.M - n) / 16), per = (p.rank + 63) / 64;  // chunks of the worst distribution
+  hipLaunchKernelGGL((adapter_down_kernel<AB, MB, NW, NS>), dim3((unsigned)(blocks * per + p.adapters * kFiniteParts)),
+                     dim3(NW * 64), 0, s, p, blocks, per);
 }
 
 template <int AB>
 void launch(const AdapterDownParams& p, hipStream_t s) {
-  if (p.M * p.rank <= 8192)
-    hipLaunchKernelGGL(adapter_dots_kernel<AB>, dim3((unsigned)(p.rank / 4), (unsigned)p.M), dim3(256), 0, s, p);
-  else if (p.rank <= 16) down<AB, 2, 1>(p, s);
-  else if (p.rank <= 32) down<AB, 2, 2>(p, s);
-  else if (p.rank <= 64) down<AB, 2, 4>(p, s);
-  else down<AB, 1, 8>(p, s);
+  if (!adapter_sorted(p.M, p.rank)) {
+    const int blocks = (int)(p.M * p.rank / 4);
+    hipLaunchKernelGGL(adapter_dots_kernel<AB>, dim3((unsigned)(blocks + (p.finite ? p.adapters * kFiniteParts : 0))), dim3(256),
+                       0, s, p, blocks);
+    return;
+  }
+  SortParams q = {};
+  q.ids = p.ids;
+  q.offsets = p.offsets;
+  q.order = p.order;
+  q.counts = p.counts;
+  q.tokens = p.M;
+  q.top_k = 1;
+  q.experts = p.adapters;
+  q.chunks = (int32_t)sort_chunks(p.M);
+  launch_expert_sort(q, s);
+  if (p.rank <= 16) down<AB, 4, 4, 2>(p, s);
+  else if (p.rank <= 32) down<AB, 8, 4, 1>(p, s);
+  else down<AB, 16, 8, 1>(p, s);
 }
 
 }  // namespace

@@ -16,7 +16,7 @@ constexpr int P = GEMM_ADAPTER_PART;
 
 template <class CF>
 __global__ __launch_bounds__(CF::THREADS, CF::OCC) void adapter_kernel(AdapterParams p) {
-  __shared__ __attribute__((aligned(1024))) char lds[CF::LDS_BYTES];
+  __shared__ __attribute__((aligned(1024))) char lds[CF::LDS_BYTES + AdapterTiles<CF>::LDS_BYTES];
   gemm_epi_body<CF>(p, lds, blockIdx.x, gridDim.x);
 }
 

@@ -1000,10 +1000,10 @@ struct GroupTile {
   int group, begin, end;  // the group and its rows
   int first, tiles;       // its first row tile among all groups', and their number
 };
-// Adds the rows' adapters to a wave's accumulators (gemm_adapter.hpp; ADAPTERS
-// kernels only).
-template <class CF, class ACC>
-__device__ void adapter_step(const AdapterParams& p, ACC (&acc)[CF::FM][CF::FN], int mw, int nw);
+// The rows' adapters (gemm_adapter.hpp; ADAPTERS kernels only): K tiles of their own
+// behind those of A and B.
+template <class CF>
+struct AdapterTiles;
 
 // What a workgroup does of a GROUP_ROWS problem: items begin .. end - 1, of the
 // table of groups `first` (in LDS).  quarter: an item is a quarter of a tile of
@@ -1094,6 +1094,7 @@ __device__ __forceinline__ void gemm_epi_body(const typename CF::params_t& p, ch
     const int64_t kbytes = (split < 0 ? K : min(K - kbeg, p.kslice)) * ES;  // this item's K, in bytes
     int KT = (int)((kbytes + CF::ROWB - 1) / CF::ROWB);
     if constexpr (CF::GROUP == GROUP_K) KT = max(KT, 1);  // (a group without rows: one K tile of zeros)
+    [[maybe_unused]] const int KTA = KT;  // K tiles of A and B
     int m0 = tc.tm * BM, n0 = tc.tn * BN;
     if constexpr (CF::GROUP == GROUP_ROWS) {
       if (work.quarter) m0 = 2 * m0 + (t & 1) * BM, n0 = 2 * n0 + ((t >> 1) & 1) * BN;
@@ -1117,6 +1118,12 @@ __device__ __forceinline__ void gemm_epi_body(const typename CF::params_t& p, ch
     } else {
       opa.setup((const char*)p.A + (int64_t)l * p.M * p.K * ES, p.M, p.K, kbeg, m0, wave, lane);
       opb.setup((const char*)p.B + (int64_t)l * p.N * p.K * ES, p.N, p.K, kbeg, n0, wave, lane);
+    }
+
+    typename std::conditional<CF::ADAPTERS, AdapterTiles<CF>, IntC<0>>::type adapters;
+    if constexpr (CF::ADAPTERS) {
+      adapters.setup(p, lds, m0, n0, split <= 0, opa.cb, lane);  // (once per tile)
+      KT += adapters.tiles;
     }
 
     acc_t acc[CF::FM][CF::FN];
@@ -1163,6 +1170,15 @@ __device__ __forceinline__ void gemm_epi_body(const typename CF::params_t& p, ch
       constexpr int D = decltype(d_c)::value;
       constexpr bool GUARD = decltype(guard_c)::value;
       if (GUARD && k_tile >= KT) return;
+      if constexpr (CF::ADAPTERS && GUARD) {
+        if (k_tile >= KTA) {
+          if constexpr (D < NQ_A)
+            adapters.template issue_rows<D>(p, lds, lds_wave + (uint32_t)stg * (uint32_t)A_STAGE, k_tile - KTA);
+          else
+            adapters.template issue_columns<D - NQ_A>(p, lds_wave + (uint32_t)(B_REGION + stg * B_STAGE));
+          return;
+        }
+      }
       const int kv = GUARD ? (int)min(kbytes - (int64_t)k_tile * CF::ROWB, (int64_t)CF::ROWB) : CF::ROWB;
       if constexpr (D < NQ_A)
         opa.template issue_one<D, GUARD>(lds_wave + (uint32_t)stg * (uint32_t)A_STAGE, k_tile, kv);
@@ -1327,7 +1343,7 @@ __device__ __forceinline__ void gemm_epi_body(const typename CF::params_t& p, ch
     constexpr bool NM = CF::CD_NMAJOR;
     const int emw = m0 + wm * CF::WM, enw = n0 + wn * CF::WN;
     if constexpr (CF::ADAPTERS) {
-      if (split <= 0) adapter_step<CF>(p, acc, emw, enw);  // (once per tile)
+      if (adapters.apart) adapters.step(p, acc, emw, enw);
     }
     if constexpr (CF::GROUP != GROUP_NONE) {
       typename CF::params_t q = p;

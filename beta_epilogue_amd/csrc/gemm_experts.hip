@@ -73,7 +73,7 @@ int finish(const D& d, H** out) {
 struct gemm_epi_expert_sort_handle {
   gemm_epi_expert_sort_desc d;  // strides filled in
   int device, cus;
-  int64_t chunks() const { return (d.tokens * d.top_k + kSortChunk - 1) / kSortChunk; }
+  int64_t chunks() const { return sort_chunks(d.tokens * d.top_k); }
   int64_t ws() const { return chunks() > 1 ? chunks() * d.experts * 4 : 0; }
 };
 

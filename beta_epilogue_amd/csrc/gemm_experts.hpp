@@ -10,17 +10,22 @@ namespace gemm_epi {
 
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 64;
-// Choices (of a token and an expert) that one workgroup ranks.
+// Choices (of a token and an expert) that one workgroup ranks: all of up to twice a
+// chunk, or a chunk each.
 constexpr int kSortChunk = 4096;
+inline int64_t sort_chunks(int64_t choices) {
+  return choices <= 2 * kSortChunk ? 1 : (choices + kSortChunk - 1) / kSortChunk;
+}
 
 struct SortParams {
   const void* ids;       // choices x int32 or int64
   const void* X;         // rows to move, or NULL
   const float* scale;    // of the rows of X, or NULL
   int32_t* offsets;      // experts + 1
-  int32_t* rows;         // choices
+  int32_t* rows;         // choices (NULL: not wanted)
   void* Y;
   float* scale_out;
+  int32_t* order;        // the choice of each row (NULL: not wanted)
   int32_t* counts;       // workspace: chunks x experts (one chunk: NULL)
   int64_t tokens;
   int64_t row_bytes, ldx, ldy;  // bytes; a multiple of 16

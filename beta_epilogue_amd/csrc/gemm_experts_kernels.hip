@@ -2,9 +2,9 @@
 // back with the router's weights, and the gradient of that.
 //
 // The sort is a stable counting sort of the T * top_k choices: row = offsets[e]
-// + the number of earlier choices of e.  Counts are integers, so LDS atomics on
-// them leave nothing to the order in which they run; ranks come from ballots,
-// never from atomics.  Moving the rows is bound by memory: a token's row is read
+// + the number of earlier choices of e.  Counts and ranks come from ballots (LDS
+// atomics of choices that are alike queue up: 4001 choices of 5 runs took 8.7 us
+// with one per choice).  Moving the rows is bound by memory: a token's row is read
 // once and stored top_k times.
 #include "gemm_experts.hpp"
 #include "gemm_linear.hpp"
@@ -14,7 +14,6 @@ namespace gemm_epi {
 namespace {
 
 constexpr int kSortThreads = 1024, kSortWaves = 16;
-constexpr int kPerWave = kSortChunk / kSortWaves;  // consecutive choices of a wave
 
 // Choice i's expert; -1: none.
 __device__ __forceinline__ int choice(const SortParams& p, int64_t i, int64_t n) {
@@ -25,28 +24,51 @@ __device__ __forceinline__ int choice(const SortParams& p, int64_t i, int64_t n)
 
 struct SortLds {
   int cnt[kSortWaves][kMaxExperts];  // a wave's choices of an expert, then its next row
-  int base[kMaxExperts];             // rows before this chunk's: of earlier experts and chunks
   int wave_sum[kSortWaves];
 };
 
-// Counts of the chunk's choices, per wave.
-__device__ __forceinline__ void count_chunk(const SortParams& p, int chunk, SortLds& s, int (&e)[kPerWave / 64]) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t n = p.tokens * p.top_k, i0 = (int64_t)chunk * kSortChunk + wave * kPerWave;
-#pragma unroll
-  for (int k = 0; k < kPerWave / 64; ++k) e[k] = choice(p, i0 + k * 64 + lane, n);
-  for (int i = threadIdx.x; i < kSortWaves * p.experts; i += kSortThreads) s.cnt[i / p.experts][i % p.experts] = 0;
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < kPerWave / 64; ++k)
-    if (e[k] >= 0) atomicAdd(&s.cnt[wave][e[k]], 1);
-  __syncthreads();
-}
+// A wave's part of a chunk: `steps` (up to IT) times 64 consecutive choices.
+template <int IT>
+struct SortPart {
+  int64_t first;       // this lane's first choice
+  int steps;
+  int e[IT];           // experts
+  uint64_t same[IT];   // the lanes of the same expert (without one: anything)
 
+  // Reads the choices and counts them.
+  __device__ __forceinline__ void count(const SortParams& p, SortLds& s) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t n = p.tokens * p.top_k, c0 = (int64_t)blockIdx.x * (IT * 1024);
+    steps = (int)((min(n - c0, (int64_t)IT * 1024) + 1023) >> 10);  // few choices: one step of every wave
+    first = c0 + wave * (steps * 64) + lane;
+#pragma unroll
+    for (int k = 0; k < IT; ++k) e[k] = k < steps ? choice(p, first + k * 64, n) : -1;
+    for (int x = lane; x < p.experts; x += 64) s.cnt[wave][x] = 0;
+    const int bits = 32 - __clz(p.experts);
+#pragma unroll
+    for (int k = 0; k < IT; ++k) {
+      if (k >= steps) break;
+      // by one ballot per bit of the expert's number
+      same[k] = __ballot(e[k] >= 0);
+      for (int b = 0; b < bits; ++b) {
+        const uint64_t one = __ballot((e[k] >> b) & 1);
+        same[k] &= (e[k] >> b) & 1 ? one : ~one;
+      }
+      if (e[k] >= 0 && earlier(k) == 0) atomicAdd(&s.cnt[wave][e[k]], __popcll(same[k]));
+    }
+    __syncthreads();
+  }
+  // Lanes before this one with the same expert in step k.
+  __device__ __forceinline__ int earlier(int k) const {
+    return __popcll(same[k] & ((uint64_t(1) << (threadIdx.x & 63)) - 1));
+  }
+};
+
+template <int IT>
 __global__ __launch_bounds__(kSortThreads) void expert_count_kernel(SortParams p) {
   __shared__ SortLds s;
-  int e[kPerWave / 64];
-  count_chunk(p, blockIdx.x, s, e);
+  SortPart<IT> part;
+  part.count(p, s);
   for (int x = threadIdx.x; x < p.experts; x += kSortThreads) {
     int n = 0;
 #pragma unroll
@@ -55,13 +77,14 @@ __global__ __launch_bounds__(kSortThreads) void expert_count_kernel(SortParams p
   }
 }
 
-// Ranks the choices of one chunk: their rows into row[] (-1: none); offsets by
-// the workgroup that has `write`.
-__device__ __forceinline__ void rank_chunk(const SortParams& p, int chunk, bool write, SortLds& s,
-                                           int (&row)[kPerWave / 64]) {
+// Ranks the choices of chunk blockIdx.x: rows, the choice of each row, and (the
+// first workgroup) offsets.
+template <int IT>
+__global__ __launch_bounds__(kSortThreads) void expert_rank_kernel(SortParams p) {
+  __shared__ SortLds s;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, t = threadIdx.x;
-  int e[kPerWave / 64];
-  count_chunk(p, chunk, s, e);
+  SortPart<IT> part;
+  part.count(p, s);
   // expert t's choices in all, and in the chunks before this one
   int all = 0, before = 0;
   if (t < p.experts) {
@@ -73,7 +96,7 @@ __device__ __forceinline__ void rank_chunk(const SortParams& p, int chunk, bool 
       for (int c = 0; c < p.chunks; ++c) {
         const int n = p.counts[(int64_t)c * p.experts + t];
         all += n;
-        before += c < chunk ? n : 0;
+        before += c < (int)blockIdx.x ? n : 0;
       }
     }
   }
@@ -89,7 +112,7 @@ __device__ __forceinline__ void rank_chunk(const SortParams& p, int chunk, bool 
   int first = sum - all;
   for (int w = 0; w < wave; ++w) first += s.wave_sum[w];
   if (t < p.experts) {
-    if (write) {
+    if (blockIdx.x == 0) {
       p.offsets[t] = first;
       if (t == p.experts - 1) p.offsets[t + 1] = first + all;
     }
@@ -102,34 +125,21 @@ __device__ __forceinline__ void rank_chunk(const SortParams& p, int chunk, bool 
     }
   }
   __syncthreads();
-  // a wave's choices in order, 64 at a time: those of the same expert among
-  // them by one ballot per bit of the expert's number
-  const int bits = 32 - __clz(p.experts);
-#pragma unroll
-  for (int k = 0; k < kPerWave / 64; ++k) {
-    uint64_t same = __ballot(e[k] >= 0);
-    for (int b = 0; b < bits; ++b) {
-      const uint64_t one = __ballot((e[k] >> b) & 1);
-      same &= (e[k] >> b) & 1 ? one : ~one;
-    }
-    const int earlier = __popcll(same & ((uint64_t(1) << lane) - 1));
-    row[k] = -1;
-    if (e[k] >= 0) row[k] = s.cnt[wave][e[k]] + earlier;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    if (e[k] >= 0 && earlier == 0) s.cnt[wave][e[k]] += __popcll(same);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  }
-}
-
-__global__ __launch_bounds__(kSortThreads) void expert_rank_kernel(SortParams p) {
-  __shared__ SortLds s;
-  int row[kPerWave / 64];
-  rank_chunk(p, blockIdx.x, blockIdx.x == 0, s, row);
+  // a wave's choices in order, 64 at a time: the first lane of each expert takes
+  // the rows of its equals
   const int64_t n = p.tokens * p.top_k;
-  const int64_t i0 = (int64_t)blockIdx.x * kSortChunk + (threadIdx.x >> 6) * kPerWave + (threadIdx.x & 63);
 #pragma unroll
-  for (int k = 0; k < kPerWave / 64; ++k)
-    if (i0 + k * 64 < n) p.rows[i0 + k * 64] = row[k];
+  for (int k = 0; k < IT; ++k) {
+    if (k >= part.steps) break;
+    const int e = part.e[k], earlier = part.earlier(k);
+    int at = 0;
+    if (e >= 0 && earlier == 0) at = atomicAdd(&s.cnt[wave][e], __popcll(part.same[k]));
+    at = __shfl(at, e >= 0 ? __ffsll((unsigned long long)part.same[k]) - 1 : lane) + earlier;
+    const int64_t i = part.first + k * 64;
+    if (i >= n) continue;
+    if (p.rows) p.rows[i] = e >= 0 ? at : -1;
+    if (p.order && e >= 0) p.order[at] = (int32_t)i;
+  }
 }
 
 // A thread moves 16 bytes of a token's row; `chunks` of them per row.
@@ -297,8 +307,14 @@ void combine_grad(const CombineParams& p, int cus, hipStream_t s) {
 }  // namespace
 
 void launch_expert_sort(const SortParams& p, hipStream_t s) {
-  if (p.chunks > 1) hipLaunchKernelGGL(expert_count_kernel, dim3(p.chunks), dim3(kSortThreads), 0, s, p);
-  hipLaunchKernelGGL(expert_rank_kernel, dim3(p.chunks), dim3(kSortThreads), 0, s, p);
+  if (p.chunks > 1) {
+    hipLaunchKernelGGL(expert_count_kernel<4>, dim3(p.chunks), dim3(kSortThreads), 0, s, p);
+    hipLaunchKernelGGL(expert_rank_kernel<4>, dim3(p.chunks), dim3(kSortThreads), 0, s, p);
+  } else if (p.tokens * p.top_k <= kSortChunk) {
+    hipLaunchKernelGGL(expert_rank_kernel<4>, dim3(1), dim3(kSortThreads), 0, s, p);
+  } else {
+    hipLaunchKernelGGL(expert_rank_kernel<8>, dim3(1), dim3(kSortThreads), 0, s, p);
+  }
   if (!p.X) return;
   const int64_t n = p.tokens * (p.row_bytes / 16);
   hipLaunchKernelGGL(expert_gather_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, p);

@@ -112,10 +112,15 @@ struct RowsLds {
   static constexpr int BYTES = RING > JOIN ? RING : JOIN;
 };
 
-// Columns n0 .. n0 + 15 of D for p.M <= 4 * MB tokens, with the LDS array `lds`
-// (1 KiB aligned).  more(acc): what a wave adds to its part of the sums.
-template <int AB, int MB, int NW, int NS, bool MUL, class F>
-__device__ __forceinline__ void linear_rows_body(const LinParams& p, int64_t n0, char* lds, F&& more) {
+// The products of up to 16 weight rows with p.M <= 4 * MB tokens (the rows of p.A),
+// with the LDS array `lds` (1 KiB aligned).  weights: a buffer resource; place(i): the
+// byte in it at which weight row i begins (0x80000000: there is none).  begin(m, n)
+// is called before the products by the lane that finishes weight rows n .. n + 3 of
+// token m, where there are such, and finish(m, n, sums) after them; more(acc): what a
+// wave adds to its part of the sums.
+template <int AB, int MB, int NW, int NS, class PLACE, class BEGIN, class MORE, class FINISH>
+__device__ __forceinline__ void rows_products(const LinParams& p, v4i weights, PLACE&& place, char* lds, BEGIN&& begin,
+                                              MORE&& more, FINISH&& finish) {
   using MM = RowsMma<AB>;
   constexpr int ES = AB == T_F16 || AB == T_BF16 ? 2 : 1;
   constexpr int NB = (MB + 3) / 4;               // token blocks of 16
@@ -127,17 +132,17 @@ __device__ __forceinline__ void linear_rows_body(const LinParams& p, int64_t n0,
 
   // Rows past the matrix and chunks past K get an offset outside the
   // resource's extent and arrive as zeros.
-  const int64_t lda = p.lda * ES, ldb = p.ldb * ES;
+  const int64_t lda = p.lda * ES;
   const uint32_t kbytes = (uint32_t)(p.K * ES);
-  const int brows = (int)min((int64_t)16, p.N - n0);
-  const v4i rb = make_rsrc((const char*)p.B + n0 * ldb, (uint32_t)((brows - 1) * ldb + kbytes));
+  const v4i rb = weights;
   const v4i ra = make_rsrc(p.A, (uint32_t)((p.M - 1) * lda + kbytes));
   // DMA lane: row 4 * instruction + q, chunk position r
   uint32_t ob[4], oa[MB], cb[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     cb[i] = (uint32_t)((r ^ (4 * i + q)) * 16);  // logical chunk of row 4 i + q (mod 16)
-    ob[i] = 4 * i + q < brows ? (uint32_t)((4 * i + q) * ldb) + cb[i] : 0x80000000u;
+    const uint32_t at = place(4 * i + q);
+    ob[i] = at != 0x80000000u ? at + cb[i] : 0x80000000u;
   }
 #pragma unroll
   for (int i = 0; i < MB; ++i) oa[i] = 4 * i + q < p.M ? (uint32_t)((4 * i + q) * lda) + cb[i & 3] : 0x80000000u;
@@ -146,10 +151,9 @@ __device__ __forceinline__ void linear_rows_body(const LinParams& p, int64_t n0,
   // The outputs this wave finishes: token block `wave`, whose bias, scales and
   // residual are read ahead.
   static_assert(NB <= NW, "a wave finishes at most one block");
-  const int64_t fm = wave * 16 + r, fn = n0 + 4 * q;
-  const bool fin = wave < NB && fm < p.M && fn < p.N;
-  Epi4<MUL> epi;
-  if (fin) epi.load(p, fm, fn);
+  const int fm = wave * 16 + r, fn = 4 * q;
+  const bool fin = wave < NB && fm < p.M;
+  if (fin) begin(fm, fn);
 
   typename MM::acc_t acc[NB];
 #pragma unroll
@@ -210,7 +214,26 @@ __device__ __forceinline__ void linear_rows_body(const LinParams& p, int64_t n0,
   typename MM::acc_t sum = __builtin_bit_cast(typename MM::acc_t, part[0][wave][lane]);
 #pragma unroll
   for (int w = 1; w < NW; ++w) sum += __builtin_bit_cast(typename MM::acc_t, part[w][wave][lane]);
-  epi.finish(p, fm, fn, v4f{(float)sum[0], (float)sum[1], (float)sum[2], (float)sum[3]});
+  finish(fm, fn, v4f{(float)sum[0], (float)sum[1], (float)sum[2], (float)sum[3]});
+}
+
+// Columns n0 .. n0 + 15 of D for p.M <= 4 * MB tokens.
+template <int AB, int MB, int NW, int NS, bool MUL, class MORE>
+__device__ __forceinline__ void linear_rows_body(const LinParams& p, int64_t n0, char* lds, MORE&& more) {
+  constexpr int ES = AB == T_F16 || AB == T_BF16 ? 2 : 1;
+  const int64_t ldb = p.ldb * ES;
+  const int brows = (int)min((int64_t)16, p.N - n0);
+  const v4i rb = make_rsrc((const char*)p.B + n0 * ldb, (uint32_t)((brows - 1) * ldb + p.K * ES));
+  Epi4<MUL> epi;
+  rows_products<AB, MB, NW, NS>(
+      p, rb, [&](int i) { return i < brows ? (uint32_t)(i * ldb) : 0x80000000u; }, lds,
+      [&](int m, int n) {
+        if (n0 + n < p.N) epi.load(p, m, n0 + n);
+      },
+      more,
+      [&](int m, int n, v4f sum) {
+        if (n0 + n < p.N) epi.finish(p, m, n0 + n, sum);
+      });
 }
 
 }  // namespace gemm_epi

@@ -8,6 +8,7 @@
  *
  * Rows whose id lies outside 0 .. adapters - 1 have no adapter.  Rows of the same
  * adapter need not lie together; they are fastest where they do (packed prompts).
+ * An infinity or a NaN in one adapter's weights reaches that adapter's rows only.
  * The inner products scale[g] A[m] . down[g]^T are summed in fp32 and rounded once
  * to the operands' type, which the matrix cores read; everything else is as in
  * gemm_epi_linear.h, whose conventions hold.  Adapters of a smaller rank are padded
@@ -26,13 +27,14 @@ typedef struct gemm_epi_adapter_linear_desc {
   gemm_epi_linear_desc linear; /* the projection: ab_dtype F16 or BF16, D of the
                                   same type, no scale_a and scale_b */
   int32_t rank;                /* 8 .. 128, a multiple of 8 */
-  int32_t adapters;            /* >= 1 */
+  int32_t adapters;            /* 1 .. 1024 */
 } gemm_epi_adapter_linear_desc;
 
 typedef struct gemm_epi_adapter_linear_handle gemm_epi_adapter_linear_handle;
 
 /* Validate and plan, with the projection's plan (errors as for
- * gemm_epi_linear_create). */
+ * gemm_epi_linear_create; 2^26 or more rows, and A, up or one adapter's down of 2
+ * GiB or more, are UNSUPPORTED). */
 int gemm_epi_adapter_linear_create(const gemm_epi_adapter_linear_desc* desc, gemm_epi_adapter_linear_handle** out);
 
 /* The same with the linear layer's kernel `variant` (-1: its choice). */

@@ -50,7 +50,7 @@ def _create(rank=16, count=4, **fields):
 
 BAD = [
     (dict(rank=0), INVALID), (dict(rank=-8), INVALID), (dict(rank=12), ALIGN), (dict(rank=136), UNSUPPORTED),
-    (dict(count=0), INVALID), (dict(count=-1), INVALID), (dict(M=0), INVALID), (dict(N=-8), INVALID), (dict(K=0), INVALID),
+    (dict(count=0), INVALID), (dict(count=1025), UNSUPPORTED), (dict(M=1 << 26), UNSUPPORTED), (dict(count=-1), INVALID), (dict(M=0), INVALID), (dict(N=-8), INVALID), (dict(K=0), INVALID),
     (dict(ab_dtype=T["e4m3"]), UNSUPPORTED), (dict(ab_dtype=T["i8"]), UNSUPPORTED), (dict(ab_dtype=0), INVALID),
     (dict(ab_dtype=99), INVALID), (dict(d_dtype=T["f32"]), UNSUPPORTED), (dict(d_dtype=T["f16"]), UNSUPPORTED),
     (dict(scale_a=1), UNSUPPORTED), (dict(scale_b=1), UNSUPPORTED), (dict(act=7), INVALID), (dict(bias_dtype=T["i8"]), INVALID),
@@ -67,7 +67,7 @@ def test_validation(bad, code):
 def test_valid_problems_stop_at_the_device():
     if torch.cuda.is_available():
         pytest.skip("a GPU is present")
-    for more in ({}, dict(M=1, rank=8, count=1), dict(rank=128, count=1000), dict(ab_dtype=T["f16"], d_dtype=T["f16"], act=4),
+    for more in ({}, dict(M=1, rank=8, count=1), dict(rank=128, count=1024), dict(ab_dtype=T["f16"], d_dtype=T["f16"], act=4),
                  dict(residual=1, ldr=264, z=1, lda=520, ldd=256, bias_dtype=T["f32"], splits=2)):
         assert _create(**more) == DEVICE, ge.last_error()
 

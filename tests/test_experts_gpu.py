@@ -66,7 +66,7 @@ def run_sort(T, k, E, cols, x="bf16", ids="i64", kind="some", scale=False, pad=0
 
 
 @pytest.mark.parametrize("T,k,E", [(1, 1, 1), (1, 8, 64), (3, 2, 5), (16, 8, 64), (63, 1, 2), (64, 1, 1024), (65, 3, 13),
-                                   (512, 8, 128), (4096, 1, 16), (4097, 1, 16), (683, 6, 1000), (5000, 8, 256),
+                                   (512, 8, 128), (4096, 1, 16), (4097, 1, 16), (8192, 1, 16), (8193, 1, 1024), (683, 6, 1000), (5000, 8, 256),
                                    (20, 64, 100), (12345, 5, 33)])
 def test_sort(T, k, E):
     run_sort(T, k, E, 64, kind="some", seed=T)
@@ -254,7 +254,7 @@ def test_streams_and_graphs():
     """Two streams at once and two graphs replayed in turn give what one call
     gives, with rows of their own and a workspace each."""
     g = torch.Generator().manual_seed(8)
-    T, k, E, cols = 3000, 4, 40, 256
+    T, k, E, cols = 3000, 4, 40, 256  # two chunks of the sort
     ids = _ids(g, T, k, E).cuda()
     X, w = _draw(g, T, cols, torch.bfloat16).cuda(), torch.rand(T, k, generator=g).cuda()
     sort, back = ge.ExpertSort(T, k, E, cols=cols), ge.ExpertCombine(T, k, cols)
