@@ -1170,8 +1170,8 @@ __device__ __forceinline__ void gemm_epi_body(const typename CF::params_t& p, ch
       constexpr int D = decltype(d_c)::value;
       constexpr bool GUARD = decltype(guard_c)::value;
       if (GUARD && k_tile >= KT) return;
-      if constexpr (CF::ADAPTERS && GUARD) {
-        if (k_tile >= KTA) {
+      if constexpr (CF::ADAPTERS) {
+        if (GUARD && k_tile >= KTA) {
           if constexpr (D < NQ_A)
             adapters.template issue_rows<D>(p, lds, lds_wave + (uint32_t)stg * (uint32_t)A_STAGE, k_tile - KTA);
           else

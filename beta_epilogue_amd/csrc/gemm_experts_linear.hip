@@ -348,7 +348,10 @@ struct gemm_epi_expert_linear_grad_handle {
   int64_t chunk, slots;   // rows of a chunk of the elementwise pass, and chunks at most
   int64_t ga, gb, sums;   // workgroups of the products and of the column sums
   int64_t ws_bytes;
-  bool pass() const { return d.act != GEMM_EPI_ACT_NONE || d.mul || d.dbias_dtype != GEMM_EPI_NONE; }
+  // without an activation and mul dbias adds up dD's rows beside the products, in
+  // workgroups of 64 columns and all rows of an expert: where those are not too many
+  bool sum_rows;
+  bool pass() const { return has_z() || (d.dbias_dtype != GEMM_EPI_NONE && !sum_rows); }
   bool has_z() const { return d.act != GEMM_EPI_ACT_NONE || d.mul; }
 };
 
@@ -402,7 +405,9 @@ extern "C" int gemm_epi_expert_linear_grad_create(const gemm_epi_expert_linear_g
   const int64_t tn = (d.N + h.tile - 1) / h.tile, tk = (d.K + h.tile - 1) / h.tile;
   h.ga = d.da_dtype != GEMM_EPI_NONE ? worst_chunks(d.rows, d.experts, h.tile) * tk : 0;
   h.gb = d.db_dtype != GEMM_EPI_NONE ? 8 * d.experts * ((tn * tk + 7) / 8) : 0;
-  h.sums = d.dbias_dtype != GEMM_EPI_NONE ? d.experts * ((d.N + 255) / 256) : 0;
+  h.sum_rows = !h.has_z() && h.ga + h.gb > 0 && d.rows / d.experts <= 4096;
+  const int64_t columns = h.sum_rows ? 64 : 256;
+  h.sums = d.dbias_dtype != GEMM_EPI_NONE ? d.experts * ((d.N + columns - 1) / columns) : 0;
   // 256 threads for each, fewer than 2^32 in all
   if (h.ga + h.gb + h.sums >= int64_t(1) << 24) return fail(GEMM_EPI_ERR_UNSUPPORTED, "2^24 or more work items");
   // rows per workgroup of the elementwise pass: 64, fewer as long as there are under
@@ -411,7 +416,7 @@ extern "C" int gemm_epi_expert_linear_grad_create(const gemm_epi_expert_linear_g
   while (h.chunk > 8 && (d.N + 255) / 256 * worst_chunks(d.rows, d.experts, h.chunk) < 4 * cus) h.chunk /= 2;
   while (worst_chunks(d.rows, d.experts, h.chunk) > 65535) h.chunk *= 2;
   h.slots = worst_chunks(d.rows, d.experts, h.chunk);
-  h.ws_bytes = d.dbias_dtype != GEMM_EPI_NONE ? up256(h.slots * d.N * 4) : 0;
+  h.ws_bytes = d.dbias_dtype != GEMM_EPI_NONE && !h.sum_rows ? up256(h.slots * d.N * 4) : 0;
   *out = new (std::nothrow) gemm_epi_expert_linear_grad_handle(h);
   return *out ? GEMM_EPI_OK : fail(GEMM_EPI_ERR_HOST_ALLOC, "out of host memory");
 }
@@ -514,6 +519,7 @@ extern "C" int gemm_epi_expert_linear_grad_run(const gemm_epi_expert_linear_grad
   p.ga = (int32_t)h->ga;
   p.gb = (int32_t)h->gb;
   p.sums = (int32_t)h->sums;
+  p.sum_rows = dbias && h->sum_rows ? dD : nullptr;
   p.partial = (const float*)workspace;
   p.chunk = (int32_t)h->chunk;
   p.slots = (int32_t)h->slots;

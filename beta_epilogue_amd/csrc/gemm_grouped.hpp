@@ -165,6 +165,7 @@ struct GroupGradParams {
   GroupParams a, b;
   int32_t ga, gb, sums;   // workgroups
   int32_t b_first;
+  const void* sum_rows;   // dD, whose rows dbias adds up; NULL: the chunks' sums
   const float* partial;   // [chunk][N]
   int32_t chunk, slots;   // rows of a chunk, chunks that partial holds
   void* dbias;            // groups x N

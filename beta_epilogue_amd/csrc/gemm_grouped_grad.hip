@@ -6,7 +6,7 @@
 // the most rows first and each expert's spread over the XCDs (16384 rows of 8
 // experts, 825 to 4282 each, N 4096, K 2048: dB 344 us with an expert per XCD).
 // dbias is made by further workgroups from the elementwise pass's column sums, in
-// the order of the chunks.
+// the order of the chunks, or without such a pass from dD's rows.
 #include "gemm_grouped.hpp"
 
 #ifndef GEMM_GROUPED_GRAD_PART
@@ -16,6 +16,35 @@
 namespace gemm_epi {
 
 namespace {
+
+// 64 columns of group g's dbias, straight from its rows of dD: 8 lanes of 8 columns
+// by 32 strands of rows, joined in a fixed order.  red: 32 x 68 words.
+template <int AB>
+__device__ __forceinline__ void group_row_sums(const GroupGradParams& p, int block, float* red) {
+  const int per = (int)((p.N + 63) / 64), g = block / per;
+  const GroupTile t = group_rows(p.a, g);
+  const int cl = threadIdx.x & 7, pl = threadIdx.x >> 3;
+  const int64_t c0 = (int64_t)(block - g * per) * 64, c = c0 + cl * 8;
+  float s[8] = {};
+  if (c < p.N) {
+#pragma unroll 8
+    for (int r = t.begin + pl; r < t.end; r += 32) {
+      const v4u w = *(const v4u*)((const uint16_t*)p.sum_rows + r * p.N + c);
+      const v4f lo = epi_dec<AB>(w, 0), hi = epi_dec<AB>(w, 1);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[k] += lo[k], s[4 + k] += hi[k];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) red[pl * 68 + cl * 8 + k] = s[k];
+  __syncthreads();
+  const int64_t n = c0 + threadIdx.x;
+  if (threadIdx.x >= 64 || n >= p.N) return;
+  float v = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 32; ++k) v += red[k * 68 + threadIdx.x];
+  store_as(p.dbias, g * p.N + n, p.dbias_dtype, v);
+}
 
 // 256 columns of group g's dbias.
 __device__ __forceinline__ void group_sums(const GroupGradParams& p, int block, int* first) {
@@ -44,6 +73,8 @@ __global__ __launch_bounds__(256, grad_occ(KIND)) void grouped_grad_kernel(Group
     gemm_epi_body<CA>(p.a, lds, bid - a0, p.ga, GroupWork{first, 0, total, 0});
   } else if (bid < p.gb + p.ga) {
     gemm_epi_body<CB>(p.b, lds, bid - b0, p.gb);
+  } else if (p.sum_rows) {
+    group_row_sums<AB>(p, bid - p.gb - p.ga, (float*)lds);
   } else {
     group_sums(p, bid - p.gb - p.ga, (int*)lds);
   }

@@ -13,7 +13,8 @@ namespace {
 // Persistent workgroups, an equal share of the tiles each.  Only the device knows
 // how many tiles there are, and a last round of 256x256 tiles that leaves half of
 // the compute units or more idle runs as quarters on the 128x128 kernel: a
-// quarter takes under half of a tile's time.
+// quarter takes under half of a tile's time.  (Quarters first in every other
+// workgroup, so that not all of them write at the same time, changed nothing.)
 template <class CF>
 __global__ __launch_bounds__(CF::THREADS, CF::OCC) void grouped_kernel(GroupParams p) {
   __shared__ __attribute__((aligned(1024))) char lds[CF::LDS_BYTES + kGroupTableBytes];
@@ -21,9 +22,9 @@ __global__ __launch_bounds__(CF::THREADS, CF::OCC) void grouped_kernel(GroupPara
   const int G = gridDim.x, total = group_table_rows(p, first, CF::BM) * p.tiles_n;
   if constexpr (CF::BM == 256) {
     const int left = total % G, whole = left <= G / 2 ? total - left : total;
-    gemm_epi_body<CF>(p, lds, blockIdx.x, G, GroupWork{first, 0, whole, 0});
     using Q = GroupedQuarter<CF::AB>;
     static_assert(Q::LDS_BYTES <= CF::LDS_BYTES && Q::THREADS == CF::THREADS, "one workgroup for both");
+    gemm_epi_body<CF>(p, lds, blockIdx.x, G, GroupWork{first, 0, whole, 0});
     gemm_epi_body<Q>(p, lds, blockIdx.x, G, GroupWork{first, 4 * whole, 4 * total, 1});
   } else {
     gemm_epi_body<CF>(p, lds, blockIdx.x, G, GroupWork{first, 0, total, 0});
