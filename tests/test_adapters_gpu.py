@@ -255,3 +255,35 @@ def test_refusals():
                 dict(workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))):
         with pytest.raises((ValueError, ge.GemmEpiError)):
             op(**(good | bad))
+
+
+@pytest.mark.parametrize("name", TILES)
+@pytest.mark.parametrize("splits", [1, 2])
+def test_adapters_that_are_not_finite(name, splits):
+    """An infinity or a NaN in some adapters' up reaches their rows only, in every
+    kernel: the others' rows are what they are without it, bit for bit."""
+    ab, v = name.split("_")[1], ge.linear_variant_names().index(name)
+    M, N, K, rank, G = 300, 264, 136, 24, 6
+    g = torch.Generator().manual_seed(3)
+    T = TORCH[ab]
+    A, B = _draw(g, M, K, T).cuda(), _draw(g, N, K, T, K ** -0.5).cuda()
+    ids = some_ids(g, M, G, "mixed")
+    down, up = _draw(g, G * rank, K, T, K ** -0.5).view(G, rank, K).cuda(), _draw(g, G * N, rank, T).view(G, N, rank).cuda()
+    bad = up.clone()
+    bad[2, 7, 3], bad[2, N - 1, rank - 1], bad[5, 0, 0] = float("inf"), -float("inf"), NAN
+    op = ge.AdapterLinear(M, N, K, rank, G, ab=ab, variant=v, splits=splits)
+    D, want = torch.zeros(M, N, dtype=T, device="cuda"), torch.zeros(M, N, dtype=T, device="cuda")
+    scale = torch.ones(G, device="cuda")
+    _say("case not finite", name, splits)
+    op(A, B, ids.cuda(), down, up, scale, D=want)
+    op(A, B, ids.cuda(), down, bad, scale, D=D)
+    theirs = (ids == 2) | (ids == 5)
+    assert torch.equal(D[~theirs], want[~theirs])
+    assert torch.isnan(D[ids == 5][:, 0]).all() and torch.isfinite(D[ids == 5][:, 1:]).all()
+    assert not torch.isfinite(D[ids == 2][:, 7]).any() and not torch.isfinite(D[ids == 2][:, N - 1]).any()
+    assert torch.isfinite(D[ids == 2][:, 8:N - 1]).all()
+    # (their finite columns: the same sums in another order)
+    d, _, bd, _ = plain(A.cpu(), B.cpu(), ids, down.cpu(), up.cpu(), torch.ones(G), "none", None, None, T)
+    rest = torch.ones(N, dtype=torch.bool)
+    rest[[0, 7, N - 1]] = False
+    ref.check("D", D[theirs][:, rest], d[theirs][:, rest], bd[theirs][:, rest])

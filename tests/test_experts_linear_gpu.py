@@ -488,3 +488,41 @@ def test_refusals():
                 dict(dA=good["A"]), dict(offsets=None), dict(workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))):
         with pytest.raises((ValueError, ge.GemmEpiError)):
             grad(**(good | bad))
+
+
+def test_far_weights_and_rows():
+    """Weights of more than 4 GiB in all, and rows that begin more than 4 GiB into A
+    and D, through the few-row kernels and the tiles."""
+    if torch.cuda.mem_get_info()[0] < 64 << 30:
+        pytest.skip("less than 64 GiB of device memory free")
+    g = torch.Generator().manual_seed(4)
+    E, N, K = 40, 8192, 8192  # 5.4 GB of bf16
+    last = _draw(g, N, K, torch.bfloat16, K ** -0.5)
+    B = torch.zeros(E, N, K, dtype=torch.bfloat16, device="cuda")
+    B[E - 1] = last.cuda()
+    for R in (3, 100):
+        A = _draw(g, R, K, torch.bfloat16)
+        off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+        off[E] = R
+        D = torch.zeros(R, N, dtype=torch.bfloat16, device="cuda")
+        op = ge.ExpertLinear(R, E, N, K)
+        _say("case far weights", R, op.plan["name"])
+        op(A.cuda(), B, off, D=D)
+        cols = slice(N - 64, N)
+        dr, _, S = ref.linear(A, last[cols])
+        ref.check("D", D[:, cols], dr, (K + 4) * ref.U * S + ref.half_step(dr.abs() + K * ref.U * S, torch.bfloat16))
+    del B
+    R, E, N, K, ld = 1200, 3, 64, 64, 2 << 20  # 4 MiB between rows: 5 GB
+    big = torch.zeros(R, ld, dtype=torch.bfloat16, device="cuda")
+    A, B = _draw(g, R, K, torch.bfloat16), _draw(g, E * N, K, torch.bfloat16).view(E, N, K)
+    view = big[:, :K]
+    view.copy_(A)
+    out = big[:, 64:64 + N]
+    off = [0, 5, 1000, R]
+    op = ge.ExpertLinear(R, E, N, K, lda=ld, ldd=ld)
+    _say("case far rows", op.plan["name"])
+    op(view, B.cuda(), torch.tensor(off, dtype=torch.int32, device="cuda"), D=out)
+    for e in range(E):
+        at = slice(off[e], off[e + 1])
+        dr, _, S = ref.linear(A[at], B[e])
+        ref.check("D", out[at], dr, (K + 4) * ref.U * S + ref.half_step(dr.abs() + K * ref.U * S, torch.bfloat16))
