@@ -56,8 +56,8 @@ double likely_chunks(int64_t rows, int64_t experts, int64_t chunk) {
 // Modelled time (us) of a tile kernel: the linear layer's model over the tiles
 // that are to be expected (half a round on the mean for the last one; 256x256 tiles
 // may finish it as quarters), and the weights of the experts that have rows once
-// from memory, at the 5.2 TB/s that the 64x64 tiles reach (512 rows, 64 experts,
-// bf16 1536 x 2048: 78 us).
+// from memory, at the 5.2 TB/s that the 64x64 tiles reach and the larger ones do not
+// (512 rows, 64 experts, bf16 1536 x 2048: 78, 102 and 141 us).
 double tiles_time(const GroupedVariant& v, const gemm_epi_expert_linear_desc& d, int64_t cus) {
   const LinearCost& w = linear_cost(v.ab);
   const double items = likely_chunks(d.rows, d.experts, v.bm) * (double)((d.N + v.bn - 1) / v.bn);
@@ -66,10 +66,11 @@ double tiles_time(const GroupedVariant& v, const gemm_epi_expert_linear_desc& d,
   if (v.occ >= 2 && items > (double)cus) tk = v.bm == 128 ? w.pair128 : w.pair64, slots *= 2;
   if (v.occ >= 3 && items > 2.0 * (double)cus) tk = w.three64, slots *= 1.5;
   const double item = tk * (double)((d.K + v.bk - 1) / v.bk) + epi;
-  const double rounds = std::max(1.0, items / slots + (v.bm == 256 ? 0.35 : 0.5));
+  const double full = items / slots, last = full <= 0.8 ? 0.2 : v.bm == 256 ? 0.35 : 0.5;
+  const double rounds = std::max(1.0, full + last);
   const double es = elem_bytes(d.ab_dtype), n = (double)std::min<int64_t>(d.rows, d.experts);
   const double stream = (n * (double)d.N + (double)d.rows) * (double)d.K * es / 5.2e6;
-  return w.start + std::max(rounds * item, stream);
+  return w.start + std::max(rounds * item, stream * (v.bm == 64 ? 1.0 : v.bm == 128 ? 1.15 : 1.5));
 }
 
 // The few-row kernels: a workgroup's waves stream runs of 256 bytes of K each; a
