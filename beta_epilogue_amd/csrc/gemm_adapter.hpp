@@ -193,14 +193,16 @@ struct AdapterDownParams {
   const int32_t* ids;
   void* U;
   int32_t* finite;
-  int32_t* order;      // workspace, with adapter_sorted: the rows by adapter,
+  int32_t* order;      // workspace, with adapter_sorted (else NULL): the rows by adapter,
   int32_t* offsets;    // where each adapter's begin,
   int32_t* counts;     // and the sort's
   int64_t M, N, K, lda;
   int32_t rank, adapters;
 };
-// Whether the rows are sorted by adapter first.
-inline bool adapter_sorted(int64_t M, int rank) { return M * rank > 8192; }
+// Up to so many products (rows times rank) a wave makes each by itself; of more the
+// rows are sorted by adapter first, where there are more than two.
+constexpr int64_t kAdapterDots = 8192;
+inline bool adapter_sorted(int64_t M, int rank, int adapters) { return M * rank > kAdapterDots && adapters > 2; }
 void launch_adapter_down(int ab, const AdapterDownParams& p, hipStream_t s);
 
 // The linear layer's kernels with the rows' adapters.

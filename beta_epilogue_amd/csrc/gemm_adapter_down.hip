@@ -8,7 +8,9 @@
 // More rows are sorted by adapter (gemm_experts_kernels.hip), so that a workgroup
 // has 16 rows of one, streamed past the adapter's weights by the few-row kernel
 // (gemm_linear_rows.hip): 4001 x 4096, rank 64, 14 us with the fragments through LDS
-// and 24 with fragments straight from memory.
+// and 24 with fragments straight from memory.  With up to two adapters the rows stay
+// as they are, and a workgroup takes one after the other: a launch less.  (With four,
+// all mixed, 1000 x 1024, rank 32, that is 14.4 us against 3.1 and 6.3.)
 //
 // Further workgroups of the same launch look whether the up[g] that the rows meet
 // are finite (AdapterTiles).
@@ -90,8 +92,9 @@ __global__ __launch_bounds__(256) void adapter_dots_kernel(AdapterDownParams p, 
   if (lane == 0) store_as(p.U, (int64_t)m * p.rank + j, AB, s * p.scale[g]);
 }
 
-// 16 rows of one adapter, 64 of its products (4 * MB at most): the few-row kernel with
-// the rows in the weight's place and the adapter's in the tokens'.
+// 16 rows, 64 of their products (4 * MB at most): the few-row kernel with the rows in
+// the weight's place and the adapter's in the tokens'.  Sorted rows have one adapter,
+// others are taken one adapter at a time.
 template <int AB, int MB, int NW, int NS>
 __global__ __launch_bounds__(NW * 64) void adapter_down_kernel(AdapterDownParams p, int blocks, int per) {
   __shared__ __attribute__((aligned(1024))) char lds[RowsLds<AB, MB, NW, NS>::BYTES];
@@ -99,63 +102,84 @@ __global__ __launch_bounds__(NW * 64) void adapter_down_kernel(AdapterDownParams
     finite_block<AB>(p, blockIdx.x - blocks * per, (int*)lds);
     return;
   }
-  GroupParams gp;
-  gp.offsets = p.offsets;
-  gp.groups = p.adapters;
-  gp.rows = (int)p.M;
   const int chunk = blockIdx.x / per, j0 = (blockIdx.x - chunk * per) * 64;
-  const GroupTile t = group_chunk(gp, chunk, 16);
-  if (t.group < 0) return;
   const int lane = threadIdx.x & 63;
-  const int mine = t.begin + (lane & 15) < t.end ? p.order[t.begin + (lane & 15)] : -1;  // lane i: row i
-  LinParams q;
-  q.A = (const char*)p.down + ((int64_t)t.group * p.rank + j0) * p.K * 2;
-  q.M = min(p.rank - j0, 64);
-  q.K = q.lda = p.K;
-  const float f = p.scale[t.group];
-  rows_products<AB, MB, NW, NS>(
-      q, make_rsrc(p.A, (uint32_t)(((p.M - 1) * p.lda + p.K) * 2)),
-      [&](int i) {
-        const int m = __shfl(mine, i);
-        return m >= 0 ? (uint32_t)(m * p.lda * 2) : 0x80000000u;
-      },
-      lds, [](int, int) {}, [](auto&) {},
-      [&](int j, int i, v4f sum) {
+  int mine = -1, id = -1;  // lane i (and 16 + i, ...): the chunk's row i and its adapter
+  int first = chunk * 16, end = (int)p.M;
+  if (p.order) {
+    GroupParams gp;
+    gp.offsets = p.offsets;
+    gp.groups = p.adapters;
+    gp.rows = (int)p.M;
+    const GroupTile t = group_chunk(gp, chunk, 16);
+    if (t.group < 0) return;
+    first = t.begin;
+    end = t.end;
+    if (first + (lane & 15) < end) mine = p.order[first + (lane & 15)], id = t.group;
+  } else if (first + (lane & 15) < end) {
+    mine = first + (lane & 15);
+    id = p.ids[mine];
+    if (id < 0 || id >= p.adapters) id = -1;
+  }
+  // one adapter of the chunk's rows after the other
+  for (uint64_t todo = __ballot(id >= 0); todo;) {
+    const int g = __builtin_amdgcn_readlane(id, __ffsll((unsigned long long)todo) - 1);
+    todo &= ~__ballot(id == g);
+    const int row = id == g ? mine : -1;
+    LinParams q;
+    q.A = (const char*)p.down + ((int64_t)g * p.rank + j0) * p.K * 2;
+    q.M = min(p.rank - j0, 64);
+    q.K = q.lda = p.K;
+    const float f = p.scale[g];
+    rows_products<AB, MB, NW, NS>(
+        q, make_rsrc(p.A, (uint32_t)(((p.M - 1) * p.lda + p.K) * 2)),
+        [&](int i) {
+          const int m = __shfl(row, i);
+          return m >= 0 ? (uint32_t)(m * p.lda * 2) : 0x80000000u;
+        },
+        lds, [](int, int) {}, [](auto&) {},
+        [&](int j, int i, v4f sum) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (t.begin + i + e >= t.end) continue;
-          const int64_t m = p.order[t.begin + i + e];
-          store_as(p.U, m * p.rank + j0 + j, AB, sum[e] * f);
-        }
-      });
+          for (int e = 0; e < 4; ++e) {
+            const int at = first + i + e;
+            if (at >= end || (!p.order && p.ids[at] != g)) continue;
+            const int64_t m = p.order ? p.order[at] : at;
+            store_as(p.U, m * p.rank + j0 + j, AB, sum[e] * f);
+          }
+        });
+    __syncthreads();  // the sums' join is read: the ring may be filled again
+  }
 }
 
 template <int AB, int MB, int NW, int NS>
 void down(const AdapterDownParams& p, hipStream_t s) {
+  // chunks; sorted: of the worst distribution
   const int64_t n = p.M < p.adapters ? p.M : p.adapters;
-  const int blocks = (int)(n + (p.M - n) / 16), per = (p.rank + 63) / 64;  // chunks of the worst distribution
+  const int blocks = (int)(p.order ? n + (p.M - n) / 16 : (p.M + 15) / 16), per = (p.rank + 63) / 64;
   hipLaunchKernelGGL((adapter_down_kernel<AB, MB, NW, NS>), dim3((unsigned)(blocks * per + p.adapters * kFiniteParts)),
                      dim3(NW * 64), 0, s, p, blocks, per);
 }
 
 template <int AB>
 void launch(const AdapterDownParams& p, hipStream_t s) {
-  if (!adapter_sorted(p.M, p.rank)) {
+  if (p.M * p.rank <= kAdapterDots) {
     const int blocks = (int)(p.M * p.rank / 4);
     hipLaunchKernelGGL(adapter_dots_kernel<AB>, dim3((unsigned)(blocks + (p.finite ? p.adapters * kFiniteParts : 0))), dim3(256),
                        0, s, p, blocks);
     return;
   }
-  SortParams q = {};
-  q.ids = p.ids;
-  q.offsets = p.offsets;
-  q.order = p.order;
-  q.counts = p.counts;
-  q.tokens = p.M;
-  q.top_k = 1;
-  q.experts = p.adapters;
-  q.chunks = (int32_t)sort_chunks(p.M);
-  launch_expert_sort(q, s);
+  if (p.order) {
+    SortParams q = {};
+    q.ids = p.ids;
+    q.offsets = p.offsets;
+    q.order = p.order;
+    q.counts = p.counts;
+    q.tokens = p.M;
+    q.top_k = 1;
+    q.experts = p.adapters;
+    q.chunks = (int32_t)sort_chunks(p.M);
+    launch_expert_sort(q, s);
+  }
   if (p.rank <= 16) down<AB, 4, 4, 2>(p, s);
   else if (p.rank <= 32) down<AB, 8, 4, 1>(p, s);
   else down<AB, 16, 8, 1>(p, s);

@@ -68,7 +68,7 @@ extern "C" int gemm_epi_adapter_linear_create_variant(const gemm_epi_adapter_lin
   h->rank = desc->rank;
   h->adapters = desc->adapters;
   h->bm = plan.tile_k ? plan.tile_m : 0;
-  h->sorted = adapter_sorted(d.M, desc->rank);
+  h->sorted = adapter_sorted(d.M, desc->rank, desc->adapters);
   const int64_t chunks = sort_chunks(d.M);
   h->at_finite = up256(d.M * desc->rank * 2);
   h->at_order = h->at_finite + (h->bm ? up256((int64_t)desc->adapters * kFiniteParts * 4) : 0);

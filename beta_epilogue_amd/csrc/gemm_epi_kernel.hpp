@@ -1121,10 +1121,6 @@ __device__ __forceinline__ void gemm_epi_body(const typename CF::params_t& p, ch
     }
 
     typename std::conditional<CF::ADAPTERS, AdapterTiles<CF>, IntC<0>>::type adapters;
-    if constexpr (CF::ADAPTERS) {
-      adapters.setup(p, lds, m0, n0, split <= 0, opa.cb, lane);  // (once per tile)
-      KT += adapters.tiles;
-    }
 
     acc_t acc[CF::FM][CF::FN];
 #pragma unroll
@@ -1279,10 +1275,23 @@ __device__ __forceinline__ void gemm_epi_body(const typename CF::params_t& p, ch
       asm("" : "+s"(k_tile));
       static_for<0, NQ_STAGE>([&](auto d_c) { dma_one(d_c, IntC<1>{}, k_tile, k_tile % S); });
     };
+    // ADAPTERS: their K tiles are found (once per tile) while the first ones of A
+    // and B are on their way.
+    if constexpr (CF::ADAPTERS) {
+      constexpr int PRO = S == 2 ? 2 : S - 1;
+#pragma unroll
+      for (int k = 0; k < PRO; ++k)
+        if (k < KTA) issue_tile(k);
+      adapters.setup(p, lds, m0, n0, split <= 0, opa.cb, lane);
+      KT += adapters.tiles;
+#pragma unroll
+      for (int k = 1; k < PRO; ++k)
+        if (k >= KTA && k < KT) issue_tile(k);
+    }
     if constexpr (S == 2) {
-      issue_tile(0);
+      if constexpr (!CF::ADAPTERS) issue_tile(0);
       if (1 < KT) {
-        issue_tile(1);
+        if constexpr (!CF::ADAPTERS) issue_tile(1);
         wait_vmcnt<NQ_STAGE>();
       } else {
         wait_vmcnt<0>();
@@ -1290,7 +1299,7 @@ __device__ __forceinline__ void gemm_epi_body(const typename CF::params_t& p, ch
     } else {
 #pragma unroll
       for (int k = 0; k < S - 1; ++k)
-        if (k < KT) issue_tile(k);
+        if (!CF::ADAPTERS && k < KT) issue_tile(k);
       wait_pending(min(S - 1, KT) - 1);
       int t_pro = S - 1;
       asm("" : "+s"(t_pro));
