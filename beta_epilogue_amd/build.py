@@ -156,7 +156,8 @@ def build(verbose: bool = False, extra=(), only=None, cache_dir=None) -> str:
                   for k in range(GEMM_GROUPED_PARTS)]
         units += [obj("grouped_grad%d.o" % k, GROUPED_GRAD_SOURCE, grouped_deps, ["-DGEMM_GROUPED_GRAD_PART=%d" % k])
                   for k in range(GEMM_GROUPED_GRAD_PARTS)]
-        adapter_deps = linear_deps + [os.path.join(CSRC, "gemm_adapter.hpp")]
+        adapter_deps = linear_deps + [os.path.join(CSRC, f) for f in ("gemm_adapter.hpp", "gemm_grouped.hpp",
+                                                                       "gemm_experts.hpp")]
         units += [obj("adapter%d.o" % k, ADAPTER_PART_SOURCE, adapter_deps, ["-DGEMM_ADAPTER_PART=%d" % k])
                   for k in range(GEMM_ADAPTER_PARTS)]
         units += [obj(os.path.basename(f) + ".o", f, HEADERS) for f in LINEAR_SOURCES]

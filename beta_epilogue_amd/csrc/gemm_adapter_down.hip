@@ -43,14 +43,16 @@ __device__ __forceinline__ bool any_thread(bool v, int* red) {
 }
 
 // Whether part `block % kFiniteParts` of up[block / kFiniteParts] is finite; an
-// adapter that no row has is not read (and nobody asks).
+// adapter that no row has is not read (and nobody asks), unless it takes a pass over
+// many rows to know.
 template <int AB>
 __device__ __forceinline__ void finite_block(const AdapterDownParams& p, int block, int* red) {
   const int g = block / kFiniteParts, part = block % kFiniteParts, threads = blockDim.x;
-  bool met = false;
+  bool met = true;
   if (p.offsets) {
     met = p.offsets[g + 1] > p.offsets[g];
-  } else {
+  } else if (p.M * p.rank <= kAdapterDots) {
+    met = false;
     for (int64_t m = threadIdx.x; m < p.M; m += threads) met |= p.ids[m] == g;
     met = any_thread(met, red);
   }

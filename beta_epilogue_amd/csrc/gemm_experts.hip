@@ -39,7 +39,7 @@ int check_rows(const char* name, int64_t* ld, int64_t rows, int64_t cols, int ty
     return fail(GEMM_EPI_ERR_ALIGNMENT, "rows (%lld elements) and row strides (%lld) must be multiples of 16 bytes",
                 (long long)cols, (long long)*ld);
   // a thread for every 16 bytes of the tokens' rows
-  if (!mul_ok(cols * es / 16 + 1, rows, &n) || n >= int64_t(1) << 32)
+  if (!mul_ok(cols * es / 16 + 1, rows, &n) || n > (int64_t(1) << 32) - 256)
     return fail(GEMM_EPI_ERR_UNSUPPORTED, "%lld rows of %lld elements: more than a launch has threads for",
                 (long long)rows, (long long)cols);
   return GEMM_EPI_OK;

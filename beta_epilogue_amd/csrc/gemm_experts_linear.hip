@@ -523,7 +523,6 @@ extern "C" int gemm_epi_expert_linear_grad_run(const gemm_epi_expert_linear_grad
   p.sum_rows = dbias && h->sum_rows ? dD : nullptr;
   p.partial = (const float*)workspace;
   p.chunk = (int32_t)h->chunk;
-  p.slots = (int32_t)h->slots;
   p.dbias = dbias;
   p.dbias_dtype = d.dbias_dtype;
   p.N = d.N;

@@ -70,10 +70,13 @@ __device__ __forceinline__ int group_k_item(const GroupParams& p, int bid) {
 
 // The table of groups in LDS: first[g] = tiles of `rows` rows in the groups
 // before g (first[groups]: in all, returned).  All threads of the workgroup.
+// Offsets that do not ascend could count rows more than once; there are never more
+// tiles than the worst distribution has, which is what the host made sure of.
 constexpr int kGroupTableBytes = (kMaxExperts + 1) * 4 + 12;
 __device__ __forceinline__ int group_table_rows(const GroupParams& p, int* first, int rows) {
   const int lane = __lane_id();
   if (threadIdx.x < 64) {
+    const int n0 = min(p.rows, p.groups), most = n0 + (p.rows - n0) / rows;
     int before = 0;
     for (int base = 0; base < p.groups; base += 64) {
       const int g = base + lane;
@@ -82,9 +85,10 @@ __device__ __forceinline__ int group_table_rows(const GroupParams& p, int* first
         const GroupTile t = group_rows(p, g);
         n = (t.end - t.begin + rows - 1) / rows;
       }
-      const int sum = wave_scan(n, lane);
-      if (g < p.groups) first[g] = before + sum - n;
-      before += __shfl(sum, 63);
+      // (unsigned: 64 groups of up to 2^25 tiles)
+      const uint32_t sum = (uint32_t)before + (uint32_t)wave_scan(n, lane);
+      if (g < p.groups) first[g] = (int)min(sum - (uint32_t)n, (uint32_t)most);
+      before = (int)min((uint32_t)__shfl((int)sum, 63), (uint32_t)most);
     }
     if (lane == 0) first[p.groups] = before;
   }
@@ -167,7 +171,7 @@ struct GroupGradParams {
   int32_t b_first;
   const void* sum_rows;   // dD, whose rows dbias adds up; NULL: the chunks' sums
   const float* partial;   // [chunk][N]
-  int32_t chunk, slots;   // rows of a chunk, chunks that partial holds
+  int32_t chunk;          // rows of a chunk
   void* dbias;            // groups x N
   int32_t dbias_dtype;
   int64_t N;

@@ -54,9 +54,8 @@ __device__ __forceinline__ void group_sums(const GroupGradParams& p, int block, 
   const int64_t n = (int64_t)(block - g * per) * 256 + threadIdx.x;
   if (n >= p.N) return;
   float s = 0.0f;
-  const int last = min(first[g + 1], p.slots);  // (offsets that do not ascend could have more)
 #pragma unroll 8
-  for (int c = first[g]; c < last; ++c) s += p.partial[c * p.N + n];
+  for (int c = first[g]; c < first[g + 1]; ++c) s += p.partial[c * p.N + n];
   store_as(p.dbias, g * p.N + n, p.dbias_dtype, s);
 }
 

@@ -126,6 +126,14 @@ def test_ranks(M, rank):
     run(M, 136, 328, rank, 200, kind="mixed")
 
 
+@pytest.mark.parametrize("rank,G", [(16, 2), (24, 1), (32, 2), (64, 2), (128, 2)])
+@pytest.mark.parametrize("kind", ["mixed", "runs", "none"])
+def test_up_to_two_adapters(rank, G, kind):
+    """Their rows are not sorted."""
+    run(701, 264, 520, rank, G, kind=kind, seed=rank)
+    run(1040, 72, 2056, rank, G, "f16", kind=kind, seed=rank + 1)
+
+
 @pytest.mark.parametrize("M,N,K", [(65, 8, 8), (65, 264, 16), (257, 520, 1032), (1001, 256, 40), (300, 2552, 24),
                                    (65, 16, 8200), (2100, 64, 4104)])
 @pytest.mark.parametrize("kind", ["mixed", "runs"])

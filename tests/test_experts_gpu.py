@@ -254,7 +254,7 @@ def test_streams_and_graphs():
     """Two streams at once and two graphs replayed in turn give what one call
     gives, with rows of their own and a workspace each."""
     g = torch.Generator().manual_seed(8)
-    T, k, E, cols = 3000, 4, 40, 256  # two chunks of the sort
+    T, k, E, cols = 3000, 4, 40, 256  # three chunks of the sort
     ids = _ids(g, T, k, E).cuda()
     X, w = _draw(g, T, cols, torch.bfloat16).cuda(), torch.rand(T, k, generator=g).cuda()
     sort, back = ge.ExpertSort(T, k, E, cols=cols), ge.ExpertCombine(T, k, cols)

@@ -296,6 +296,24 @@ def test_grad_parts():
     run_grad(100, 3, 64, 48, "f16", "none", mul=True, da="f16")
 
 
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("tile", [64, 128, 256])
+def test_grad_of_offsets_outside_the_batch(tile, act):
+    """As in the forward: nothing outside the tensors is touched."""
+    R, E, N, K = 40, 4, 64, 72
+    T = torch.bfloat16
+    x = lambda *s: torch.ones(*s, dtype=T, device="cuda")  # noqa: E731
+    dD, A, B = x(R, N), x(R, K), x(E, N, K)
+    for off in ([-5, 10, 20, 1000, 2000], [0, 30, 10, 1 << 30, -(1 << 31)], [7] + [(1 << 31) - 1, 0] * 2):
+        dA, dB, dbias, dZ = Out(R, K, T), Out(E * N, K, T), Out(E, N, T), Out(R, N, T)
+        _say("case gradients of offsets", off, tile, act)
+        op = ge.ExpertLinearGrad(R, E, N, K, act=act, da="bf16", db="bf16", dbias="bf16", tile=tile)
+        z = dict(Z=dD, dZ=dZ.t) if act != "none" else {}
+        op(dD, A, B, torch.tensor(off, dtype=torch.int32, device="cuda"), dA=dA.t, dB=dB.t.view(E, N, K), dbias=dbias.t, **z)
+        torch.cuda.synchronize()
+        assert dA.intact() and dB.intact() and dbias.intact() and dZ.intact()
+
+
 @pytest.mark.parametrize("alias", ["dD", "Z"])
 def test_grad_in_place(alias):
     run_grad(200, 3, 72, 64, "bf16", "gelu_tanh", mul=True, da="bf16", db="f32", dbias="f32", db_in=True, alias=alias)
