@@ -45,8 +45,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t adapter_up(const AdapterParams
 // adapters that the tile's rows have add K tiles to the tile's, staged and
 // multiplied by the same loop: A's rows are U's, zero for rows of other adapters,
 // B's are up[g]'s.  A K tile of 64 holds as many adapters as fit (rank 16: four).
-// Packed prompts have one or two adapters per tile (4001 x 4096 x 4096, rank 64: 112 us
-// of a plain projection's 95 to 101); a batch of single tokens has up to one per row
+// Packed prompts have one or two adapters per tile (4001 x 4096 x 4096, rank 64: 112 us,
+// a plain projection 95 to 101); a batch of single tokens has up to one per row
 // (256 rows of 48 adapters, rank 16: 34 us with both launches).
 //
 // A zero times an infinity or a NaN in up[g] would reach the other rows, so an
@@ -200,8 +200,10 @@ struct AdapterDownParams {
   int32_t rank, adapters;
 };
 // Up to so many products (rows times rank) a wave makes each by itself; of more the
-// rows are sorted by adapter first, where there are more than two.
-constexpr int64_t kAdapterDots = 8192;
+// rows are sorted by adapter first, where there are more than two.  (256 rows of rank
+// 64, 4096 x 4096, 4 adapters, in all: 37.5 against 38.8 us; 1024 of rank 32, 8 adapters:
+// 77.6 against 68.1.)
+constexpr int64_t kAdapterDots = 16384;
 inline bool adapter_sorted(int64_t M, int rank, int adapters) { return M * rank > kAdapterDots && adapters > 2; }
 void launch_adapter_down(int ab, const AdapterDownParams& p, hipStream_t s);
 

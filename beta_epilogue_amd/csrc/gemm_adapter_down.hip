@@ -1,7 +1,7 @@
 // gemm_adapter_down.hip -- the rows' inner products with their own adapters:
 //   U[m][j] = scale[g] sum_k A[m][k] down[g][j][k],  g = ids[m].
 //
-// Few rows (M * rank up to 8192): a wave takes one product of one row, so rows of
+// Few rows (kAdapterDots): a wave takes one product of one row, so rows of
 // as many adapters cost the same, and every weight is read once per row that has
 // it, from the cache but for the first time.
 //
@@ -153,21 +153,23 @@ __global__ __launch_bounds__(NW * 64) void adapter_down_kernel(AdapterDownParams
   }
 }
 
+// Workgroups that look at up.
+int looks(const AdapterDownParams& p) { return p.finite ? p.adapters * kFiniteParts : 0; }
+
 template <int AB, int MB, int NW, int NS>
 void down(const AdapterDownParams& p, hipStream_t s) {
   // chunks; sorted: of the worst distribution
   const int64_t n = p.M < p.adapters ? p.M : p.adapters;
   const int blocks = (int)(p.order ? n + (p.M - n) / 16 : (p.M + 15) / 16), per = (p.rank + 63) / 64;
-  hipLaunchKernelGGL((adapter_down_kernel<AB, MB, NW, NS>), dim3((unsigned)(blocks * per + p.adapters * kFiniteParts)),
-                     dim3(NW * 64), 0, s, p, blocks, per);
+  hipLaunchKernelGGL((adapter_down_kernel<AB, MB, NW, NS>), dim3((unsigned)(blocks * per + looks(p))), dim3(NW * 64), 0, s, p,
+                     blocks, per);
 }
 
 template <int AB>
 void launch(const AdapterDownParams& p, hipStream_t s) {
   if (p.M * p.rank <= kAdapterDots) {
     const int blocks = (int)(p.M * p.rank / 4);
-    hipLaunchKernelGGL(adapter_dots_kernel<AB>, dim3((unsigned)(blocks + (p.finite ? p.adapters * kFiniteParts : 0))), dim3(256),
-                       0, s, p, blocks);
+    hipLaunchKernelGGL(adapter_dots_kernel<AB>, dim3((unsigned)(blocks + looks(p))), dim3(256), 0, s, p, blocks);
     return;
   }
   if (p.order) {

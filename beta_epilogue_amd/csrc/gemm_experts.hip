@@ -61,7 +61,7 @@ int finish(const D& d, H** out) {
   int device = 0, cus = 0;
   const int rc = device_query(&device, &cus);
   if (rc) return rc;
-  *out = new (std::nothrow) H{d, device, cus};
+  *out = new (std::nothrow) H{d, device};
   return *out ? GEMM_EPI_OK : fail(GEMM_EPI_ERR_HOST_ALLOC, "out of host memory");
 }
 
@@ -72,7 +72,7 @@ int finish(const D& d, H** out) {
 // ---------------------------------------------------------------------------
 struct gemm_epi_expert_sort_handle {
   gemm_epi_expert_sort_desc d;  // strides filled in
-  int device, cus;
+  int device;
   int64_t chunks() const { return sort_chunks(d.tokens * d.top_k); }
   int64_t ws() const { return chunks() > 1 ? chunks() * d.experts * 4 : 0; }
 };
@@ -168,7 +168,7 @@ extern "C" int64_t gemm_epi_expert_sort_workspace(const gemm_epi_expert_sort_han
 // ---------------------------------------------------------------------------
 struct gemm_epi_expert_combine_handle {
   gemm_epi_expert_combine_desc d;  // strides filled in
-  int device, cus;
+  int device;
 };
 
 extern "C" int gemm_epi_expert_combine_create(const gemm_epi_expert_combine_desc* desc,
@@ -234,7 +234,7 @@ extern "C" int gemm_epi_expert_combine_destroy(gemm_epi_expert_combine_handle* h
 
 struct gemm_epi_expert_combine_grad_handle {
   gemm_epi_expert_combine_grad_desc d;  // strides filled in
-  int device, cus;
+  int device;
 };
 
 extern "C" int gemm_epi_expert_combine_grad_create(const gemm_epi_expert_combine_grad_desc* desc,
@@ -291,7 +291,7 @@ extern "C" int gemm_epi_expert_combine_grad_run(const gemm_epi_expert_combine_gr
   p.ldg = d.ldg;
   p.top_k = d.top_k;
   (void)hipGetLastError();
-  launch_expert_combine_grad(d.x_dtype, p, h->cus, (hipStream_t)stream);
+  launch_expert_combine_grad(d.x_dtype, p, (hipStream_t)stream);
   return launched();
 }
 

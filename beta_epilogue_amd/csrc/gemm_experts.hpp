@@ -47,6 +47,6 @@ struct CombineParams {
 };
 // t: T_F16, T_BF16 or T_F32.
 void launch_expert_combine(int t, const CombineParams& p, hipStream_t s);
-void launch_expert_combine_grad(int t, const CombineParams& p, int cus, hipStream_t s);
+void launch_expert_combine_grad(int t, const CombineParams& p, hipStream_t s);
 
 }  // namespace gemm_epi

@@ -351,6 +351,8 @@ struct gemm_epi_expert_linear_grad_handle {
   int64_t ws_bytes;
   // without an activation and mul dbias adds up dD's rows beside the products, in
   // workgroups of 64 columns and all rows of an expert: where those are not too many
+  // (8192 of each expert, 8 experts, 512 x 512: 104 against 121 us with a pass of its
+  // own; 16384, 2 experts, 256 x 512: 85 against 77)
   bool sum_rows;
   bool pass() const { return has_z() || (d.dbias_dtype != GEMM_EPI_NONE && !sum_rows); }
   bool has_z() const { return d.act != GEMM_EPI_ACT_NONE || d.mul; }
@@ -406,7 +408,7 @@ extern "C" int gemm_epi_expert_linear_grad_create(const gemm_epi_expert_linear_g
   const int64_t tn = (d.N + h.tile - 1) / h.tile, tk = (d.K + h.tile - 1) / h.tile;
   h.ga = d.da_dtype != GEMM_EPI_NONE ? worst_chunks(d.rows, d.experts, h.tile) * tk : 0;
   h.gb = d.db_dtype != GEMM_EPI_NONE ? 8 * d.experts * ((tn * tk + 7) / 8) : 0;
-  h.sum_rows = !h.has_z() && h.ga + h.gb > 0 && d.rows / d.experts <= 4096;
+  h.sum_rows = !h.has_z() && h.ga + h.gb > 0 && d.rows / d.experts <= 8192;
   const int64_t columns = h.sum_rows ? 64 : 256;
   h.sums = d.dbias_dtype != GEMM_EPI_NONE ? d.experts * ((d.N + columns - 1) / columns) : 0;
   // 256 threads for each, fewer than 2^32 in all

@@ -1,6 +1,13 @@
 // gemm_grouped_part.hip -- compiles the tile kernels of
 // gemm_grouped_variants.inc whose `part` equals GEMM_GROUPED_PART (the build
 // compiles this file once per part, in parallel).
+//
+// The linear layer's main loop and epilogue (gemm_epi_kernel.hpp) with each tile's rows
+// ending at its expert's end.  Bound by the MFMAs where experts have hundreds of rows:
+// 16384 rows of 8 experts, bf16, N 4096, K 2048, silu, U and Z, 309 us (890 TFLOP/s;
+// the epilogue is 13 of a tile's 55 us, with nothing to hide behind), and by the weights'
+// bytes below that: 2048 rows of 64 experts, e4m3, 1536 x 2048, 48 us (4.3 TB/s) in
+// 64x64 tiles.
 #include "gemm_grouped.hpp"
 
 #ifndef GEMM_GROUPED_PART

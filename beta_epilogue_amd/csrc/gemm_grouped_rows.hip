@@ -1,7 +1,9 @@
 // gemm_grouped_rows.hip -- the experts' linear layer with few rows per expert
 // (decoding): the few-row kernel (gemm_linear_rows.hip) on chunks of an expert's
 // rows.  The time is the weights' of the experts that have rows; a workgroup
-// streams 16 weight rows of one of them past a chunk of up to 4 * MB of its rows.
+// streams 16 weight rows of one of them past a chunk of up to 4 * MB of its rows
+// (8 rows of 8 experts, bf16, 512 x 4096: 8.7 us, in 64x64 tiles 15.6; 1536 x 2048: 14.3
+// and 15.0).
 #include "gemm_grouped.hpp"
 #include "gemm_linear_rows.hpp"
 
