@@ -319,6 +319,12 @@ def test_grad_in_place(alias):
     run_grad(200, 3, 72, 64, "bf16", "gelu_tanh", mul=True, da="bf16", db="f32", dbias="f32", db_in=True, alias=alias)
 
 
+@pytest.mark.parametrize("kind", ["one", "none"])
+@pytest.mark.parametrize("db", ["f32", "bf16"])
+def test_grad_in_place_without_rows(db, kind):
+    run_grad(90, 5, 72, 200, "bf16", "silu", da="bf16", db=db, db_in=True, alias="dD", kind=kind)
+
+
 @pytest.mark.parametrize("act", ["none", "silu", "gelu"])
 def test_grad_against_differences(act):
     """Central differences of f = sum(dD * act(A B[e]^T + shift) * U) in 64 bits
