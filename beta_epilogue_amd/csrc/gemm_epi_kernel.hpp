@@ -1005,22 +1005,21 @@ struct GroupTile {
 template <class CF>
 struct AdapterTiles;
 
-// What a workgroup does of a GROUP_ROWS problem: items begin .. end - 1, of the
-// table of groups `first` (in LDS).  quarter: an item is a quarter of a tile of
+// What a workgroup does of a GROUP_K problem: item `begin`, of a group with rows.  Of a
+// GROUP_ROWS problem: items begin .. end - 1, of the table of groups `first` (in LDS).  quarter: an item is a quarter of a tile of
 // twice the height and width, which the table counts.
 struct GroupWork {
   const int* first;
   int begin, end, quarter;
+  int row, rows_end;  // GROUP_K: its group's rows
 };
 __device__ GroupTile group_of_tile(const GroupParams& p, const int* first, int row_tile);
-__device__ GroupTile group_rows(const GroupParams& p, int group);
-__device__ int group_k_item(const GroupParams& p, int bid);
 
 // ---------------------------------------------------------------------------
 // The kernel
 // ---------------------------------------------------------------------------
 // The work of workgroup `bid` of `G` that share a problem, with the LDS array
-// `lds` of CF::LDS_BYTES (1 KiB aligned).  GROUP_ROWS: its share of `work`.
+// `lds` of CF::LDS_BYTES (1 KiB aligned).  GROUP_ROWS: its share of `work`; GROUP_K: `work`.
 template <class CF>
 __device__ __forceinline__ void gemm_epi_body(const typename CF::params_t& p, char* lds, int bid, int G,
                                               GroupWork work = {}) {
@@ -1048,7 +1047,7 @@ __device__ __forceinline__ void gemm_epi_body(const typename CF::params_t& p, ch
   int g = p.xcd_remap ? (bid & 7) * (G >> 3) + over + (bid >> 3) : bid;
   int tiles_total = p.tiles_total;
   if constexpr (CF::GROUP == GROUP_ROWS) g += work.begin, tiles_total = work.end;
-  if constexpr (CF::GROUP == GROUP_K) g = group_k_item(p, bid);
+  if constexpr (CF::GROUP == GROUP_K) g = work.begin;
 
   using OpA = Operand<CF, BM, CF::WM, CF::A_KMAJOR>;
   using OpB = Operand<CF, BN, CF::WN, CF::B_KMAJOR>;
@@ -1085,15 +1084,13 @@ __device__ __forceinline__ void gemm_epi_body(const typename CF::params_t& p, ch
     const TileRC tc = raster_tile(ts, tiles_m, p.tiles_n, p.group_m);
     const int l = tc.l;
     if constexpr (CF::GROUP == GROUP_K) {
-      gt = group_rows(p, l);
-      gt.begin = __builtin_amdgcn_readfirstlane(gt.begin);
-      gt.end = __builtin_amdgcn_readfirstlane(gt.end);
+      gt.begin = work.row;
+      gt.end = work.rows_end;
     }
     const int64_t kbeg = split > 0 ? (int64_t)split * p.kslice : 0;
     const int64_t K = CF::GROUP == GROUP_K ? (int64_t)(gt.end - gt.begin) : p.K;
     const int64_t kbytes = (split < 0 ? K : min(K - kbeg, p.kslice)) * ES;  // this item's K, in bytes
     int KT = (int)((kbytes + CF::ROWB - 1) / CF::ROWB);
-    if constexpr (CF::GROUP == GROUP_K) KT = max(KT, 1);  // (a group without rows: one K tile of zeros)
     [[maybe_unused]] const int KTA = KT;  // K tiles of A and B
     int m0 = tc.tm * BM, n0 = tc.tn * BN;
     if constexpr (CF::GROUP == GROUP_ROWS) {
@@ -1109,7 +1106,6 @@ __device__ __forceinline__ void gemm_epi_body(const typename CF::params_t& p, ch
     } else if constexpr (CF::GROUP == GROUP_K) {
       opa.setup((const char*)p.A + gt.begin * p.M * ES, p.M, K, 0, m0, wave, lane);
       opb.setup((const char*)p.B + gt.begin * p.N * ES, p.N, K, 0, n0, wave, lane);
-      if (K == 0) opa.rsrc[2] = opb.rsrc[2] = 0;
     } else if constexpr (CF::LIN) {
       // a K-major operand's row stride stands for its row length: chunks past
       // K are masked by the K tile's guard, not by the extent

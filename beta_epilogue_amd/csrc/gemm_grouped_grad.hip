@@ -62,12 +62,11 @@ __device__ __forceinline__ void group_sums(const GroupGradParams& p, int block, 
 
 // dB[e] of an expert without rows is dB_in[e] or zero: each of the expert's items
 // copies its share, straight from and to memory (one token, 6 of 28 experts, 3856 x 896
-// bf16, 193 MB: 180 us as 64x64 tiles of a K tile of zeros, 59 in 128x128 ones so).  False:
-// the item's expert has rows.
-__device__ __forceinline__ bool fill_without_rows(const GroupParams& p, int item) {
-  const int tiles = p.tiles_m * p.tiles_n, e = item / tiles;
-  const GroupTile t = group_rows(p, e);
-  if (t.end > t.begin) return false;
+// bf16, 193 MB: 46 us, as tiles with a K tile of zeros 180).  False: the item's expert has
+// rows.
+__device__ __forceinline__ bool fill_without_rows(const GroupParams& p, const GroupWork& w) {
+  if (w.rows_end > w.row) return false;
+  const int item = w.begin, tiles = p.tiles_m * p.tiles_n, e = item / tiles;
   if (p.R == p.D) return true;
   const int64_t n = p.M * p.N << epi_shift(p.d_dtype) >> 4, share = (n + tiles - 1) / tiles;  // 16-byte pieces
   const int64_t begin = (item - e * tiles) * share, end = min(begin + share, n);
@@ -91,9 +90,9 @@ __global__ __launch_bounds__(256, grad_occ(KIND)) void grouped_grad_kernel(Group
     const int total = group_table_rows(p.a, first, CA::BM) * p.a.tiles_n;
     gemm_epi_body<CA>(p.a, lds, bid - a0, p.ga, GroupWork{first, 0, total, 0});
   } else if (bid < p.gb + p.ga) {
-    const int item = group_k_item(p.b, bid - b0);
-    if (item < p.b.tiles_total && fill_without_rows(p.b, item)) return;
-    gemm_epi_body<CB>(p.b, lds, bid - b0, p.gb);
+    const GroupWork w = group_k_item(p.b, bid - b0);
+    if (w.begin >= p.b.tiles_total || fill_without_rows(p.b, w)) return;
+    gemm_epi_body<CB>(p.b, lds, bid - b0, p.gb, w);
   } else if (p.sum_rows) {
     group_row_sums<AB>(p, bid - p.gb - p.ga, (float*)lds);
   } else {
