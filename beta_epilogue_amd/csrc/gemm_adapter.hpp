@@ -96,7 +96,7 @@ struct AdapterTiles {
     __syncthreads();
     if (t < 64) {
       uint32_t word = t < BITS ? (uint32_t)bits[t] : 0u;
-      const int n = __popc(word), sum = wave_scan(n, lane);
+      const int n = __popc(word), sum = wave_scan(n);
       for (int i = sum - n; word; ++i, word &= word - 1) list[i] = t * 32 + __ffs(word) - 1;
       if (t == 63) count[0] = sum;
     }

@@ -17,6 +17,19 @@ inline int64_t sort_chunks(int64_t choices) {
   return choices <= 2 * kSortChunk ? 1 : (choices + kSortChunk - 1) / kSortChunk;
 }
 
+// The sum of v over this lane and those before it; every lane of the wave calls.
+// Shifts inside rows of 16 lanes, then the rows' totals: register to register, for it
+// stands at the start of every workgroup that looks for its expert.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // lane 15 to row 1, 47 to row 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // lane 31 to rows 2 and 3
+  return v;
+}
+
 struct SortParams {
   const void* ids;       // choices x int32 or int64
   const void* X;         // rows to move, or NULL

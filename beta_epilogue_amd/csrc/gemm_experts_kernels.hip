@@ -122,12 +122,7 @@ __global__ __launch_bounds__(kSortThreads) void expert_rank_kernel(SortParams p)
     }
   }
   // an exclusive sum over the experts
-  int sum = all;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(sum, d);
-    sum += lane >= d ? o : 0;
-  }
+  const int sum = wave_scan(all);
   if (lane == 63) s.wave_sum[wave] = sum;
   __syncthreads();
   int first = sum - all;

@@ -35,15 +35,6 @@ __device__ __forceinline__ GroupTile group_rows(const GroupParams& p, int group)
   return t;
 }
 
-__device__ __forceinline__ int wave_scan(int v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(v, d);
-    v += lane >= d ? o : 0;
-  }
-  return v;
-}
-
 // GROUP_K: the item (tile of a group's output) of workgroup bid of 8 * groups *
 // ceil(tiles / 8), tiles_total for none, and the group's rows.  Workgroups go round
 // the 8 XCDs, and a group with many rows has long items: every group's tiles are
@@ -101,9 +92,9 @@ __device__ __forceinline__ int group_table_rows(const GroupParams& p, int* first
         n = (t.end - t.begin + rows - 1) / rows;
       }
       // (unsigned: 64 groups of up to 2^25 tiles)
-      const uint32_t sum = (uint32_t)before + (uint32_t)wave_scan(n, lane);
+      const uint32_t sum = (uint32_t)before + (uint32_t)wave_scan(n);
       if (g < p.groups) first[g] = (int)min(sum - (uint32_t)n, (uint32_t)most);
-      before = (int)min((uint32_t)__shfl((int)sum, 63), (uint32_t)most);
+      before = (int)min((uint32_t)__builtin_amdgcn_readlane((int)sum, 63), (uint32_t)most);
     }
     if (lane == 0) first[p.groups] = before;
   }
@@ -139,19 +130,19 @@ __device__ __forceinline__ GroupTile group_chunk(const GroupParams& p, int slot,
     GroupTile t = {};
     if (g < p.groups) t = group_rows(p, g);
     const int n = (t.end - t.begin + rows - 1) / rows;
-    const int sum = before + wave_scan(n, lane);  // chunks of this group and those before
+    const int sum = before + wave_scan(n);  // chunks of this group and those before
     const uint64_t behind = __ballot(sum > slot);
     if (behind) {
       const int l = __ffsll((unsigned long long)behind) - 1;
       GroupTile r = {};
       r.group = base + l;
-      const int begin = __builtin_amdgcn_readfirstlane(__shfl(t.begin, l)), end = __builtin_amdgcn_readfirstlane(__shfl(t.end, l));
-      const int c = slot - __builtin_amdgcn_readfirstlane(__shfl(sum - n, l));
+      const int begin = __builtin_amdgcn_readlane(t.begin, l), end = __builtin_amdgcn_readlane(t.end, l);
+      const int c = slot - __builtin_amdgcn_readlane(sum - n, l);
       r.begin = begin + c * rows;
       r.end = min(end, r.begin + rows);
       return r;
     }
-    before = __builtin_amdgcn_readfirstlane(__shfl(sum, 63));
+    before = __builtin_amdgcn_readlane(sum, 63);
   }
   GroupTile none = {};
   none.group = -1;
