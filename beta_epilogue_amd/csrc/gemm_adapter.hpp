@@ -66,8 +66,9 @@ struct AdapterTiles {
   uint32_t k;       // and which byte of the rank (past it: at least 2 * rank)
   int shift;        // adapters in a K tile: 1 << shift; -1: two K tiles for one
   uint32_t bytes;   // of a row of U and of up
-  int cur;          // the adapter being staged
-  uint32_t at;      // its byte in up
+  int listed;       // adapters in the list
+  uint32_t at;      // the byte in up of the adapter being staged, 0x80000000: none
+  uint32_t mine;    // bit Q: the row that instruction Q stages has it
 
   static __device__ __forceinline__ int* ids(char* lds) { return (int*)(lds + CF::LDS_BYTES); }
 
@@ -101,15 +102,15 @@ struct AdapterTiles {
       if (t == 63) count[0] = sum;
     }
     __syncthreads();
-    const int n = __builtin_amdgcn_readfirstlane(count[0]);
+    listed = __builtin_amdgcn_readfirstlane(count[0]);
     apart = __builtin_amdgcn_readfirstlane(count[1]) != 0;
     bytes = (uint32_t)p.rank * 2;
     shift = p.rank <= 8 ? 3 : p.rank <= 16 ? 2 : p.rank <= 32 ? 1 : p.rank <= 64 ? 0 : -1;
-    tiles = shift < 0 ? 2 * n : (n + (1 << shift) - 1) >> shift;
+    tiles = shift < 0 ? 2 * listed : (listed + (1 << shift) - 1) >> shift;
     slot = shift < 0 ? 0 : (int)(cb >> (7 - shift));
     k = shift < 0 ? cb : cb & (127u >> shift);
-    cur = -1;
-    at = 0;
+    at = 0x80000000u;
+    mine = 0;
   }
 
   // The row that this lane stages by instruction Q.
@@ -118,27 +119,32 @@ struct AdapterTiles {
     const int lane = __lane_id(), wave = threadIdx.x >> 6;
     return (uint32_t)((Q * CF::NW + wave) * CF::ROWS_PER_DMA + lane / CF::CH);
   }
-  // Instruction Q of K tile t (a K tile's instructions are issued in order, the rows' first).
+  // Instruction Q of K tile t (a K tile's instructions are issued in order, the rows'
+  // first).  The rows' adapters are looked up together, for one wait for LDS between
+  // the MFMAs (4001 x 4096 x 4096, rank 64: 136.5 us in all with one each, 134.4 so).
   template <int Q>
   __device__ __forceinline__ void issue_rows(const AdapterParams& p, char* lds, uint32_t sbase, int t) {
+    const uint32_t kk = k + (shift < 0 && (t & 1) ? 128u : 0u);
     if constexpr (Q == 0) {
       const int a = shift < 0 ? t >> 1 : (t << shift) + slot;
-      const int n = ids(lds)[2 * CF::BM + BITS];
-      cur = a < n ? ids(lds)[CF::BM + a] : -1;
-      const uint32_t kk = k + (shift < 0 && (t & 1) ? 128u : 0u);
-      if (kk >= bytes) cur = -1;
-      at = (uint32_t)cur * (uint32_t)p.N * bytes + kk;
+      const bool any = a < listed && kk < bytes;
+      const int cur = any ? ids(lds)[CF::BM + a] : -2;
+      mine = 0;
+      static_for<0, CF::BM / (CF::NW * CF::ROWS_PER_DMA)>([&](auto q_c) {
+        constexpr int q = decltype(q_c)::value;
+        mine |= ids(lds)[stage_row<q>()] == cur ? 1u << q : 0u;
+      });
+      at = any ? (uint32_t)cur * (uint32_t)p.N * bytes + kk : 0x80000000u;
     }
     const v4i ru = make_rsrc((const char*)p.U + (int64_t)m0 * bytes, (uint32_t)min((int64_t)CF::BM, p.M - m0) * bytes);
-    const uint32_t row = stage_row<Q>(), kk = k + (shift < 0 && (t & 1) ? 128u : 0u);
-    dma16s<(uint32_t)Q * CF::NW * 1024u>(ru, sbase, cur >= 0 && ids(lds)[row] == cur ? row * bytes + kk : 0x80000000u, 0);
+    dma16s<(uint32_t)Q * CF::NW * 1024u>(ru, sbase, mine >> Q & 1 ? stage_row<Q>() * bytes + kk : 0x80000000u, 0);
   }
   template <int Q>
   __device__ __forceinline__ void issue_columns(const AdapterParams& p, uint32_t sbase) {
     const int64_t first = (int64_t)n0 * bytes;
     const v4i rp = make_rsrc((const char*)p.up + first, (uint32_t)((int64_t)p.adapters * p.N * bytes - first));
     // (columns past the matrix get something else's weights, and are never stored)
-    dma16s<(uint32_t)Q * CF::NW * 1024u>(rp, sbase, cur >= 0 ? at + stage_row<Q>() * bytes : 0x80000000u, 0);
+    dma16s<(uint32_t)Q * CF::NW * 1024u>(rp, sbase, at != 0x80000000u ? at + stage_row<Q>() * bytes : 0x80000000u, 0);
   }
 
   // Adds what was left out to a wave's accumulators (rows mw .., columns nw ..):
