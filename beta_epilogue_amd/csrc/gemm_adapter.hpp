@@ -18,11 +18,12 @@ struct AdapterParams : LinParams {
   const void* U;          // M x rank
   const void* up;         // adapters x N x rank
   const int32_t* ids;     // M
-  const int32_t* finite;  // adapters x kFiniteParts: 1 where that part of up[g] is finite
+  const uint32_t* finite; // adapters: a byte for each part of up[g], 1 where it is finite
   int32_t rank, adapters;
 };
 
 constexpr int kFiniteParts = 4;
+constexpr uint32_t kFinite = 0x01010101u;  // all of them
 constexpr int kMaxRank = 128;
 
 // The adapter of row m; -1: none, or no such row.
@@ -56,9 +57,11 @@ template <class CF>
 struct AdapterTiles {
   using MM = typename CF::MM;
   static_assert(CF::BLK == 16 && MM::KSB == 64 && CF::ROWB == 128 && CF::BM <= CF::THREADS, "16-bit operands, 16x16 blocks");
-  // behind the ring: the rows' adapters, a list of them, a bit for each, counts
-  static constexpr int BITS = kMaxExperts / 32;
-  static constexpr int LDS_BYTES = (2 * CF::BM + BITS + 4) * 4;
+  // behind the ring, in words: the rows' ids, the adapters' finite words, the rows'
+  // adapters, a list of them, a bit for each, counts
+  static constexpr int BITS = kMaxExperts / 32, FINITE = CF::BM, ROW = FINITE + kMaxExperts, LIST = ROW + CF::BM,
+                       SEEN = LIST + CF::BM, COUNT = SEEN + BITS;
+  static constexpr int LDS_BYTES = (COUNT + 4) * 4;
   int tiles;        // K tiles
   bool apart;       // some row's adapter is not finite
   int m0, n0;       // the tile's first row and column
@@ -70,40 +73,62 @@ struct AdapterTiles {
   uint32_t at;      // the byte in up of the adapter being staged, 0x80000000: none
   uint32_t mine;    // bit Q: the row that instruction Q stages has it
 
-  static __device__ __forceinline__ int* ids(char* lds) { return (int*)(lds + CF::LDS_BYTES); }
+  static __device__ __forceinline__ int* words(char* lds) { return (int*)(lds + CF::LDS_BYTES); }
 
-  // on: this item adds them at all (one K slice of a tile does); cb: the byte of K
-  // that this lane stages
-  __device__ __forceinline__ void setup(const AdapterParams& p, char* lds, int row0, int column0, bool on, uint32_t cb,
-                                        int lane) {
+  // 64 words from byte `from` of r to byte `to` of LDS.
+  static __device__ __forceinline__ void fetch64(v4i r, uint32_t from, uint32_t to, int lane) {
+    asm volatile(
+        "s_mov_b32 m0, %0\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dword %1, %2, 0 offen lds"
+        :
+        : "s"(to), "v"(from + 4u * (uint32_t)lane), "s"(r)
+        : "memory", "m0");
+  }
+  // Starts to load what `setup` looks at, ahead of the tile's first loads, whose
+  // latency is then behind that of these.  on: this item adds adapters at all (one K
+  // slice of a tile does).
+  __device__ __forceinline__ void fetch(const AdapterParams& p, char* lds, int row0, bool on, int wave, int lane) {
     m0 = row0;
-    n0 = column0;
     tiles = 0;
     apart = false;
     if (!on) return;
-    int *id = ids(lds), *list = id + CF::BM, *bits = list + CF::BM, *count = bits + BITS;
+    const uint32_t at = (uint32_t)(uintptr_t)(lds_void_t*)words(lds);
+    const int rows = (int)min((int64_t)CF::BM, p.M - m0);
+    if (wave < CF::BM / 64)
+      fetch64(make_rsrc((const char*)(p.ids + m0), (uint32_t)rows * 4), (uint32_t)wave * 256, at + (uint32_t)wave * 256, lane);
+    const v4i rf = make_rsrc((const char*)p.finite, (uint32_t)p.adapters * 4);
+    for (int c = wave; c * 64 < p.adapters; c += CF::NW)
+      fetch64(rf, (uint32_t)c * 256, at + FINITE * 4 + (uint32_t)c * 256, lane);
+    if (threadIdx.x < BITS + 2) words(lds)[SEEN + threadIdx.x] = 0;
+  }
+
+  // After a wait for the loads of `fetch`.  cb: the byte of K that this lane stages.
+  __device__ __forceinline__ void setup(const AdapterParams& p, char* lds, int column0, bool on, uint32_t cb) {
+    n0 = column0;
+    if (!on) return;
+    int* w = words(lds);
     const int t = threadIdx.x;
-    if (t < BITS + 2) bits[t] = 0;
-    __syncthreads();
+    barrier_lds();
     if (t < CF::BM) {
-      int g = row_adapter(p, (int64_t)m0 + t);
+      int g = (int64_t)m0 + t < p.M ? w[t] : -1;
+      if (g < 0 || g >= p.adapters) g = -1;
       if (g >= 0) {
-        const v4i f = *(const v4i*)(p.finite + (int64_t)g * kFiniteParts);
-        if (f.x & f.y & f.z & f.w) atomicOr(&bits[g >> 5], 1 << (g & 31));
-        else g = -1, atomicOr(&count[1], 1);
+        if ((uint32_t)w[FINITE + g] == kFinite) atomicOr(&w[SEEN + (g >> 5)], 1 << (g & 31));
+        else g = -1, atomicOr(&w[COUNT + 1], 1);
       }
-      id[t] = g;
+      w[ROW + t] = g;
     }
-    __syncthreads();
+    barrier_lds();
     if (t < 64) {
-      uint32_t word = t < BITS ? (uint32_t)bits[t] : 0u;
+      uint32_t word = t < BITS ? (uint32_t)w[SEEN + t] : 0u;
       const int n = __popc(word), sum = wave_scan(n);
-      for (int i = sum - n; word; ++i, word &= word - 1) list[i] = t * 32 + __ffs(word) - 1;
-      if (t == 63) count[0] = sum;
+      for (int i = sum - n; word; ++i, word &= word - 1) w[LIST + i] = t * 32 + __ffs(word) - 1;
+      if (t == 63) w[COUNT] = sum;
     }
-    __syncthreads();
-    listed = __builtin_amdgcn_readfirstlane(count[0]);
-    apart = __builtin_amdgcn_readfirstlane(count[1]) != 0;
+    barrier_lds();
+    listed = __builtin_amdgcn_readfirstlane(w[COUNT]);
+    apart = __builtin_amdgcn_readfirstlane(w[COUNT + 1]) != 0;
     bytes = (uint32_t)p.rank * 2;
     shift = p.rank <= 8 ? 3 : p.rank <= 16 ? 2 : p.rank <= 32 ? 1 : p.rank <= 64 ? 0 : -1;
     tiles = shift < 0 ? 2 * listed : (listed + (1 << shift) - 1) >> shift;
@@ -128,11 +153,11 @@ struct AdapterTiles {
     if constexpr (Q == 0) {
       const int a = shift < 0 ? t >> 1 : (t << shift) + slot;
       const bool any = a < listed && kk < bytes;
-      const int cur = any ? ids(lds)[CF::BM + a] : -2;
+      const int cur = any ? words(lds)[LIST + a] : -2;
       mine = 0;
       static_for<0, CF::BM / (CF::NW * CF::ROWS_PER_DMA)>([&](auto q_c) {
         constexpr int q = decltype(q_c)::value;
-        mine |= ids(lds)[stage_row<q>()] == cur ? 1u << q : 0u;
+        mine |= words(lds)[ROW + stage_row<q>()] == cur ? 1u << q : 0u;
       });
       at = any ? (uint32_t)cur * (uint32_t)p.N * bytes + kk : 0x80000000u;
     }
@@ -159,10 +184,7 @@ struct AdapterTiles {
     static_for<0, CF::FM>([&](auto i_c) {
       constexpr int i = decltype(i_c)::value;
       int id = row_adapter(p, mw + i * 16 + r);
-      if (id >= 0) {
-        const v4i f = *(const v4i*)(p.finite + (int64_t)id * kFiniteParts);
-        if (f.x & f.y & f.z & f.w) id = -1;
-      }
+      if (id >= 0 && p.finite[id] == kFinite) id = -1;
       uint32_t todo = (uint32_t)__ballot(id >= 0) & 0xffffu;  // rows whose adapter is still to come
       while (todo) {
         const int g = __builtin_amdgcn_readlane(id, __ffs(todo) - 1);
@@ -198,7 +220,7 @@ struct AdapterDownParams {
   const float* scale;  // adapters
   const int32_t* ids;
   void* U;
-  int32_t* finite;
+  uint8_t* finite;     // kFiniteParts each
   int32_t* order;      // workspace, with adapter_sorted (else NULL): the rows by adapter,
   int32_t* offsets;    // where each adapter's begin,
   int32_t* counts;     // and the sort's

@@ -71,7 +71,7 @@ __device__ __forceinline__ void finite_block(const AdapterDownParams& p, int blo
       bad |= (v[k] & kExp) == kExp || (v[k] & (kExp << 16)) == kExp << 16;
   }
   bad = any_thread(bad, red);
-  if (threadIdx.x == 0) p.finite[g * kFiniteParts + part] = !bad;
+  if (threadIdx.x == 0) p.finite[g * kFiniteParts + part] = bad ? 0 : 1;
 }
 
 // Products 4 x .. 4 x + 3 of a row, one wave each.

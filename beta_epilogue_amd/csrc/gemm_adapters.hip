@@ -71,7 +71,7 @@ extern "C" int gemm_epi_adapter_linear_create_variant(const gemm_epi_adapter_lin
   h->sorted = adapter_sorted(d.M, desc->rank, desc->adapters);
   const int64_t chunks = sort_chunks(d.M);
   h->at_finite = up256(d.M * desc->rank * 2);
-  h->at_order = h->at_finite + (h->bm ? up256((int64_t)desc->adapters * kFiniteParts * 4) : 0);
+  h->at_order = h->at_finite + (h->bm ? up256((int64_t)desc->adapters * kFiniteParts) : 0);
   h->at_offsets = h->at_order + (h->sorted ? up256(d.M * 4) : 0);
   h->at_counts = h->at_offsets + (h->sorted ? up256(((int64_t)desc->adapters + 1) * 4) : 0);
   h->own_bytes = h->at_counts + (h->sorted && chunks > 1 ? up256(chunks * desc->adapters * 4) : 0);
@@ -108,7 +108,7 @@ extern "C" int gemm_epi_adapter_linear_run(const gemm_epi_adapter_linear_handle*
   p.U = ws;
   p.up = up;
   p.ids = ids;
-  p.finite = (const int32_t*)(ws + h->at_finite);
+  p.finite = (const uint32_t*)(ws + h->at_finite);
   p.rank = h->rank;
   p.adapters = h->adapters;
   AdapterDownParams q = {};
@@ -118,7 +118,7 @@ extern "C" int gemm_epi_adapter_linear_run(const gemm_epi_adapter_linear_handle*
   q.scale = scale;
   q.ids = ids;
   q.U = ws;
-  q.finite = h->bm ? (int32_t*)(ws + h->at_finite) : nullptr;
+  q.finite = h->bm ? (uint8_t*)(ws + h->at_finite) : nullptr;
   q.order = h->sorted ? (int32_t*)(ws + h->at_order) : nullptr;
   q.offsets = h->sorted ? (int32_t*)(ws + h->at_offsets) : nullptr;
   q.counts = h->sorted ? (int32_t*)(ws + h->at_counts) : nullptr;

@@ -1275,10 +1275,13 @@ __device__ __forceinline__ void gemm_epi_body(const typename CF::params_t& p, ch
     // and B are on their way.
     if constexpr (CF::ADAPTERS) {
       constexpr int PRO = S == 2 ? 2 : S - 1;
+      adapters.fetch(p, lds, m0, split <= 0, wave, lane);
 #pragma unroll
       for (int k = 0; k < PRO; ++k)
         if (k < KTA) issue_tile(k);
-      adapters.setup(p, lds, m0, n0, split <= 0, opa.cb, lane);
+      if (KTA >= PRO) wait_vmcnt<PRO * NQ_STAGE>();
+      else wait_vmcnt<0>();
+      adapters.setup(p, lds, n0, split <= 0, opa.cb);
       KT += adapters.tiles;
 #pragma unroll
       for (int k = 1; k < PRO; ++k)
