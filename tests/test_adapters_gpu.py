@@ -78,7 +78,8 @@ def run(M, N, K, rank, G, ab="bf16", act="none", bias=None, res=False, z=False, 
     plan = op.plan
     _say("case", M, N, K, "rank", rank, "of", G, ab, act, kind, "pad", pad, plan["name"], "splits", plan["splits"])
     ws = torch.full((plan["workspace_bytes"],), 0xff, dtype=torch.uint8, device="cuda")  # NaN wherever it is not written
-    op(_strided(A, pad), _strided(B, pad), ids.cuda(), down.cuda(), up.cuda(), scale.cuda(), D=D.t,
+    there = torch.cat([torch.zeros(1, dtype=torch.int32), ids]).cuda()[1:]  # (not 16-byte aligned)
+    op(_strided(A, pad), _strided(B, pad), there, down.cuda(), up.cuda(), scale.cuda(), D=D.t,
        bias=b.cuda() if bias else None, residual=Rd, Z=Z.t if z else None, workspace=ws)
     torch.cuda.synchronize()
     assert D.intact() and (Z is None or Z.intact()), "a guard was overwritten"
@@ -132,6 +133,12 @@ def test_up_to_two_adapters(rank, G, kind):
     """Their rows are not sorted."""
     run(701, 264, 520, rank, G, kind=kind, seed=rank)
     run(1040, 72, 2056, rank, G, "f16", kind=kind, seed=rank + 1)
+
+
+@pytest.mark.parametrize("M,rank,G", [(1500, 8, 1024), (300, 16, 1000), (70, 128, 600), (2200, 64, 257), (8200, 8, 300)])
+@pytest.mark.parametrize("name", TILES)
+def test_many_adapters(M, rank, G, name):
+    run(M, 72, 72, rank, G, name.split("_")[1], kind="mixed", seed=G, variant=ge.linear_variant_names().index(name))
 
 
 @pytest.mark.parametrize("M,N,K", [(65, 8, 8), (65, 264, 16), (257, 520, 1032), (1001, 256, 40), (300, 2552, 24),
