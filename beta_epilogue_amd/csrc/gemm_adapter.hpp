@@ -46,7 +46,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t adapter_up(const AdapterParams
 // adapters that the tile's rows have add K tiles to the tile's, staged and
 // multiplied by the same loop: A's rows are U's, zero for rows of other adapters,
 // B's are up[g]'s.  A K tile of 64 holds as many adapters as fit (rank 16: four).
-// Packed prompts have one or two adapters per tile (4001 x 4096 x 4096, rank 64: 112 us,
+// Packed prompts have one or two adapters per tile (4001 x 4096 x 4096, rank 64: 110 us,
 // a plain projection 95 to 101); a batch of single tokens has up to one per row
 // (256 rows of 48 adapters, rank 16: 34 us with both launches).
 //

@@ -7,9 +7,9 @@
 //
 // More rows are sorted by adapter (gemm_experts_kernels.hip), so that a workgroup
 // has 16 rows of one, streamed past the adapter's weights by the few-row kernel
-// (gemm_linear_rows.hip): 4001 x 4096, rank 64, 12 us (18 with eight waves, whose LDS
-// leaves room for one workgroup only, so that the ones below came in a round of their
-// own; 24 with fragments straight from memory).  What bounds it is each adapter's
+// (gemm_linear_rows.hip): 4001 x 4096, rank 64, 16 us (17 to 19 with eight waves,
+// whose LDS leaves room for one workgroup only, so that the ones below came in a round
+// of their own; 24 with fragments straight from memory).  What bounds it is each adapter's
 // weights, once from the cache for every 16 rows.  With up to two adapters the rows stay
 // as they are, and a workgroup takes one after the other: a launch less.  (With four,
 // all mixed, 1000 x 1024, rank 32, that is 14.4 us against 3.1 and 6.3.)

@@ -1,7 +1,7 @@
 // gemm_adapter_part.hip -- compiles the linear layer's tile kernels with
 // adapters (gemm_adapter.hpp); GEMM_ADAPTER_PART 0 .. 3: one shape of tile each.
-// 4001 x 4096 x 4096 bf16, rank 64, 5 adapters: 112 us, with the sort (6) and the inner
-// products (15) before it 132 (the projection by itself 95 to 101).
+// 4001 x 4096 x 4096 bf16, rank 64, 7 adapters: 110 us, with the sort (6) and the inner
+// products (16) before it 130 (the projection by itself 95 to 101).
 #include "gemm_adapter.hpp"
 
 #ifndef GEMM_ADAPTER_PART
