@@ -254,6 +254,45 @@ def test_behind_the_norm():
         assert same(eager) and all(map(same, outs[:2]))
 
 
+@pytest.mark.parametrize("M,G", [(2100, 5), (9000, 70), (2100, 2)])
+def test_sorted_rows_on_streams_and_in_graphs(M, G):
+    """Many rows, whose inner products take a sort (but for two adapters): two
+    streams, and two graphs replayed in turn with eager calls between."""
+    g = torch.Generator().manual_seed(M)
+    N, K, rank = 72, 136, 16
+    b = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+    A, B, down, up = b(M, K), b(N, K), b(G, rank, K), b(G, N, rank)
+    scale, ids = torch.rand(G, generator=g).cuda(), some_ids(g, M, G, "mixed").cuda()
+    op = ge.AdapterLinear(M, N, K, rank, G)
+    _say("case sorted rows, streams and graphs", M, G, op.plan["name"])
+    new = lambda: torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    call = lambda d, stream=None: op(A, B, ids, down, up, scale, D=d, stream=stream)  # noqa: E731
+    want = call(new())
+    d, _, bd, _ = plain(A.cpu(), B.cpu(), ids.cpu(), down.cpu(), up.cpu(), scale.cpu(), "none", None, None, torch.bfloat16)
+    ref.check("D", want, d, bd)
+    outs = [new() for _ in range(6)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for i, o in enumerate(outs):
+        call(o, streams[i % 2])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    graphs = []
+    for o in outs[:2]:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            call(o)
+        graphs.append(gr)
+    for _ in range(3):
+        for o in outs[:2]:
+            o.zero_()
+        for gr in graphs:
+            gr.replay()
+        eager = call(new())
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, want) for o in (eager, *outs[:2]))
+
+
 def test_refusals():
     M, N, K, rank, G = 16, 64, 128, 16, 2
     b = dict(dtype=torch.bfloat16, device="cuda")
