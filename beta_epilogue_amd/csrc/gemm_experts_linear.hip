@@ -320,6 +320,13 @@ extern "C" const char* gemm_epi_expert_linear_variant_name(int variant) {
 namespace {
 
 constexpr int kGradKTile = 64;
+// dbias straight from dD's rows (no activation and mul): a workgroup adds up 64 columns
+// of an expert's rows, 2 us for 1024 of them.  The rows may all be one expert's.  With dB
+// its tiles take longer over the same rows; without, of more than kSumRows, workgroups add
+// up kSumChunk each and a second launch (4 us) joins them.  65536 rows of 8 experts,
+// 512 x 512, dA and dbias: even 59 us, 40960 of one expert 73; each expert's at once 64 and
+// 138.  16384 rows: 17 and 29, in chunks 18.5 and 22.
+constexpr int64_t kSumRows = 16384, kSumChunk = 1024;
 
 // Modelled time (us) of the products with the rows spread evenly, with the linear
 // backward's figures: an item takes 1.1 us per K tile with 256x256 tiles, 0.45 (a
@@ -354,11 +361,8 @@ struct gemm_epi_expert_linear_grad_handle {
   int64_t chunk, slots;   // rows of a chunk of the elementwise pass, and chunks at most
   int64_t ga, gb, sums;   // workgroups of the products and of the column sums
   int64_t ws_bytes;
-  // without an activation and mul dbias adds up dD's rows beside the products, in
-  // workgroups of 64 columns and all rows of an expert: where those are not too many
-  // (8192 of each expert, 8 experts, 512 x 512: 104 against 121 us with a pass of its
-  // own; 16384, 2 experts, 256 x 512: 85 against 77)
-  bool sum_rows;
+  bool sum_rows;  // dbias from dD's rows, beside the products
+  bool sum_chunks() const { return sum_rows && d.rows > kSumRows && d.db_dtype == GEMM_EPI_NONE; }
   bool pass() const { return has_z() || (d.dbias_dtype != GEMM_EPI_NONE && !sum_rows); }
   bool has_z() const { return d.act != GEMM_EPI_ACT_NONE || d.mul; }
 };
@@ -413,9 +417,11 @@ extern "C" int gemm_epi_expert_linear_grad_create(const gemm_epi_expert_linear_g
   const int64_t tn = (d.N + h.tile - 1) / h.tile, tk = (d.K + h.tile - 1) / h.tile;
   h.ga = d.da_dtype != GEMM_EPI_NONE ? worst_chunks(d.rows, d.experts, h.tile) * tk : 0;
   h.gb = d.db_dtype != GEMM_EPI_NONE ? 8 * d.experts * ((tn * tk + 7) / 8) : 0;
-  h.sum_rows = !h.has_z() && h.ga + h.gb > 0 && d.rows / d.experts <= 8192;
+  const bool dbias = d.dbias_dtype != GEMM_EPI_NONE;
+  h.sum_rows = dbias && !h.has_z() && h.ga + h.gb > 0;
   const int64_t columns = h.sum_rows ? 64 : 256;
-  h.sums = d.dbias_dtype != GEMM_EPI_NONE ? d.experts * ((d.N + columns - 1) / columns) : 0;
+  const int64_t parts = h.sum_chunks() ? worst_chunks(d.rows, d.experts, kSumChunk) : d.experts;
+  h.sums = dbias ? parts * ((d.N + columns - 1) / columns) : 0;
   // 256 threads for each, fewer than 2^32 in all
   if (h.ga + h.gb + h.sums >= int64_t(1) << 24) return fail(GEMM_EPI_ERR_UNSUPPORTED, "2^24 or more work items");
   // rows per workgroup of the elementwise pass: 64, fewer as long as there are under
@@ -423,8 +429,9 @@ extern "C" int gemm_epi_expert_linear_grad_create(const gemm_epi_expert_linear_g
   h.chunk = 64;
   while (h.chunk > 8 && (d.N + 255) / 256 * worst_chunks(d.rows, d.experts, h.chunk) < 4 * cus) h.chunk /= 2;
   while (worst_chunks(d.rows, d.experts, h.chunk) > 65535) h.chunk *= 2;
+  if (h.sum_chunks()) h.chunk = kSumChunk;
   h.slots = worst_chunks(d.rows, d.experts, h.chunk);
-  h.ws_bytes = d.dbias_dtype != GEMM_EPI_NONE && !h.sum_rows ? up256(h.slots * d.N * 4) : 0;
+  h.ws_bytes = dbias && (!h.sum_rows || h.sum_chunks()) ? up256(h.slots * d.N * 4) : 0;
   *out = new (std::nothrow) gemm_epi_expert_linear_grad_handle(h);
   return *out ? GEMM_EPI_OK : fail(GEMM_EPI_ERR_HOST_ALLOC, "out of host memory");
 }
@@ -521,13 +528,15 @@ extern "C" int gemm_epi_expert_linear_grad_run(const gemm_epi_expert_linear_grad
   p.b.d_dtype = d.db_dtype;
   p.b.tiles_m = (int32_t)((d.N + h->tile - 1) / h->tile);
   p.b.tiles_total = d.experts * p.b.tiles_m * p.b.tiles_n;
-  // the last items should be short ones: dA's are N long, dB's (the longest first)
-  // the experts' rows
+  // the last items should be short ones: dA's are N long, dB's (the longest first) and
+  // the column sums the experts' rows.  (Sums behind dA: 65536 rows of 8 experts, 40960
+  // of one, 256 x 512, both products: 188 us for 155.)
   p.b_first = d.rows > d.experts * d.N;
   p.ga = (int32_t)h->ga;
   p.gb = (int32_t)h->gb;
   p.sums = (int32_t)h->sums;
-  p.sum_rows = dbias && h->sum_rows ? dD : nullptr;
+  p.sum_rows = h->sum_rows ? dD : nullptr;
+  p.row_sums = h->sum_chunks() ? (float*)workspace : nullptr;
   p.partial = (const float*)workspace;
   p.chunk = (int32_t)h->chunk;
   p.dbias = dbias;
@@ -539,7 +548,14 @@ extern "C" int gemm_epi_expert_linear_grad_run(const gemm_epi_expert_linear_grad
        launch_grouped_grad<T_F16, 3>},
       {launch_grouped_grad<T_BF16, 0>, launch_grouped_grad<T_BF16, 1>, launch_grouped_grad<T_BF16, 2>,
        launch_grouped_grad<T_BF16, 3>}};
-  kLaunch[d.ab_dtype == GEMM_EPI_BF16][kind](p, s);
+  const auto launch = kLaunch[d.ab_dtype == GEMM_EPI_BF16][kind];
+  launch(p, s);
+  rc = launched();
+  if (rc || !h->sum_chunks()) return rc;
+  p.ga = p.gb = 0;
+  p.sums = (int32_t)(d.experts * ((d.N + 255) / 256));
+  p.sum_rows = nullptr;
+  launch(p, s);
   return launched();
 }
 

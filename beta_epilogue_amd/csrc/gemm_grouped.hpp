@@ -167,7 +167,7 @@ void launch_grouped_rows(int ab, int mb, const GroupParams& p, int slots, hipStr
 // The backward's products, one launch for both (GRAD_* as for the linear layer):
 //   a: dA = dZ . B[e] over groups of rows; ga workgroups, a tile each at most
 //   b: dB[e] = dB_in[e] + dZ^T . A over each group's rows; gb workgroups
-// b's come first with b_first; the rest add up the chunks' column sums: dbias.
+// sums workgroups make dbias.  In the order a, b, sums, or with b_first b, sums, a.
 template <int AB, bool ROWS, int KIND>
 using GroupedGradCfg = Cfg<AB, ROWS, false, true, grad_tile(KIND), grad_tile(KIND), 128, 2, 2, grad_stages(KIND),
                            KIND == GRAD_256 ? 2 : 0, 32, ROWS ? 4 : 5, grad_occ(KIND)>;
@@ -176,7 +176,8 @@ struct GroupGradParams {
   int32_t ga, gb, sums;   // workgroups
   int32_t b_first;
   const void* sum_rows;   // dD, whose rows dbias adds up; NULL: the chunks' sums
-  const float* partial;   // [chunk][N]
+  float* row_sums;        // ... chunk by chunk, into this one's [chunk][N]; NULL: an expert's at once
+  const float* partial;   // the chunks' sums, [chunk][N]
   int32_t chunk;          // rows of a chunk
   void* dbias;            // groups x N
   int32_t dbias_dtype;

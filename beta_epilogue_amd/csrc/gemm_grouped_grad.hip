@@ -18,14 +18,15 @@ namespace gemm_epi {
 
 namespace {
 
-// 64 columns of group g's dbias, straight from its rows of dD: 8 lanes of 8 columns
-// by 32 strands of rows, joined in a fixed order.  red: 32 x 68 words.
+// 64 columns of a group's dbias, or of a chunk's sums, straight from the rows of dD: 8
+// lanes of 8 columns by 32 strands of rows, joined in a fixed order.  red: 32 x 68 words.
 template <int AB>
 __device__ __forceinline__ void group_row_sums(const GroupGradParams& p, int block, float* red) {
-  const int per = (int)((p.N + 63) / 64), g = block / per;
-  const GroupTile t = group_rows(p.a, g);
+  const int per = (int)((p.N + 63) / 64), slot = block / per;
+  const GroupTile t = p.row_sums ? group_chunk(p.a, slot, p.chunk) : group_rows(p.a, slot);
+  if (t.group < 0) return;
   const int cl = threadIdx.x & 7, pl = threadIdx.x >> 3;
-  const int64_t c0 = (int64_t)(block - g * per) * 64, c = c0 + cl * 8;
+  const int64_t c0 = (int64_t)(block - slot * per) * 64, c = c0 + cl * 8;
   float s[8] = {};
   if (c < p.N) {
 #pragma unroll 8
@@ -44,7 +45,8 @@ __device__ __forceinline__ void group_row_sums(const GroupGradParams& p, int blo
   float v = 0.0f;
 #pragma unroll
   for (int k = 0; k < 32; ++k) v += red[k * 68 + threadIdx.x];
-  store_as(p.dbias, g * p.N + n, p.dbias_dtype, v);
+  if (p.row_sums) p.row_sums[slot * p.N + n] = v;
+  else store_as(p.dbias, slot * p.N + n, p.dbias_dtype, v);
 }
 
 // 256 columns of group g's dbias.
@@ -84,19 +86,19 @@ __global__ __launch_bounds__(256, grad_occ(KIND)) void grouped_grad_kernel(Group
   using CB = GroupedGradCfg<AB, false, KIND>;
   constexpr int A_BYTES = CA::LDS_BYTES + kGroupTableBytes;
   __shared__ __attribute__((aligned(1024))) char lds[A_BYTES > CB::LDS_BYTES ? A_BYTES : CB::LDS_BYTES];
-  const int bid = blockIdx.x, a0 = p.b_first ? p.gb : 0, b0 = p.b_first ? 0 : p.ga;
+  const int bid = blockIdx.x, a0 = p.b_first ? p.gb + p.sums : 0, b0 = p.b_first ? 0 : p.ga;
   if (bid >= a0 && bid < a0 + p.ga) {
     int* first = (int*)(lds + CA::LDS_BYTES);
     const int total = group_table_rows(p.a, first, CA::BM) * p.a.tiles_n;
     gemm_epi_body<CA>(p.a, lds, bid - a0, p.ga, GroupWork{first, 0, total, 0});
-  } else if (bid < p.gb + p.ga) {
+  } else if (bid >= b0 && bid < b0 + p.gb) {
     const GroupWork w = group_k_item(p.b, bid - b0);
     if (w.begin >= p.b.tiles_total || fill_without_rows(p.b, w)) return;
     gemm_epi_body<CB>(p.b, lds, bid - b0, p.gb, w);
-  } else if (p.sum_rows) {
-    group_row_sums<AB>(p, bid - p.gb - p.ga, (float*)lds);
   } else {
-    group_sums(p, bid - p.gb - p.ga, (int*)lds);
+    const int block = bid - p.gb - (p.b_first ? 0 : p.ga);
+    if (p.sum_rows) group_row_sums<AB>(p, block, (float*)lds);
+    else group_sums(p, block, (int*)lds);
   }
 }
 

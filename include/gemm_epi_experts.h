@@ -178,7 +178,8 @@ typedef struct gemm_epi_expert_linear_grad_handle gemm_epi_expert_linear_grad_ha
 
 /*
  * Validate and plan a backward (of a forward without scales): an elementwise
- * pass, then one launch for both products and dbias.  dZ is rounded to ab_dtype,
+ * pass, then one launch for both products and dbias (and one that joins dbias of
+ * many rows where there is no pass and no dB).  dZ is rounded to ab_dtype,
  * the type the matrix cores read; dbias is summed before that rounding, in a
  * fixed order.  UNSUPPORTED as well: an expert's B, or with dB the whole of A or dZ,
  * of 2 GiB or more; 2^24 or more work items.

@@ -287,6 +287,52 @@ def test_grad_more_tiles_than_fit():
     run_grad(2500, 6, 1032, 520, "bf16", "relu", da="bf16", db="bf16", tile=128)
 
 
+@pytest.mark.parametrize("kind", ["uneven", "one", "none", "less"])
+@pytest.mark.parametrize("da,db", [("bf16", None), (None, "f32"), ("bf16", "f32")])
+def test_grad_bias_of_many_rows(da, db, kind):
+    """Without an activation and dB, of more rows than one workgroup adds up in the time
+    of a product: any of them may be one expert's, so chunks of them are added up apart
+    and joined from the workspace."""
+    R, E, N, K = 17000, 5, 328, 72
+    run_grad(R, E, N, K, da=da, db=db, dbias="f32", kind=kind)
+    need = lambda R, **kw: ge.ExpertLinearGrad(R, E, N, K, da=da, db=db, **kw).workspace_bytes  # noqa: E731
+    assert need(R, dbias="f32") >= (0 if db else R // 1024 * N * 4)
+    assert need(16384, dbias="f32") == 0 and need(R) == 0
+
+
+def test_grad_bias_of_many_rows_in_graphs():
+    """Two graphs replayed in turn with eager calls between, bit for bit as alone."""
+    R, E, N, K = 17000, 5, 72, 72
+    g, T = torch.Generator().manual_seed(3), torch.bfloat16
+    dD, B = _draw(g, R, N, T).cuda(), _draw(g, E * N, K, T).view(E, N, K).cuda()
+    off = torch.tensor(sizes(g, R, E, "uneven"), dtype=torch.int32, device="cuda")
+    op = ge.ExpertLinearGrad(R, E, N, K, da="bf16", dbias="f32")
+    new = lambda: (torch.zeros(R, K, dtype=T, device="cuda"), torch.zeros(E, N, device="cuda"))  # noqa: E731
+    call = lambda o: op(dD, None, B, off, dA=o[0], dbias=o[1])  # noqa: E731
+    _say("case bias in graphs", R, E, N, K)
+    want, outs, graphs = new(), [new(), new()], [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    call(want)
+    torch.cuda.synchronize()
+    for gr, o in zip(graphs, outs):
+        with torch.cuda.graph(gr):
+            call(o)
+    for _ in range(3):
+        eager = new()
+        for o in outs:
+            o[0].zero_(), o[1].zero_()
+        for gr in graphs:
+            gr.replay()
+        call(eager)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for o in outs + [eager] for a, b in zip(o, want))
+
+
+def test_grad_bias_of_many_rows_and_experts():
+    run_grad(16385, 1024, 72, 16, "f16", da="f16", dbias="f16")
+    run_grad(30000, 2, 1032, 8, "bf16", da="bf16", dbias="bf16", tile=128)
+    run_grad(30000, 70, 8, 8, "bf16", db="f32", dbias="f32", tile=256, kind="less")
+
+
 def test_grad_parts():
     run_grad(100, 3, 64, 48, "bf16", "gelu", dbias="f16")
     run_grad(100, 3, 64, 48, "bf16", "gelu", da="f32")
@@ -312,6 +358,19 @@ def test_grad_of_offsets_outside_the_batch(tile, act):
         op(dD, A, B, torch.tensor(off, dtype=torch.int32, device="cuda"), dA=dA.t, dB=dB.t.view(E, N, K), dbias=dbias.t, **z)
         torch.cuda.synchronize()
         assert dA.intact() and dB.intact() and dbias.intact() and dZ.intact()
+
+
+def test_grad_bias_of_offsets_outside_many_rows():
+    R, E, N, K = 17000, 4, 64, 72
+    T = torch.bfloat16
+    dD, B = torch.ones(R, N, dtype=T, device="cuda"), torch.ones(E, N, K, dtype=T, device="cuda")
+    for off in ([-5, 10, 20, 30000, 40000], [0, 30, 10, 1 << 30, -(1 << 31)], [7] + [(1 << 31) - 1, 0] * 2):
+        dA, dbias = Out(R, K, T), Out(E, N, T)
+        _say("case bias of offsets", off)
+        op = ge.ExpertLinearGrad(R, E, N, K, da="bf16", dbias="bf16")
+        op(dD, None, B, torch.tensor(off, dtype=torch.int32, device="cuda"), dA=dA.t, dbias=dbias.t)
+        torch.cuda.synchronize()
+        assert dA.intact() and dbias.intact()
 
 
 @pytest.mark.parametrize("alias", ["dD", "Z"])
