@@ -51,7 +51,8 @@ extern "C" int gemm_epi_adapter_linear_create_variant(const gemm_epi_adapter_lin
   if (d.N > INT32_MAX / 2 / desc->rank / desc->adapters || d.K > INT32_MAX / 2 / desc->rank)
     return fail(GEMM_EPI_ERR_UNSUPPORTED, "up, or one adapter's down, of 2 GiB or more");
   gemm_epi_linear_handle* linear = nullptr;
-  int rc = gemm_epi_linear_create_variant(&d, variant, &linear);
+  const LinearAdapters adapters = {desc->rank, desc->adapters};
+  int rc = linear_create(&d, variant, &adapters, &linear);
   if (rc) return rc;
   if (linear->d.M * linear->d.lda > INT32_MAX / 2) {
     gemm_epi_linear_destroy(linear);

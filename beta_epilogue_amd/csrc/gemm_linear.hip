@@ -69,13 +69,20 @@ double rows_time(const gemm_epi_linear_desc& d, int64_t cus) {
   return std::max(4.5 + (double)runs * latency, 3.0 + (double)runs * per_cu * busy);
 }
 
-double linear_time(const LinearVariant& v, const LinearCut& c, const gemm_epi_linear_desc& d, int64_t cus) {
+// adapters: NULL for the plain layer.
+double linear_time(const LinearVariant& v, const LinearCut& c, const gemm_epi_linear_desc& d,
+                   const LinearAdapters* adapters, int64_t cus) {
   const LinearCost& w = linear_cost(v.ab);
   const double epi = linear_epilogue_time(w, v.bm, v.bn);
-  auto rounds = [&](int64_t items, int64_t k) {
-    return linear_rounds(w, v.bm, v.bn, v.occ, items, (k + v.bk - 1) / v.bk, cus);
+  const double more = adapters ? adapters->k_tiles(d.M, v.bm) : 0.0;
+  auto rounds = [&](int64_t items, int64_t k, double tiles) {
+    return linear_rounds(w, v.bm, v.bn, v.occ, items, (double)((k + v.bk - 1) / v.bk) + tiles, cus);
   };
-  const double products = rounds(c.tiles - c.tail, d.K) + rounds(c.tail * c.splits, std::min(c.kslice, d.K));
+  double products = rounds(c.tiles - c.tail, d.K, more) + rounds(c.tail * c.splits, std::min(c.kslice, d.K), 0.0);
+  if (c.tail) {  // its first slices have them, all in one round
+    const int64_t first = std::min<int64_t>(c.tail * c.splits, cus * v.occ);
+    products += rounds(first, 0, more) - rounds(first, 0, 0.0);
+  }
   // A and B once from memory, at the 4.5 TB/s that tiles of few rows reach (24
   // bf16 rows, N = K = 8192: 39 us, 20 by the items alone)
   const double stream = (double)(d.M + d.N) * (double)(d.K * elem_bytes(d.ab_dtype)) / 4.5e6 + epi;
@@ -146,9 +153,8 @@ static int validate_linear(gemm_epi_linear_desc* d) {
   return GEMM_EPI_OK;
 }
 
-extern "C" int gemm_epi_linear_create_variant(const gemm_epi_linear_desc* desc, int variant,
-                                              gemm_epi_linear_handle** out) {
-  clear_error();
+int gemm_epi::linear_create(const gemm_epi_linear_desc* desc, int variant, const LinearAdapters* adapters,
+                            gemm_epi_linear_handle** out) {
   if (!out) return fail(GEMM_EPI_ERR_INVALID_ARG, "out is NULL");
   *out = nullptr;
   if (!desc) return fail(GEMM_EPI_ERR_INVALID_ARG, "desc is NULL");
@@ -176,7 +182,7 @@ extern "C" int gemm_epi_linear_create_variant(const gemm_epi_linear_desc* desc, 
       if (kLinear[i].ab != kernel_ab || (forced != -1 && i != forced)) continue;
       for (int64_t s = d.splits ? d.splits : 1; s <= (d.splits ? d.splits : 16); ++s) {
         const LinearCut c = cut_linear(kLinear[i], d, s, d.splits != 0, cus);
-        const double us = linear_time(kLinear[i], c, d, cus);
+        const double us = linear_time(kLinear[i], c, d, adapters, cus);
         if (best.tiles == 0 || us < best_us) best_us = us, best = c, variant = i;
       }
     }
@@ -223,6 +229,12 @@ extern "C" int gemm_epi_linear_create_variant(const gemm_epi_linear_desc* desc, 
   h->ws_bytes = h->splits > 1 ? h->splits * h->tail * v.bm * v.bn * 4 : 0;
   *out = h;
   return GEMM_EPI_OK;
+}
+
+extern "C" int gemm_epi_linear_create_variant(const gemm_epi_linear_desc* desc, int variant,
+                                              gemm_epi_linear_handle** out) {
+  clear_error();
+  return linear_create(desc, variant, nullptr, out);
 }
 
 extern "C" int gemm_epi_linear_create(const gemm_epi_linear_desc* desc, gemm_epi_linear_handle** out) {

@@ -34,15 +34,34 @@ inline double linear_epilogue_time(const LinearCost& w, int bm, int bn) {
   return w.e0 + w.e1 * ((double)bm * bn / 65536.0);
 }
 
+// The adapters of a projection's rows (gemm_adapter.hpp), and the K tiles of 64 that
+// they add to a tile of bm rows, or to the first K slice of one: for as many adapters
+// as the tile's rows meet where those of each adapter lie together, of which rows in
+// any other order meet more.  Over 84 shapes (24 to 4001 rows, 1 to 300 adapters of rank
+// 8 to 128, N 256 to 8192, K 256 to 8192) the plans with them take 0.4 % longer than the
+// best ones with packed rows and 0.8 % with mixed ones, 17 % at worst; without them 1.9
+// and 2.3 %, 40 % (64 rows of 48 adapters of rank 32, 512 x 4096: K slices for 30 us, the
+// few-row kernel takes 21; 512 rows of 300 of rank 8, 1024 x 8192: 52 and 40).
+struct LinearAdapters {
+  int rank, adapters;
+  double k_tiles(int64_t M, int bm) const {
+    const double rows = (double)(M < bm ? M : bm), met = 1.0 + rows * adapters / (double)M;
+    const double n = met < adapters ? met : adapters;
+    if (rank > 64) return 2.0 * n;
+    const double tiles = n / (rank <= 8 ? 8 : rank <= 16 ? 4 : rank <= 32 ? 2 : 1);
+    return tiles < 1.0 ? 1.0 : tiles;
+  }
+};
+
 // Rounds of `items` tiles of bm x bn over `ktiles` K tiles, occ workgroups to a
 // compute unit.
-inline double linear_rounds(const LinearCost& w, int bm, int bn, int occ, int64_t items, int64_t ktiles, int64_t cus) {
+inline double linear_rounds(const LinearCost& w, int bm, int bn, int occ, int64_t items, double ktiles, int64_t cus) {
   if (items == 0) return 0.0;
   double tk = bm == 256 ? w.tk256 : bm == 192 ? w.tk192 : bn == 256 ? w.tk128x256 : bm == 128 ? w.tk128 : w.tk64;
   int64_t slots = cus;
   if (occ >= 2 && items > cus) tk = bm == 128 ? w.pair128 : w.pair64, slots = 2 * cus;
   if (occ >= 3 && items > 2 * cus) tk = w.three64, slots = 3 * cus;
-  return (double)((items + slots - 1) / slots) * (tk * (double)ktiles + linear_epilogue_time(w, bm, bn));
+  return (double)((items + slots - 1) / slots) * (tk * ktiles + linear_epilogue_time(w, bm, bn));
 }
 
 }  // namespace gemm_epi

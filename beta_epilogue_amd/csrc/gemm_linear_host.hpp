@@ -4,6 +4,7 @@
 
 #include "gemm_epi_linear.h"
 #include "gemm_linear.hpp"
+#include "gemm_linear_cost.hpp"
 
 struct gemm_epi_linear_handle {
   gemm_epi_linear_desc d;  // strides filled in
@@ -15,6 +16,10 @@ struct gemm_epi_linear_handle {
 };
 
 namespace gemm_epi {
+
+// gemm_epi_linear_create_variant, for rows with adapters (NULL: none).
+int linear_create(const gemm_epi_linear_desc* desc, int variant, const LinearAdapters* adapters,
+                  gemm_epi_linear_handle** out);
 
 // What a run checks, and its kernels' arguments.
 int linear_params(const gemm_epi_linear_handle* h, const void* A, const void* B, const void* bias,

@@ -32,7 +32,8 @@ typedef struct gemm_epi_adapter_linear_desc {
 
 typedef struct gemm_epi_adapter_linear_handle gemm_epi_adapter_linear_handle;
 
-/* Validate and plan, with the projection's plan (errors as for
+/* Validate and plan: the projection's plan, chosen with the work that the adapters add
+ * where each adapter's rows lie together (errors as for
  * gemm_epi_linear_create; 2^26 or more rows, and A, up or one adapter's down of 2
  * GiB or more, are UNSUPPORTED). */
 int gemm_epi_adapter_linear_create(const gemm_epi_adapter_linear_desc* desc, gemm_epi_adapter_linear_handle** out);

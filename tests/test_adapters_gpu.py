@@ -162,6 +162,14 @@ def test_strides_and_in_place(M):
     run(M, 264, 512, 32, 4, res=True, z=True, pad=32)
 
 
+def test_the_plan_counts_the_adapters():
+    """The K tiles that a tile's adapters add fall on its first K slice, so many adapters
+    want fewer slices and smaller tiles than the projection alone, or few-row kernels."""
+    for M, N, K, rank, G in ((512, 1024, 8192, 8, 300), (64, 512, 4096, 32, 48)):
+        alone, many = ge.FusedLinear(M, N, K).plan, ge.AdapterLinear(M, N, K, rank, G).plan
+        assert many["splits"] < alone["splits"] and many["tile_m"] <= alone["tile_m"], (alone, many)
+
+
 def test_without_adapters_it_is_the_linear_layer():
     g = torch.Generator().manual_seed(2)
     for M in (16, 300):
