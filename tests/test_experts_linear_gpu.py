@@ -113,6 +113,38 @@ def test_every_kernel(variant):
             run(90, 33, 72, 80, ab, d, scaled=q, variant=variant, kind="less", act="silu")
 
 
+@pytest.mark.parametrize("rows,cols", [(True, False), (False, True), (True, True)])
+@pytest.mark.parametrize("variant", range(len(NAMES)), ids=NAMES)
+def test_scales(variant, rows, cols):
+    """Row scales and each expert's column scales, alone and together, in every kernel
+    and type, with uneven and empty experts (bounds as in ``run``)."""
+    name, R, E, N, K = NAMES[variant], 333, 6, 136, 208
+    for ab, d in (("bf16", "bf16"), ("f16", "f16"), ("e4m3", "f16"), ("e4m3", "f32"), ("i8", "bf16")):
+        wide = ab == "e4m3" and d == "f32"
+        if "rows" not in name and (name.split("_")[1] != ab or wide != ("f32" in name)):
+            continue
+        g = torch.Generator().manual_seed(variant)
+        off = [0, 0, 70, 201, 201, 330, 330]
+        unit = K ** -0.5 * (1 / 1600.0 if ab == "i8" else 1.0)
+        A, B = _draw(g, R, K, TORCH[ab]), _draw(g, E * N, K, TORCH[ab]).view(E, N, K)
+        sa = (torch.rand(R, generator=g) + 0.5) * unit if rows else None
+        sb = (torch.rand(E, N, generator=g) + 0.5) * (1.0 if rows else unit) if cols else None
+        op = ge.ExpertLinear(R, E, N, K, ab=ab, d=d, scale_a=rows, scale_b=cols, variant=variant)
+        D = Out(R, N, TORCH[d])
+        _say("case scales", name, ab, d, rows, cols)
+        op(A.cuda(), B.cuda(), torch.tensor(off, dtype=torch.int32, device="cuda"), D=D.t, scale_a=_cuda(sa), scale_b=_cuda(sb))
+        torch.cuda.synchronize()
+        assert D.intact() and (D.t[off[-1]:].float() == -80.0).all()
+        fp8 = ab == "e4m3" and not wide and "rows" not in name
+        acc = 1e-3 if fp8 else (2 * ref.U if ab == "i8" else K * ref.U)
+        for e in range(E):
+            at = slice(off[e], off[e + 1])
+            if off[e] < off[e + 1]:
+                dr, _, S = ref.linear(A[at], B[e], "none", None, sa[at] if rows else None, sb[e] if cols else None)
+                ed = (acc + 4 * ref.U) * S
+                ref.check("D of %d" % e, D.t[at], dr, ed + ref.half_step(dr.abs() + ed, TORCH[d]))
+
+
 @pytest.mark.parametrize("R,E", [(1, 1), (1, 64), (8, 64), (15, 4), (64, 3), (65, 65), (128, 1024), (500, 100), (3000, 7)])
 @pytest.mark.parametrize("ab,d", [("bf16", "bf16"), ("f16", "f32"), ("e4m3", "bf16"), ("e4m3", "f32"), ("i8", "f16")])
 def test_rows_and_experts(R, E, ab, d):
@@ -340,6 +372,51 @@ def test_grad_parts():
     run_grad(100, 3, 64, 48, "f16", "none", dbias="f32")
     run_grad(100, 3, 64, 48, "f16", "silu", mul=True)
     run_grad(100, 3, 64, 48, "f16", "none", mul=True, da="f16")
+
+
+@pytest.mark.parametrize("R", [333, 17000])
+@pytest.mark.parametrize("act,mul", [("none", False), ("silu", True)])
+@pytest.mark.parametrize("tile", [64, 128, 256])
+def test_grad_of_one_experts_nans(tile, act, mul, R):
+    """NaN and infinities in one expert's first and last rows reach its own gradients,
+    and change no bit of the other experts'."""
+    E, N, K, T = 4, 72, 136, torch.bfloat16
+    g = torch.Generator().manual_seed(R)
+    off = [0, 5, R // 2 + 3, R - 9, R]
+    mine = slice(off[1], off[2])
+    has_z = act != "none"
+    clean = dict(dD=_draw(g, R, N, T), A=_draw(g, R, K, T), Z=_draw(g, R, N, T), U=_draw(g, R, N, T))
+    B = _draw(g, E * N, K, T, K ** -0.5).view(E, N, K).cuda()
+    offsets = torch.tensor(off, dtype=torch.int32, device="cuda")
+    for wants in (dict(da="bf16", db="f32", dbias="f32"), dict(da="bf16", dbias="f32"), dict(db="f32", dbias="f32")):
+        op = ge.ExpertLinearGrad(R, E, N, K, act=act, mul=mul, tile=tile, **wants)
+        got = []
+        for dirty in (False, True):
+            t = {n: v.clone() for n, v in clean.items()}
+            if dirty:
+                for i, v in enumerate(t.values()):
+                    v[off[1], i::7], v[off[2] - 1, i::5] = NAN, float("inf")
+            t = {n: v.cuda() for n, v in t.items()}
+            e = lambda *s: torch.zeros(*s, dtype=T, device="cuda")  # noqa: E731
+            o = dict(dbias=torch.zeros(E, N, device="cuda"))
+            if "da" in wants:
+                o["dA"] = e(R, K)
+            if "db" in wants:
+                o["dB"] = torch.zeros(E, N, K, device="cuda")
+            if has_z:
+                o |= dict(dZ=e(R, N), dU=e(R, N))
+            _say("case NaN of one expert", R, act, tile, wants, dirty)
+            op(t["dD"], t["A"] if "db" in wants else None, B if "da" in wants else None, offsets,
+               Z=t["Z"] if has_z else None, U=t["U"] if has_z else None, **o)
+            torch.cuda.synchronize()
+            got.append({n: v.cpu() for n, v in o.items()})
+        for n, want in got[0].items():
+            v = got[1][n]
+            if n in ("dB", "dbias"):
+                assert torch.isnan(v[1]).any() and torch.equal(v[[0, 2, 3]], want[[0, 2, 3]]), n
+            else:
+                assert torch.isnan(v[mine]).any(), n
+                assert torch.equal(v[:off[1]], want[:off[1]]) and torch.equal(v[off[2]:], want[off[2]:]), n
 
 
 @pytest.mark.parametrize("act", ["none", "silu"])
