@@ -15,7 +15,9 @@
 // all mixed, 1000 x 1024, rank 32, that is 14.4 us against 3.1 and 6.3.)
 //
 // Further workgroups of the same launch look whether the up[g] that the rows meet
-// are finite (AdapterTiles).
+// are finite (AdapterTiles): a read of each beside the rows' (4001 x 4096 x 4096: 7 adapters
+// of rank 64 nothing, 300 of them, 157 MB, 15 of 219 us; 512 x 2048 x 2048, 200 of them, 6
+// of 50).
 #include "gemm_adapter.hpp"
 #include "gemm_linear_rows.hpp"
 

@@ -1006,8 +1006,9 @@ template <class CF>
 struct AdapterTiles;
 
 // What a workgroup does of a GROUP_K problem: item `begin`, of a group with rows.  Of a
-// GROUP_ROWS problem: items begin .. end - 1, of the table of groups `first` (in LDS).  quarter: an item is a quarter of a tile of
-// twice the height and width, which the table counts.
+// GROUP_ROWS problem: items begin .. end - 1, of the table of groups `first` (in LDS).
+// quarter: an item is a quarter of a tile of twice the height and width, which the table
+// counts.
 struct GroupWork {
   const int* first;
   int begin, end, quarter;

@@ -8,8 +8,8 @@
 // of more, every workgroup counts a chunk of 4096 and a second launch ranks it behind the
 // counts of the chunks before it (98760 choices of 128 experts: 5 and 7 us).  Those
 // sums read every chunk's counts in every workgroup, which grows with the square of
-// the chunks (10^6 choices 23 us, 10^7 366).  Moving the rows is bound by memory: a token's row is read once and
-// stored top_k times.
+// the chunks (10^6 choices of 128 experts 23 us, of 1024 29, 10^7 of 128 370 to 470).
+// Moving the rows is bound by memory: a token's row is read once and stored top_k times.
 #include "gemm_experts.hpp"
 #include "gemm_linear.hpp"
 

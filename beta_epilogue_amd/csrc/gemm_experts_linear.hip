@@ -173,7 +173,9 @@ extern "C" int gemm_epi_expert_linear_create_variant(const gemm_epi_expert_linea
   if (d.ab_dtype == GEMM_EPI_I8 && d.K >= int64_t(1) << 17)
     return fail(GEMM_EPI_ERR_UNSUPPORTED, "int8 with K of 2^17 or more: the int32 sums could overflow");
   if (variant < -1 || variant >= kVariants) return fail(GEMM_EPI_ERR_INVALID_ARG, "variant %d out of range", variant);
-  // (the fp8 MFMA sums a group of products with fewer bits than fp32 keeps)
+  // The fp8 MFMA sums a group of products with fewer bits than fp32 keeps (+-8192 among
+  // products near 1: 5.6e-4 of sum |a||b|), which 16-bit outputs allow for the sake
+  // of its rate: 98760 rows of 128 experts, 1536 x 4096, 637 us, widened to fp16 1105.
   const int kernel_ab = d.ab_dtype == GEMM_EPI_E4M3 && d.d_dtype == GEMM_EPI_F32 ? (int)T_E4M3_WIDE : d.ab_dtype;
   auto rows_fit = [&](int v) {  // a launch's second dimension, and less than 2^32 threads
     const int64_t chunks = worst_chunks(d.rows, d.experts, 4 * kRowsBlocks[v - kTiles]);

@@ -205,7 +205,8 @@ class ExpertLinear(_ExpertPlan):
     capacity, tokens * top_k.  ab: f16, bf16, e4m3 or i8; d (of D, U and Z):
     f16, bf16 or f32.  bias: its type, or None; mul, z, scale_a, scale_b:
     whether the call has U, Z and the scales.  Z receives the pre-activation,
-    which ``ExpertLinearGrad`` takes.  A gated layer is two calls: U = ExpertLinear
+    which ``ExpertLinearGrad`` takes.  e4m3 with a 16-bit d sums with fewer bits than fp32
+    in the tile kernels (off by up to 0.0006 of the sum of |a||b|).  A gated layer is two calls: U = ExpertLinear
     of one weight, then act and mul with the other.  variant forces a kernel.
     """
 
@@ -249,6 +250,9 @@ class ExpertLinearGrad(_ExpertPlan):
     dZ.  All tensors are packed; dD, Z, U, dZ, dU, A and B have type ab (f16 or
     bf16).  da, db, dbias: the gradients' types, None for one not wanted.
     Without an activation and mul dD takes dZ's place and Z and dZ are not given.
+    With db the whole of A and of dZ must be below 2 GiB each; a larger batch is several
+    calls, each on a range of rows with ``offsets`` less its first row and dB_in = the dB
+    before (dbias adds up).
     tile (64, 128 or 256) forces the products' tile.
     """
 

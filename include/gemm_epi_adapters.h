@@ -10,8 +10,10 @@
  * adapter need not lie together; they are fastest where they do (packed prompts).
  * An infinity or a NaN in one adapter's weights reaches that adapter's rows only.
  * The inner products scale[g] A[m] . down[g]^T are summed in fp32 and rounded once
- * to the operands' type, which the matrix cores read (fp16: one beyond 65504 is
- * infinite); everything else is as in gemm_epi_linear.h, whose conventions hold.  Adapters of a smaller rank are padded
+ * to the operands' type, which the matrix cores read.  (fp16: one beyond 65504 is
+ * infinite, also where its product with up would not be; one below 6.1e-5 is off by
+ * up to 3e-8, half of a subnormal step.)  Everything else is as in
+ * gemm_epi_linear.h, whose conventions hold.  Adapters of a smaller rank are padded
  * with zeros.
  */
 #ifndef GEMM_EPI_ADAPTERS_H

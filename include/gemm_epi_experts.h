@@ -24,7 +24,12 @@
  *     sort back     dX[t] = dX_in[t] + sum_j dY[rows[t][j]]: combine without weights
  *
  * Sums are fp32 (int8 products int32) in an order that does not depend on how
- * workgroups run; every output is rounded once, to nearest-even.
+ * workgroups run; every output is rounded once, to nearest-even.  One exception: e4m3
+ * with 16-bit outputs in the tile kernels.  The fp8 matrix instructions drop bits of a
+ * product far below the largest one of its group, which leaves a sum off by up to
+ * 0.0006 of the sum of |a||b| where large products cancel (0.001 is what tests allow).
+ * The few-row kernels, and fp32 outputs in any, widen e4m3 to fp16 (exactly) and keep
+ * fp32's precision.
  *
  * Conventions as in gemm_epi_linear.h: status codes and gemm_epi_last_error();
  * everything that needs no device is checked at create; rows and row strides
@@ -134,8 +139,10 @@ typedef struct gemm_epi_expert_linear_handle gemm_epi_expert_linear_handle;
 
 /* Validate and plan: a kernel for few rows per expert, which streams the weights
  * of the experts that have rows, or a tile kernel, by a cost model that takes the
- * rows as evenly spread (the result never depends on it).  Types and errors as for
- * gemm_epi_linear_create; an expert's bias must be a multiple of 16 bytes long. */
+ * rows as evenly spread: the desc alone decides, not where the rows went.  Kernels
+ * differ in the order of their sums (e4m3: and in their precision, see above).
+ * Types and errors as for gemm_epi_linear_create; an expert's bias must be a multiple
+ * of 16 bytes long. */
 int gemm_epi_expert_linear_create(const gemm_epi_expert_linear_desc* desc, gemm_epi_expert_linear_handle** out);
 
 /* The same with kernel `variant` (-1: the plan's choice); one that cannot run the
@@ -182,7 +189,9 @@ typedef struct gemm_epi_expert_linear_grad_handle gemm_epi_expert_linear_grad_ha
  * many rows where there is no pass and no dB).  dZ is rounded to ab_dtype,
  * the type the matrix cores read; dbias is summed before that rounding, in a
  * fixed order.  UNSUPPORTED as well: an expert's B, or with dB the whole of A or dZ,
- * of 2 GiB or more; 2^24 or more work items.
+ * of 2 GiB or more; 2^24 or more work items.  A larger batch is several runs, each on
+ * a range of rows with offsets less its first row (offsets outside a run's rows are
+ * moved to their ends) and dB_in the dB before.
  */
 int gemm_epi_expert_linear_grad_create(const gemm_epi_expert_linear_grad_desc* desc,
                                        gemm_epi_expert_linear_grad_handle** out);

@@ -204,6 +204,32 @@ def test_special_values():
         assert (D[rest] == 64 + 512).all()
 
 
+@pytest.mark.parametrize("M", [7, 150])
+def test_inner_products_of_fp16(M):
+    """Below fp16's normal range they are off by half of a subnormal step (2^-25), beyond its
+    largest value infinite, in their own rows only."""
+    N, K, rank, G, T = 72, 64, 16, 3, torch.float16
+    g = torch.Generator().manual_seed(M)
+    A, B = _draw(g, M, K, T), torch.zeros(N, K, dtype=T)
+    down, up = _draw(g, G * rank, K, T, K ** -0.5).view(G, rank, K), _draw(g, G * N, rank, T, 100.0).view(G, N, rank)
+    ids = (torch.arange(M) % G).to(torch.int32)
+    for scale in (1e-4, 1e-6, 2.0 ** -24):
+        D = torch.empty(M, N, dtype=T, device="cuda")
+        s = torch.full((G,), scale)
+        _say("case small inner products", M, scale)
+        op = ge.AdapterLinear(M, N, K, rank, G, ab="f16")
+        op(A.cuda(), B.cuda(), ids.cuda(), down.cuda(), up.cuda(), s.cuda(), D=D)
+        want, _, bound, _ = plain(A, B, ids, down, up, s, "none", None, None, T)
+        ref.check("D", D, want, bound)
+    s = torch.tensor([1.0, 1e6, 1.0])
+    up = (up / 1e4).to(T)
+    op(A.cuda(), B.cuda(), ids.cuda(), down.cuda(), up.cuda(), s.cuda(), D=D)
+    want, _, bound, _ = plain(A, B, ids, down, up, s, "none", None, None, T)
+    near = ids != 1
+    ref.check("D", D[near.cuda()], want[near], bound[near])
+    assert not torch.isfinite(D[1].float()).all()
+
+
 def test_behind_the_norm():
     """Norm, projection with adapters, and an expert layer's sort of its result,
     as a program would run them, on two streams and in two graphs."""

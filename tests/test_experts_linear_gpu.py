@@ -186,6 +186,30 @@ def test_the_plan_follows_the_rows():
     assert "256" in ge.ExpertLinear(32768, 8, 4096, 4096).plan["name"]
 
 
+@pytest.mark.parametrize("K", [128, 1040])
+def test_sums_of_e4m3(K):
+    """Large products that cancel among small ones: fp32's precision where e4m3 is widened
+    (the few-row kernels, fp32 outputs), 0.001 of the sum of |a||b| where the fp8 matrix
+    instructions sum."""
+    R, N, T8 = 200, 136, torch.float8_e4m3fn
+    g = torch.Generator().manual_seed(K)
+    A, B = torch.rand(R, K, generator=g) + 0.5, torch.ones(1, N, K)
+    for d in ("f16", "f32"):
+        for size in (64.0, 2048.0, 8192.0, 65536.0):
+            A[:, 3], A[:, K // 2 + 5], B[:, :, 3], B[:, :, K // 2 + 5] = size / 256, -size / 256, 256.0, 256.0
+            a, b = A.to(T8), B.to(T8)
+            for v, name in enumerate(NAMES):
+                if "rows" not in name and ("e4m3" not in name or (d == "f32") != ("f32" in name)):
+                    continue
+                D = torch.empty(R, N, dtype=TORCH[d], device="cuda")
+                _say("case cancel", name, d, size)
+                ge.ExpertLinear(R, 1, N, K, ab="e4m3", d=d, variant=v)(
+                    a.cuda(), b.cuda(), torch.tensor([0, R], dtype=torch.int32, device="cuda"), D=D)
+                dr, _, S = ref.linear(a, b[0])
+                e = (K * ref.U if "rows" in name or d == "f32" else 1e-3) * S
+                ref.check("D", D, dr, e + ref.half_step(dr.abs() + e, TORCH[d]))
+
+
 def test_special_values():
     """A NaN or an infinity of one row stays in it; infinite factors follow the
     formula (0 * infinity is NaN)."""
@@ -312,6 +336,42 @@ def test_grad_tiles(ab, tile, kind):
     with all."""
     run_grad(700, 4, 328, 456, ab, "gelu", da=ab, db="f32", dbias="f32", db_in=True, tile=tile, kind=kind)
     run_grad(150, 7, 72, 520, ab, "none", da="f32", db=ab, dbias="f16", tile=tile, kind=kind)
+
+
+@pytest.mark.parametrize("act,mul", [("none", False), ("gelu", True)])
+def test_grad_in_ranges_of_rows(act, mul):
+    """A batch in several calls, with offsets less each range's first row: rows of other
+    ranges are neither read nor written, and dB goes on from the range before."""
+    R, E, N, K, T = 700, 6, 264, 136, torch.bfloat16
+    g = torch.Generator().manual_seed(11)
+    off = [0, 0, 130, 395, 395, 640, 690]
+    dD, A, Z, U = (_draw(g, R, n, T).cuda() for n in (N, K, N, N))
+    B = _draw(g, E * N, K, T, K ** -0.5).view(E, N, K).cuda()
+    offsets = torch.tensor(off, dtype=torch.int32, device="cuda")
+    has_z = act != "none"
+    dA, dZ, dU = Out(R, K, T), Out(R, N, T), Out(R, N, T)
+    dB, dbias = torch.zeros(E, N, K, device="cuda"), torch.zeros(E, N, device="cuda")
+    for i, (lo, hi) in enumerate(((0, 200), (200, 400), (400, R))):
+        op = ge.ExpertLinearGrad(hi - lo, E, N, K, act=act, mul=mul, da="bf16", db="f32", dbias="f32")
+        part, more = torch.empty_like(dbias), {}
+        if has_z:
+            more = dict(Z=Z[lo:hi], U=U[lo:hi], dZ=dZ.t[lo:hi], dU=dU.t[lo:hi])
+        _say("case ranges", act, lo, hi)
+        op(dD[lo:hi], A[lo:hi], B, offsets - lo, dA=dA.t[lo:hi], dB=dB, dB_in=dB if i else None, dbias=part, **more)
+        dbias += part
+    torch.cuda.synchronize()
+    assert dA.intact() and dZ.intact() and dU.intact() and (dA.t[off[-1]:].float() == -80.0).all()
+    dz = ref.f64(dZ.t if has_z else dD)
+    for e in range(E):
+        at, m = slice(off[e], off[e + 1]), off[e + 1] - off[e]
+        s, a, b = dz[at], ref.f64(A)[at], ref.f64(B)[e]
+        want, S = s @ b, s.abs() @ b.abs()
+        ref.check("dA of %d" % e, dA.t[at], want, (N + 4) * ref.U * S + ref.half_step(want.abs() + N * ref.U * S, T))
+        want, S = s.T @ a, s.abs().T @ a.abs()
+        ref.check("dB of %d" % e, dB[e], want, (m + 8) * ref.U * S + ref.half_step(want.abs() + m * ref.U * S, torch.float32))
+        # (dbias adds up dZ before its rounding)
+        half = ref.half_step(s, T).sum(0) if has_z else 0.0
+        ref.check("dbias of %d" % e, dbias[e], s.sum(0), 1.01 * half + (m + 8) * ref.U * s.abs().sum(0) + 1e-30)
 
 
 def test_grad_more_tiles_than_fit():
