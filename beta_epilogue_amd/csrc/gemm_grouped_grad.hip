@@ -6,8 +6,10 @@
 // the most rows first and each expert's spread over the XCDs (16384 rows of 8
 // experts, 825 to 4282 each, N 4096, K 2048: dB 344 us with an expert per XCD).
 // Bound by the MFMAs and the transposing LDS reads: both products of those rows take
-// 462 us (1190 TFLOP/s).  dbias is made by further workgroups from the elementwise pass's column sums, in
-// the order of the chunks, or without such a pass from dD's rows.
+// 462 us (1190 TFLOP/s).  dbias is made by further workgroups from the elementwise pass's
+// column sums, in the order of the chunks, or without such a pass from dD's rows: all of
+// an expert's at once, or chunk by chunk, for a second launch of this kernel that has
+// nothing but the join to do.
 #include "gemm_grouped.hpp"
 
 #ifndef GEMM_GROUPED_GRAD_PART

@@ -206,7 +206,7 @@ class ExpertLinear(_ExpertPlan):
     f16, bf16 or f32.  bias: its type, or None; mul, z, scale_a, scale_b:
     whether the call has U, Z and the scales.  Z receives the pre-activation,
     which ``ExpertLinearGrad`` takes.  e4m3 with a 16-bit d sums with fewer bits than fp32
-    in the tile kernels (off by up to 0.0006 of the sum of |a||b|).  A gated layer is two calls: U = ExpertLinear
+    in the tile kernels (where large products cancel, off by 0.0006 of the sum of |a||b|).  A gated layer is two calls: U = ExpertLinear
     of one weight, then act and mul with the other.  variant forces a kernel.
     """
 

@@ -26,8 +26,8 @@
  * Sums are fp32 (int8 products int32) in an order that does not depend on how
  * workgroups run; every output is rounded once, to nearest-even.  One exception: e4m3
  * with 16-bit outputs in the tile kernels.  The fp8 matrix instructions drop bits of a
- * product far below the largest one of its group, which leaves a sum off by up to
- * 0.0006 of the sum of |a||b| where large products cancel (0.001 is what tests allow).
+ * product far below the largest one of its group: sums in which large products cancel
+ * have been off by 0.0006 of the sum of |a||b| (tests allow 0.001).
  * The few-row kernels, and fp32 outputs in any, widen e4m3 to fp16 (exactly) and keep
  * fp32's precision.
  *
